@@ -304,6 +304,173 @@ mac_status mac_attention_noalloc(int batch, int heads, int kv_heads, int head_di
                                  const void *dev_q, void *dev_out, float *dev_lse, float sm_scale,
                                  void *stream);
 
+/* ---- operators around the decode step ----------------------------------- */
+
+/* What a serving loop runs around a layer's decode attention: the QKV
+ * projection's norms and rotation, the page bookkeeping of a step, and a KV
+ * store of 4 bits per value with the attention over it.  None of them
+ * allocates, synchronises with the host or reads anything back; all may be
+ * captured into a CUDA graph, and every size that changes from step to step
+ * (lengths, positions, slots, pages) is read from device memory when the work
+ * runs.  Tensors they read and write must not overlap unless stated. */
+
+/* Per-head RMS norm, rotary embedding and split of a QKV projection. */
+typedef struct {
+    int heads, kv_heads;   /* heads % kv_heads == 0, heads <= 1024              */
+    int head_dim;          /* must be 128                                        */
+    int rotary_dim;        /* r: the first r elements of a head are rotated;     */
+                           /* a multiple of 8, 0..128                            */
+    int interleaved;       /* pairs (i, i + r/2) (0) or (2 i, 2 i + 1) (1)       */
+    float eps;             /* added to the mean of squares; >= 0                 */
+    double rope_base;      /* pair i turns by pos * rope_base^(-2 i / r); >= 1   */
+} mac_rope_config;
+
+/* Made once by mac_rope_init from a configuration and kept by the caller;
+ * plain host data, shared freely between calls, streams and devices. */
+typedef struct {
+    mac_rope_config cfg;
+    uint64_t turns[64];    /* whole turns per position, as a fraction of 2^64    */
+} mac_rope;
+
+mac_status mac_rope_init(const mac_rope_config *cfg, mac_rope *out);
+
+/* For n_tokens tokens (0: nothing is done): y = x / sqrt(mean(x^2) + eps) * w
+ * for every query and key head (y = x where w is NULL), then
+ *   q_pre = y, q_post = rotated y   (queries),  k_out = rotated y   (keys),
+ *   v_out = the values unchanged,
+ * computed in fp32 (angles in 64-bit fixed point, exact at any int32
+ * position) and rounded to bf16 once.  These are the q_pre, q_post, k_new and
+ * v_new of mac_decode_step.
+ *   dev_q, dev_k, dev_v  bf16, token t's heads at element t * stride (strides
+ *                        in elements, multiples of 8, at least the heads'
+ *                        size), so slices of one projection are read in
+ *                        place; dev_v and dev_v_out may both be NULL
+ *   dev_w_q, dev_w_k     bf16 [head_dim] norm weights, or NULL for no norm
+ *   dev_pos              int32 [n_tokens] 0-based positions
+ *   dev_q_pre, dev_q_post  bf16 [n_tokens][heads][head_dim]; q_pre may be NULL
+ *   dev_k_out, dev_v_out bf16 [n_tokens][kv_heads][head_dim]
+ * All bf16 pointers 16-byte aligned.  Async on stream. */
+mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, const void *dev_q, int64_t q_stride,
+                             const void *dev_k, int64_t k_stride, const void *dev_v, int64_t v_stride,
+                             const void *dev_w_q, const void *dev_w_k, const int32_t *dev_pos,
+                             void *dev_q_pre, void *dev_q_post, void *dev_k_out, void *dev_v_out,
+                             void *stream);
+
+/* One serving step's page bookkeeping for `batch` requests (1..1024) over a
+ * pool of num_pages 16-token pages (below 2^27): page-table entries for the
+ * new tokens, the positions and slots of the packed new tokens, the new
+ * lengths, and the pages of finished requests back on the free list.
+ *   dev_len_in   int32 [batch] tokens a request holds
+ *   dev_new      int32 [batch] its new tokens; a negative number: it is
+ *                finished, its pages are freed and its length becomes 0
+ *   dev_table    int32 [batch] rows of table_cols entries, table_stride apart;
+ *                the entries of new pages are written, all others are left
+ *   dev_ring     int32 [num_pages] ring of free page ids; entry
+ *                (head + i) % num_pages, i < count, is free; freed ids are
+ *                written behind the last
+ *   dev_state_in int32 [2] {head, count}
+ *   dev_len_out, dev_state_out   the new lengths and state (may be the same
+ *                memory as the inputs)
+ *   dev_starts   int32 [batch + 1]: request b's new tokens are the packed
+ *                tokens starts[b] .. starts[b + 1] - 1 (at most max_tokens)
+ *   dev_pos      int32 [max_tokens] 0-based position of each packed token
+ *   dev_slot     int32 [max_tokens] page * 16 + offset where it is stored, or
+ *                -1: it has none.  Past the last packed token: position 0,
+ *                slot -1
+ *   dev_status   int32 [1], written by every call: 0, or bits
+ *                1  the pool has too few pages: in request order, the first
+ *                   request that does not fit and every later one that needs
+ *                   a page is denied
+ *                2  a request would outgrow its table row: denied
+ *                4  a length or the state out of range, or a page id outside
+ *                   the pool met in the table or ring (its tokens get slot -1)
+ *                8  a request's tokens would end past max_tokens: denied
+ *                16 more pages freed than the ring has room for: none is freed
+ * A denied request keeps its length and gets no page; its packed tokens have
+ * slot -1.  max_tokens 1..2^30.  Async on stream. */
+mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
+                         int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
+                         int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out,
+                         int32_t *dev_starts, int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, void *stream);
+
+/* A paged KV store of 4 bits per value, one layer per handle.  16 consecutive
+ * elements x of a head share a scale s = e4m3(max|x| / 6) and are held as
+ * e2m1(x / s) (both to nearest even, saturating; a block with a NaN or an
+ * infinity reads back as NaN).  x is the bf16 element divided by k_scale or
+ * v_scale.  144 bytes per token and KV head for K and V, against 512 in bf16. */
+typedef struct mac_quant_ctx *mac_quant_handle;
+
+typedef struct {
+    int heads, kv_heads;   /* heads % kv_heads == 0, heads <= 4096               */
+    int head_dim;          /* must be 128                                        */
+    int page_size;         /* must be 16                                         */
+    int num_pages;         /* pages in the store, 1 .. 2^27 - 1                  */
+    int max_batch;         /* requests per attention call, 1..1024               */
+    int max_query;         /* query tokens per request and call, >= 1;           */
+                           /* heads / kv_heads * max_query <= 32                 */
+    float sm_scale;        /* score scale; 0 selects 1/sqrt(head_dim)            */
+    float k_scale, v_scale;/* global scales, powers of two in 2^-60 .. 2^59: the */
+                           /* block scale covers max|x| from 0.006 to 2688       */
+} mac_quant_config;
+
+/* Bytes of the two backing buffers (host arithmetic).  store: the pages;
+ * scratch: partial summaries of one attention call and the error word. */
+mac_status mac_quant_query_sizes(const mac_quant_config *cfg, size_t *store_bytes, size_t *scratch_bytes);
+
+/* A handle over caller-allocated device buffers (256-byte aligned, at least
+ * the sizes above; MAC_ERR_OOM if not) on the current device.  Zeroes both
+ * (an unwritten slot reads as zeros).  Synchronous.  Every call below needs
+ * that device to be current (MAC_ERR_INVALID_ARG otherwise).  Calls on one
+ * handle, replays of graphs captured from it among them, must be ordered
+ * with one another (one stream, or events): they share the scratch.  Handles
+ * (the layers of a model) whose calls are ordered may share one scratch
+ * buffer. */
+mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t store_bytes, void *dev_scratch,
+                            size_t scratch_bytes, mac_quant_handle *out);
+
+/* Waits for the device, then frees the handle; the buffers stay the caller's. */
+mac_status mac_quant_destroy(mac_quant_handle h);
+
+/* Store n_tokens tokens of K (post-RoPE) and V, bf16, token t's kv_heads x 128
+ * elements at t * stride (elements, multiples of 8; 16-byte aligned), at
+ * dev_slots[t] = page * 16 + offset; a negative slot skips its token, one past
+ * the store is refused (nothing is written, mac_quant_sync reports it).  Slots
+ * of one call must differ: where two tokens share one, what it holds
+ * afterwards is a mix of both.  Async on stream. */
+mac_status mac_quant_append(mac_quant_handle h, int n_tokens, const void *dev_k, int64_t k_stride, const void *dev_v,
+                            int64_t v_stride, const int32_t *dev_slots, void *stream);
+
+/* Read tokens back: dev_k, dev_v bf16 [n_tokens][kv_heads][128], the stored
+ * values (exact in bf16; zeros for a negative or refused slot).  For a
+ * prefill's own attention, or to hand a request to a bf16 store.  Async. */
+mac_status mac_quant_gather(mac_quant_handle h, int n_tokens, const int32_t *dev_slots, void *dev_k, void *dev_v,
+                            void *stream);
+
+/* Decode attention of n_query query tokens for each of `batch` requests over
+ * the stored tokens; query i of a request of len tokens sees the first
+ * len - (n_query - 1) + i of them (its own among them: append first).
+ *   dev_q      bf16 [batch][n_query][heads][128], post-RoPE
+ *   dev_table  int32, request b's pages at b * table_stride, table_cols of them
+ *   dev_lens   int32 [batch] tokens of each request, 0 .. 16 table_cols; a
+ *              request without tokens (an idle slot) gives out 0, lse -inf
+ *   dev_out    bf16 [batch][n_query][heads][128]; dev_lse fp32
+ *              [batch][n_query][heads] natural-log LSE, or NULL
+ * What slots past a request's length hold, NaN included, has no effect.
+ * Results do not depend on other requests' values, but the split of the work,
+ * and with it the order of sums, depends on all lengths of the call.  A page
+ * outside the store or a length outside the table is not read; the request's
+ * output is then wrong and mac_quant_sync reports it.  Async on stream. */
+mac_status mac_quant_attention(mac_quant_handle h, int batch, int n_query, const void *dev_q, const int32_t *dev_table,
+                               int64_t table_stride, int table_cols, const int32_t *dev_lens, void *dev_out,
+                               float *dev_lse, void *stream);
+
+/* Wait for the device and report what its checks met since the last call:
+ * MAC_ERR_STATE (text in mac_quant_last_error), which is then cleared. */
+mac_status mac_quant_sync(mac_quant_handle h);
+
+/* Text of the handle's last error, or "" (owned by the handle). */
+const char *mac_quant_last_error(mac_quant_handle h);
+
 /* Human-readable text for a status code (static storage). */
 const char *mac_status_string(mac_status s);
 

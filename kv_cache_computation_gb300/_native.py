@@ -41,7 +41,23 @@ class MacProfile(ctypes.Structure):
                 ("steps", ctypes.c_uint64)]
 
 
+class MacRopeConfig(ctypes.Structure):
+    _fields_ = [("heads", _i), ("kv_heads", _i), ("head_dim", _i), ("rotary_dim", _i), ("interleaved", _i),
+                ("eps", _f), ("rope_base", _d)]
+
+
+class MacRope(ctypes.Structure):
+    _fields_ = [("cfg", MacRopeConfig), ("turns", ctypes.c_uint64 * 64)]
+
+
+class MacQuantConfig(ctypes.Structure):
+    _fields_ = [("heads", _i), ("kv_heads", _i), ("head_dim", _i), ("page_size", _i), ("num_pages", _i),
+                ("max_batch", _i), ("max_query", _i), ("sm_scale", _f), ("k_scale", _f), ("v_scale", _f)]
+
+
 _pcfg = ctypes.POINTER(MacConfig)
+_prope = ctypes.POINTER(MacRope)
+_pqcfg = ctypes.POINTER(MacQuantConfig)
 # Every entry point include/mac.h declares: name -> (restype, argtypes).
 SIGNATURES = {
     "mac_query_sizes": (_i, [_pcfg, _psz, _psz, _psz]),
@@ -64,6 +80,17 @@ SIGNATURES = {
     "mac_debug_get_decisions": (_i, [_vp, _i, _pi32, _pi32, _pf, _pf]),
     "mac_debug_read_ring": (_i, [_vp, _i, _pi32, _pu16, _pf, _pf, _pi64, _pi64]),
     "mac_attention_noalloc": (_i, [_i, _i, _i, _i, _i64, _vp, _vp, _pi32, _vp, _vp, _vp, _f, _vp]),
+    "mac_rope_init": (_i, [ctypes.POINTER(MacRopeConfig), _prope]),
+    "mac_qkv_norm_rope": (_i, [_prope, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mac_page_step": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mac_quant_query_sizes": (_i, [_pqcfg, _psz, _psz]),
+    "mac_quant_create": (_i, [_pqcfg, _vp, _sz, _vp, _sz, ctypes.POINTER(_vp)]),
+    "mac_quant_destroy": (_i, [_vp]),
+    "mac_quant_append": (_i, [_vp, _i, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "mac_quant_gather": (_i, [_vp, _i, _vp, _vp, _vp, _vp]),
+    "mac_quant_attention": (_i, [_vp, _i, _i, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp]),
+    "mac_quant_sync": (_i, [_vp]),
+    "mac_quant_last_error": (ctypes.c_char_p, [_vp]),
     "mac_status_string": (ctypes.c_char_p, [_i]),
     "mac_last_error": (ctypes.c_char_p, [_vp]),
 }

@@ -6,6 +6,7 @@ and the current CUDA stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -51,6 +52,30 @@ def _host(t: torch.Tensor, name, dtype, shape=None):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+@contextlib.contextmanager
+def _guard(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """The device made current, and `stream` (where given) the stream that outputs are allocated on."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _guard(device, stream)
+
+
+def _out(shape, device, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def make_config(heads, kv_heads, head_dim, ring_len, band_r, tau, max_batch, max_ctx, page_size=16,
@@ -167,6 +192,17 @@ class MacAttention:
                                      _stream_ptr(stream, self.device))
         _check("mac_decode_step", st, self._h)
         return out, lse
+
+    def decode_step_qkv(self, rotary, qkv, positions, q_weight=None, k_weight=None, out=None, lse=None, want_lse=True,
+                        stream=None):
+        """decode_step from the layer's QKV projection [batch, (heads + 2 kv_heads) * 128]: `rotary` (a QkvRotary of
+        the same heads) makes the four inputs.  positions int32 [batch]: each new token's 0-based index."""
+        if rotary.heads != self.heads or rotary.kv_heads != self.kv_heads:
+            raise ValueError("rotary was made for other heads")
+        if qkv.device != self.device:
+            raise ValueError(f"qkv is on {qkv.device}, the handle lives on {self.device}")
+        q_pre, q_post, k, v = rotary(qkv, positions, q_weight, k_weight, stream=stream)
+        return self.decode_step(q_pre, q_post, k, v, out=out, lse=lse, want_lse=want_lse, stream=stream)
 
     def decode_step_host(self, q_pre, q_post, k_new, v_new, out, lse=None, stream=None):
         """decode_step with pinned host tensors: the step's kernels read the

@@ -1,7 +1,7 @@
 """Build the CUDA library ``_build/libmac.so`` for sm_103a with nvcc.
 
-Two translation units (host C ABI, kernels) compiled in parallel, linked
-with the static CUDA runtime; no cmake, no torch extension machinery.
+The translation units of csrc/ (host C ABI, kernels) compiled in parallel,
+linked with the static CUDA runtime; no cmake, no torch extension machinery.
 """
 import os
 import subprocess
@@ -11,8 +11,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libmac.so")
-SOURCES = ["mac_api.cu", "mac_kernels.cu", "mac_attention.cu", "mac_attention_tc.cu", "mac_noalloc.cu"]
-HEADERS = ["mac_internal.cuh", "mac_device.cuh", "mac_plan.cuh", os.path.join("..", "..", "include", "mac.h")]
+SOURCES = ["mac_api.cu", "mac_kernels.cu", "mac_attention.cu", "mac_attention_tc.cu", "mac_noalloc.cu",
+           "mac_qkv.cu", "mac_pages.cu", "mac_quant.cu", "mac_quant_attention.cu"]
+HEADERS = ["mac_internal.cuh", "mac_device.cuh", "mac_plan.cuh", "mac_quant.cuh", os.path.join("..", "..", "include", "mac.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC"] + ARCH
 

@@ -1,0 +1,233 @@
+// The page bookkeeping of one serving step, on the GPU from the requests'
+// lengths: pages for the new tokens, the finished requests' pages back to the
+// free list, the new lengths, and the packed tokens' positions and slots.
+//
+// Per request b with len tokens and n new ones (n < 0: finished), in order:
+//   before = ceil(len / 16), after = ceil((len + n) / 16), need = after - before
+//   begin  = sum of n over earlier requests          (packed tokens)
+//   first  = sum of need over earlier requests       (pages taken from the ring)
+// Free page ids stand in a ring of num_pages entries; `head` is the next one
+// out and `count` how many there are.  Page j of the step's pages is
+// ring[head + j]; finished requests' pages go to ring[head + count ...].
+//
+// All of it is integers, a few hundred KB at most, so the launch and the chain
+// of dependent steps bound it: load, two block scans, one write phase.  One
+// cluster of blocks does the whole step in a single launch: every block makes
+// both scans of the (at most 1024) requests for itself, one request per
+// thread, and the cluster barrier behind the scans separates all reads of the
+// old state from all writes of the new, so a caller may update in place.
+// Tokens, new pages and freed pages are then spread over all threads, each
+// finding its request by a binary search in shared memory.
+#include "../../include/mac.h"
+#include "mac_device.cuh"
+
+using namespace macgpu;
+
+namespace macgpu {
+
+namespace {
+
+constexpr int kThreads = 1024;          // one request per thread in the scans
+constexpr int kCluster = 8;             // blocks (a portable cluster size)
+constexpr int kOneBlockTokens = 4096;   // up to this many packed tokens one block does the step
+
+struct PageArgs {
+    int batch, table_cols, num_pages, max_tokens;
+    int64_t table_stride;
+    const int32_t *len_in, *new_tokens, *state_in;
+    int32_t *len_out, *state_out, *table, *ring, *starts, *pos, *slot, *status;
+};
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
+
+// Inclusive block scan; *total gets the sum.  Ends with a barrier.
+__device__ long long block_scan(long long v, long long *buf, long long *total)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long x = warp_scan(v, lane);
+    if (lane == 31) buf[w] = x;
+    __syncthreads();
+    long long before = 0, all = 0;
+    {
+        const long long t = warp_scan(buf[lane], lane);
+        all = __shfl_sync(0xffffffffu, t, 31);
+        const long long p = __shfl_sync(0xffffffffu, t, (w + 31) & 31);
+        before = w ? p : 0;
+    }
+    __syncthreads();
+    *total = all;
+    return x + before;
+}
+
+// The last index with v[i] <= x among n non-decreasing values, v[0] <= x.
+__device__ __forceinline__ int last_at_most(const int *v, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int wrap(long long i, int n) { return (int)(i >= n ? i - n : i); }
+
+__global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_constant__ PageArgs a)
+{
+    __shared__ long long buf[32];
+    __shared__ int s_begin[kThreads], s_first[kThreads], s_rel[kThreads], s_len[kThreads];
+    __shared__ unsigned char s_ok[kThreads];
+    __shared__ int s_status, s_popped;
+    pdl_wait();
+    const int tid = threadIdx.x, b = tid;
+    if (tid == 0) s_status = s_popped = 0;
+    const int N = a.num_pages;
+    int head = a.state_in[0], count = a.state_in[1];
+    const bool bad_state = head < 0 || head >= N || count < 0 || count > N;
+    if (bad_state) head = count = 0;
+    const bool live = b < a.batch;
+    const int len = live ? a.len_in[b] : 0, asked = live ? a.new_tokens[b] : 0;
+    const bool bad = len < 0 || (long long)len > (long long)a.table_cols * kPage;
+    const long long n = asked > 0 ? asked : 0;
+    const int before = bad ? 0 : (len + kPage - 1) / kPage;
+    const long long after = bad ? 0 : (len + n + kPage - 1) / kPage;
+    __syncthreads();
+
+    long long total, total_rel, ignored;
+    const long long end = block_scan(n, buf, &total);
+    const bool gone = live && asked < 0 && !bad;
+    const long long rel_end = block_scan(gone ? before : 0, buf, &total_rel);
+    const bool wide = after > a.table_cols, late = end > a.max_tokens;
+    const bool can = live && asked >= 0 && !bad && !wide && !late;
+    const int need = can ? (int)(after - before) : 0;
+    const long long cum = block_scan(need, buf, &ignored);
+    const bool dry = can && need > 0 && cum > count;
+    const bool ok = can && !dry;
+    int bits = (dry ? 1 : 0) | (live && bad ? 4 : 0);
+    if (live && asked >= 0 && !bad) bits |= wide ? 2 : late ? 8 : 0;
+    if (bits) atomicOr(&s_status, bits);
+    if (ok && need > 0) atomicMax(&s_popped, (int)cum);
+    const long long cap = a.max_tokens;
+    const int begin = (int)(end - n < cap ? end - n : cap);
+    s_begin[tid] = begin;
+    s_first[tid] = (int)(cum - need < 0x7fffffff ? cum - need : 0x7fffffff);
+    s_rel[tid] = (int)(rel_end - (gone ? before : 0));
+    s_len[tid] = bad ? 0 : len;
+    s_ok[tid] = ok;
+    __syncthreads();
+    const int popped = s_popped;
+    const bool give_back = !bad_state && (long long)count + total_rel <= N;
+
+    // every block has read the old lengths and state by now
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+
+    const int rank = blockIdx.x, stride = gridDim.x * kThreads, gid = rank * kThreads + tid;
+    int found = 0;   // status bits met while writing
+    if (rank == 0) {
+        if (live) {
+            a.len_out[b] = gone ? 0 : ok ? (int)(len + n) : len;
+            a.starts[b] = begin;
+        }
+        if (tid == 0) {
+            a.starts[a.batch] = (int)(total < cap ? total : cap);
+            if (bad_state) {
+                a.state_out[0] = a.state_in[0];
+                a.state_out[1] = a.state_in[1];
+            } else {
+                a.state_out[0] = wrap((long long)head + popped, N);
+                a.state_out[1] = count - popped + (give_back ? (int)total_rel : 0);
+            }
+            found = s_status | (bad_state ? 4 : 0) | (total_rel && !give_back ? 16 : 0);
+        }
+    }
+    // block table: the new pages' entries
+    for (int j = gid; j < popped; j += stride) {
+        const int r = last_at_most(s_first, a.batch, j), l = s_len[r];
+        const int id = a.ring[wrap((long long)head + j, N)];
+        if ((unsigned)id >= (unsigned)N) found |= 4;
+        a.table[r * a.table_stride + (l + kPage - 1) / kPage + (j - s_first[r])] = id;
+    }
+    // finished requests' pages behind the ring's last free one
+    if (give_back) {
+        for (int j = gid; j < (int)total_rel; j += stride) {
+            const int r = last_at_most(s_rel, a.batch, j);
+            const int id = a.table[r * a.table_stride + (j - s_rel[r])];
+            if ((unsigned)id >= (unsigned)N) found |= 4;
+            a.ring[wrap(wrap((long long)head + count, N) + (long long)j, N)] = id;
+        }
+    }
+    // positions and slots of the packed tokens
+    const int tokens = (int)(total < cap ? total : cap);
+    for (int t = gid; t < a.max_tokens; t += stride) {
+        int pos = 0, slot = -1;
+        if (t < tokens) {
+            const int r = last_at_most(s_begin, a.batch, t), l = s_len[r];
+            pos = l + (t - s_begin[r]);
+            if (s_ok[r]) {
+                const int c = pos / kPage, had = (l + kPage - 1) / kPage;
+                const int id = c < had ? a.table[r * a.table_stride + c]
+                                       : a.ring[wrap((long long)head + s_first[r] + (c - had), N)];
+                if ((unsigned)id < (unsigned)N) slot = id * kPage + pos % kPage;
+                else found |= 4;
+            }
+        }
+        a.pos[t] = pos;
+        a.slot[t] = slot;
+    }
+    // status: the bits of the scans (block 0) and those met while writing,
+    // gathered in block 0's shared memory of the cluster
+    if (found) {
+        uint32_t addr;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"(smem_u32(&s_status)), "r"(0));
+        asm volatile("atom.shared::cluster.or.b32 %0, [%0], %1;\n" : "+r"(addr) : "r"(found) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    if (rank == 0 && tid == 0) *a.status = *(volatile int *)&s_status;
+}
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
+
+}  // namespace
+
+}  // namespace macgpu
+
+extern "C" mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in,
+                                    const int32_t *dev_new, int32_t *dev_len_out, int32_t *dev_table,
+                                    int64_t table_stride, int table_cols, int32_t *dev_ring,
+                                    const int32_t *dev_state_in, int32_t *dev_state_out, int32_t *dev_starts,
+                                    int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, void *stream)
+{
+    if (batch < 1 || batch > kThreads || max_tokens < 1 || max_tokens > (1 << 30)) return MAC_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > (1 << 27) - 1) return MAC_ERR_INVALID_ARG;   // slots are int32
+    if (table_cols < 1 || table_cols > (1 << 26) || table_stride < table_cols) return MAC_ERR_INVALID_ARG;
+    if ((int64_t)batch * table_cols > 0x7fffffff) return MAC_ERR_INVALID_ARG;
+    const void *p[] = {dev_len_in, dev_new, dev_len_out, dev_table, dev_ring, dev_state_in, dev_state_out, dev_starts,
+                       dev_pos, dev_slot, dev_status};
+    for (const void *x : p)
+        if (!x || !aligned4(x)) return MAC_ERR_INVALID_ARG;
+    PageArgs a{batch, table_cols, num_pages, max_tokens, table_stride, dev_len_in, dev_new, dev_state_in, dev_len_out,
+               dev_state_out, dev_table, dev_ring, dev_starts, dev_pos, dev_slot, dev_status};
+    const int blocks = max_tokens <= kOneBlockTokens ? 1 : kCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, page_step_kernel, a) == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
+}

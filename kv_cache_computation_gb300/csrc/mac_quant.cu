@@ -1,0 +1,468 @@
+// The 4-bit KV store (layout and format: mac_quant.cuh): its handle, the
+// append that quantises new tokens into it by their slots, and the gather that
+// reads tokens back.
+//
+// Append, per block of 16 elements x of a head (all exact in fp32 but the two
+// roundings the format itself makes):
+//   s = e4m3(max|x| / 6), code_i = e2m1(x_i / s)
+// The quotient is formed as x * (1 / s) and then rounded to a multiple of
+// 2^-13 before the conversion.  A tie between two e2m1 values is
+// x = t s with t in {0.25, ..., 5}; x has 8 significant bits and t s at most 7,
+// so a quotient that is no tie is off it by at least 2^-9 of it (2^-11), while
+// x * (1 / s) is within 2^-22 of it: the rounding puts ties back on the tie and
+// moves nothing across one.  A division per element would cost more than the
+// rest of the kernel together.
+#include "../../include/mac.h"
+#include "mac_device.cuh"
+#include "mac_quant.cuh"
+
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+using namespace macgpu;
+
+namespace macgpu {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// two e2m1 codes (lo in the low four bits) of two floats, ties to even, at most 6
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n.reg .b8 t;\ncvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\ncvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// the e4m3 byte of one float, ties to even, at most 448
+__device__ __forceinline__ uint32_t to_e4m3(float x)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xff;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
+{
+    uint32_t r;
+    const unsigned short h = (unsigned short)two;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(h));
+    return r;
+}
+
+// The sixteen elements (as two 16-byte loads) of one block -> scale byte and
+// eight bytes of codes.  inv: 1 / the store's global scale.
+__device__ __forceinline__ void quantise(const uint4 (&u)[2], float inv, uint32_t &scale, uint2 &codes)
+{
+    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    uint32_t top = 0;   // largest magnitude pattern: its order is that of the magnitudes, NaN above infinity
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        top = max(top, w[i] & 0x7fffu);
+        top = max(top, (w[i] >> 16) & 0x7fffu);
+    }
+    scale = 0x7f;       // NaN
+    codes = make_uint2(0, 0);
+    if (top >= 0x7f80u) return;
+    scale = to_e4m3(__uint_as_float(top << 16) * inv / 6.f);
+    if (scale == 0) return;
+    // 1 / s of an e4m3 value s
+    const uint32_t sh = e4m3x2_to_f16x2(scale);
+    const float r = inv / __low2float(*reinterpret_cast<const __half2 *>(&sh));
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        // + 1.5 x 2^10 - 1.5 x 2^10: to a multiple of 2^-13 (|x / s| is below 2^9: s is at least 15/16 of max / 6,
+        // or half of it among the smallest scales, unless the scale saturates; then anything beyond 6 ends as 6)
+        const float lo = fminf(fmaxf(__uint_as_float(w[i] << 16) * r, -8.f), 8.f);
+        const float hi = fminf(fmaxf(__uint_as_float(w[i] & 0xffff0000u) * r, -8.f), 8.f);
+        b[i] = to_e2m1x2(__fsub_rn(__fadd_rn(lo, 1536.f), 1536.f), __fsub_rn(__fadd_rn(hi, 1536.f), 1536.f));
+    }
+    codes.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    codes.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
+}
+
+// 4 x 4 bytes across four neighbouring lanes: byte k of lane i <-> byte i of lane k.
+__device__ __forceinline__ uint32_t transpose4(uint32_t x, int lane)
+{
+    uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
+    x = (lane & 1) ? __byte_perm(x, y, 0x3715) : __byte_perm(x, y, 0x6240);
+    y = __shfl_xor_sync(0xffffffffu, x, 2);
+    return (lane & 2) ? __byte_perm(x, y, 0x3276) : __byte_perm(x, y, 0x5410);
+}
+
+struct MoveArgs {
+    QuantStore st;
+    const __nv_bfloat16 *k, *v;         // append: sources with a token stride
+    int64_t k_stride, v_stride;
+    __nv_bfloat16 *k_out, *v_out;       // gather: dense destinations
+    const int32_t *slots;
+    int64_t rows;                       // 2 x tokens x kv_heads
+    int n_tokens;
+};
+
+// One row (token, K or V, head) per eight lanes, one block of 16 per lane.
+__global__ void __launch_bounds__(kThreads) quant_append_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31, j = threadIdx.x & 7;
+    const int Hkv = a.st.kv_heads;
+    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
+    const bool in = row < a.rows;
+    const int h = in ? (int)(row % Hkv) : 0;
+    const int64_t r2 = in ? row / Hkv : 0;
+    const bool is_v = r2 & 1;
+    const int t = (int)(r2 >> 1);
+    const int slot = in ? a.slots[t] : -1;
+    bool ok = slot >= 0;
+    if (ok && slot / kPage >= a.st.num_pages) {
+        ok = false;
+        if (j == 0) atomicOr(a.st.err, kQErrSlot);
+    }
+    uint32_t scale = 0;
+    uint2 codes = make_uint2(0, 0);
+    if (ok) {
+        const __nv_bfloat16 *x = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * kD + j * kQBlock;
+        const uint4 u[2] = {reinterpret_cast<const uint4 *>(x)[0], reinterpret_cast<const uint4 *>(x)[1]};
+        quantise(u, is_v ? a.st.v_inv : a.st.k_inv, scale, codes);
+    }
+    const uint32_t lo = transpose4(codes.x, lane), hi = transpose4(codes.y, lane);
+    if (!ok) return;
+    uint8_t *page = a.st.pages + ((size_t)(slot / kPage) * Hkv + h) * kQPageBytes;
+    const int tok = slot % kPage;
+    if (!is_v) {
+        *reinterpret_cast<uint2 *>(page + tok * (kD / 2) + j * 8) = codes;
+        page[kQKScale + tok * kQBlocks + j] = (uint8_t)scale;
+    } else {
+        // lane 4 w + i of the row holds the words (w, g = i) and (w, g = 4 + i)
+        const int c = tok >> 2, tt = tok & 3;
+        uint8_t *p = page + kQV + (j >> 2) * 512 + c * 16 + tt * 4;
+        *reinterpret_cast<uint32_t *>(p + (j & 3) * 64) = lo;
+        *reinterpret_cast<uint32_t *>(p + (4 + (j & 3)) * 64) = hi;
+        page[kQVScale + c * 32 + j * 4 + tt] = (uint8_t)scale;
+    }
+}
+
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\ncvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// four codes' bf16 values, times the block's scale (exact in both)
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float s)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return bf16x2_bits(__floats2bfloat162_rn(f.x * s, f.y * s));
+}
+
+__global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31, j = threadIdx.x & 7;
+    const int Hkv = a.st.kv_heads;
+    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
+    const bool in = row < a.rows;
+    const int h = in ? (int)(row % Hkv) : 0;
+    const int64_t r2 = in ? row / Hkv : 0;
+    const bool is_v = r2 & 1;
+    const int t = (int)(r2 >> 1);
+    const int slot = in ? a.slots[t] : -1;
+    bool ok = slot >= 0;
+    if (ok && slot / kPage >= a.st.num_pages) {
+        ok = false;
+        if (j == 0) atomicOr(a.st.err, kQErrSlot);
+    }
+    uint32_t scale = 0;
+    uint2 codes = make_uint2(0, 0);
+    if (ok) {
+        const uint8_t *page = a.st.pages + ((size_t)(slot / kPage) * Hkv + h) * kQPageBytes;
+        const int tok = slot % kPage;
+        if (!is_v) {
+            codes = *reinterpret_cast<const uint2 *>(page + tok * (kD / 2) + j * 8);
+            scale = page[kQKScale + tok * kQBlocks + j];
+        } else {
+            const int c = tok >> 2, tt = tok & 3;
+            const uint8_t *p = page + kQV + (j >> 2) * 512 + c * 16 + tt * 4;
+            codes.x = *reinterpret_cast<const uint32_t *>(p + (j & 3) * 64);
+            codes.y = *reinterpret_cast<const uint32_t *>(p + (4 + (j & 3)) * 64);
+            scale = page[kQVScale + c * 32 + j * 4 + tt];
+        }
+    }
+    const uint32_t lo = transpose4(codes.x, lane), hi = transpose4(codes.y, lane);
+    if (!in) return;
+    if (is_v) codes = make_uint2(lo, hi);
+    const uint32_t sh = e4m3x2_to_f16x2(scale);
+    const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * (is_v ? a.st.v_scale : a.st.k_scale);
+    uint32_t x[4], y[4];
+    e2m1x8_to_f16(codes.x, x);
+    e2m1x8_to_f16(codes.y, y);
+    __nv_bfloat16 *out = (is_v ? a.v_out : a.k_out) + ((int64_t)t * Hkv + h) * kD + j * kQBlock;
+    reinterpret_cast<uint4 *>(out)[0] = make_uint4(scaled_bf16x2(x[0], s), scaled_bf16x2(x[1], s),
+                                                   scaled_bf16x2(x[2], s), scaled_bf16x2(x[3], s));
+    reinterpret_cast<uint4 *>(out)[1] = make_uint4(scaled_bf16x2(y[0], s), scaled_bf16x2(y[1], s),
+                                                   scaled_bf16x2(y[2], s), scaled_bf16x2(y[3], s));
+}
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+bool power_of_two(float x)
+{
+    int e;
+    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e > -60 && e <= 60;
+}
+
+mac_status check_config(const mac_quant_config *c)
+{
+    if (!c) return MAC_ERR_INVALID_ARG;
+    if (c->heads < 1 || c->kv_heads < 1 || c->heads % c->kv_heads || c->heads > 4096) return MAC_ERR_INVALID_ARG;
+    if (c->head_dim != kD || c->page_size != kPage) return MAC_ERR_INVALID_ARG;
+    if (c->max_query < 1 || (int64_t)(c->heads / c->kv_heads) * c->max_query > kQMaxRows) return MAC_ERR_INVALID_ARG;
+    if (c->max_batch < 1 || c->max_batch > kQMaxBatch) return MAC_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->num_pages > (1 << 27) - 1) return MAC_ERR_INVALID_ARG;   // slots are int32
+    if (!(c->sm_scale >= 0.f) || !std::isfinite(c->sm_scale)) return MAC_ERR_INVALID_ARG;
+    if (!power_of_two(c->k_scale) || !power_of_two(c->v_scale)) return MAC_ERR_INVALID_ARG;
+    return MAC_OK;
+}
+
+struct Sizes {
+    size_t store, part_o, part_ml, meta, err, scratch;
+};
+
+Sizes sizes_of(const mac_quant_config *c)
+{
+    Sizes z;
+    z.store = (size_t)c->num_pages * c->kv_heads * kQPageBytes;
+    z.part_o = 0;
+    z.part_ml = align_up((size_t)kQPartRows * kD * 4);
+    z.meta = z.part_ml + align_up((size_t)kQPartRows * 8);
+    z.err = z.meta + align_up((size_t)kMaxCtas * sizeof(int4));
+    z.scratch = z.err + 256;
+    return z;
+}
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+}  // namespace
+
+}  // namespace macgpu
+
+struct mac_quant_ctx {
+    mac_quant_config cfg;
+    QuantStore st;
+    QuantAttnArgs attn;     // what does not change from call to call
+    int device = 0, sm_count = 0;
+    mac_status sticky = MAC_OK;
+    char errbuf[256] = {0};
+};
+
+namespace macgpu {
+
+namespace {
+
+mac_status fail_cuda(mac_quant_ctx *h, cudaError_t e, const char *where)
+{
+    h->sticky = MAC_ERR_CUDA;
+    std::snprintf(h->errbuf, sizeof h->errbuf, "%s: %s", where, cudaGetErrorString(e));
+    return MAC_ERR_CUDA;
+}
+
+// The handle is usable and its device is the current one.
+mac_status check_handle(mac_quant_ctx *h)
+{
+    if (!h) return MAC_ERR_INVALID_ARG;
+    if (h->sticky != MAC_OK) return h->sticky;
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail_cuda(h, e, "cudaGetDevice");
+    if (dev != h->device) {
+        std::snprintf(h->errbuf, sizeof h->errbuf, "the handle lives on device %d, the current device is %d", h->device, dev);
+        return MAC_ERR_INVALID_ARG;
+    }
+    return MAC_OK;
+}
+
+mac_status launch_move(mac_quant_ctx *h, bool gather, MoveArgs a, void *stream)
+{
+    a.st = h->st;
+    a.rows = 2 * (int64_t)a.n_tokens * h->cfg.kv_heads;
+    const int64_t blocks = (a.rows * 8 + kThreads - 1) / kThreads;
+    const cudaError_t e = launch_maybe_pdl(gather ? quant_gather_kernel : quant_append_kernel, dim3((unsigned)blocks),
+                                           dim3(kThreads), 0, (cudaStream_t)stream, true, a);
+    return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, gather ? "gather launch" : "append launch");
+}
+
+}  // namespace
+
+}  // namespace macgpu
+
+extern "C" {
+
+mac_status mac_quant_query_sizes(const mac_quant_config *cfg, size_t *store_bytes, size_t *scratch_bytes)
+{
+    const mac_status st = check_config(cfg);
+    if (st != MAC_OK) return st;
+    const Sizes z = sizes_of(cfg);
+    if (store_bytes) *store_bytes = z.store;
+    if (scratch_bytes) *scratch_bytes = z.scratch;
+    return MAC_OK;
+}
+
+mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t store_bytes, void *dev_scratch,
+                            size_t scratch_bytes, mac_quant_handle *out)
+{
+    if (!out) return MAC_ERR_INVALID_ARG;
+    *out = nullptr;
+    const mac_status st = check_config(cfg);
+    if (st != MAC_OK) return st;
+    if (!dev_store || !dev_scratch) return MAC_ERR_INVALID_ARG;
+    const Sizes z = sizes_of(cfg);
+    if (((uintptr_t)dev_store | (uintptr_t)dev_scratch) & 255) return MAC_ERR_OOM;
+    if (store_bytes < z.store || scratch_bytes < z.scratch) return MAC_ERR_OOM;
+    mac_quant_ctx *h = new (std::nothrow) mac_quant_ctx();
+    if (!h) return MAC_ERR_OOM;
+    h->cfg = *cfg;
+    char *sc = (char *)dev_scratch;
+    h->st.pages = (uint8_t *)dev_store;
+    h->st.num_pages = cfg->num_pages;
+    h->st.kv_heads = cfg->kv_heads;
+    h->st.k_scale = cfg->k_scale;
+    h->st.v_scale = cfg->v_scale;
+    h->st.k_inv = 1.f / cfg->k_scale;
+    h->st.v_inv = 1.f / cfg->v_scale;
+    h->st.err = (uint32_t *)(sc + z.err);
+    QuantAttnArgs &a = h->attn;
+    a = QuantAttnArgs{};
+    a.st = h->st;
+    a.heads = cfg->heads;
+    a.G = cfg->heads / cfg->kv_heads;
+    const double scale = cfg->sm_scale > 0.f ? (double)cfg->sm_scale : 1.0 / std::sqrt((double)kD);
+    a.scale_log2 = (float)(scale * 1.4426950408889634 * cfg->k_scale);
+    a.part_o = (float *)(sc + z.part_o);
+    a.part_ml = (float2 *)(sc + z.part_ml);
+    a.meta = (int4 *)(sc + z.meta);
+
+    cudaDeviceProp prop;
+    bool good = cudaGetDevice(&h->device) == cudaSuccess && cudaGetDeviceProperties(&prop, h->device) == cudaSuccess;
+    good = good && prop.major * 10 + prop.minor == 103;
+    if (good) {
+        h->sm_count = prop.multiProcessorCount;
+        // an unwritten slot reads back as zeros
+        good = quant_attention_config(h->sm_count) == cudaSuccess && cudaMemset(dev_store, 0, z.store) == cudaSuccess &&
+               cudaMemset(dev_scratch, 0, z.scratch) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+    }
+    if (!good) {
+        delete h;
+        return MAC_ERR_CUDA;
+    }
+    *out = h;
+    return MAC_OK;
+}
+
+mac_status mac_quant_destroy(mac_quant_handle h)
+{
+    if (!h) return MAC_ERR_INVALID_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(h->device) == cudaSuccess) {
+        cudaDeviceSynchronize();
+        if (dev != h->device) cudaSetDevice(dev);
+    }
+    delete h;
+    return MAC_OK;
+}
+
+const char *mac_quant_last_error(mac_quant_handle h) { return h ? h->errbuf : ""; }
+
+mac_status mac_quant_append(mac_quant_handle h, int n_tokens, const void *dev_k, int64_t k_stride, const void *dev_v,
+                            int64_t v_stride, const int32_t *dev_slots, void *stream)
+{
+    const mac_status st = check_handle(h);
+    if (st != MAC_OK) return st;
+    if (n_tokens < 0) return MAC_ERR_INVALID_ARG;
+    if (n_tokens == 0) return MAC_OK;
+    const int64_t row = (int64_t)h->cfg.kv_heads * kD;
+    if (!dev_k || !dev_v || !dev_slots || !aligned16(dev_k) || !aligned16(dev_v) || ((uintptr_t)dev_slots & 3))
+        return MAC_ERR_INVALID_ARG;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return MAC_ERR_INVALID_ARG;
+    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return MAC_ERR_INVALID_ARG;
+    MoveArgs a{};
+    a.k = (const __nv_bfloat16 *)dev_k;
+    a.v = (const __nv_bfloat16 *)dev_v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.slots = dev_slots;
+    a.n_tokens = n_tokens;
+    return launch_move(h, false, a, stream);
+}
+
+mac_status mac_quant_gather(mac_quant_handle h, int n_tokens, const int32_t *dev_slots, void *dev_k, void *dev_v,
+                            void *stream)
+{
+    const mac_status st = check_handle(h);
+    if (st != MAC_OK) return st;
+    if (n_tokens < 0) return MAC_ERR_INVALID_ARG;
+    if (n_tokens == 0) return MAC_OK;
+    if (!dev_k || !dev_v || !dev_slots || !aligned16(dev_k) || !aligned16(dev_v) || ((uintptr_t)dev_slots & 3))
+        return MAC_ERR_INVALID_ARG;
+    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return MAC_ERR_INVALID_ARG;
+    MoveArgs a{};
+    a.k_out = (__nv_bfloat16 *)dev_k;
+    a.v_out = (__nv_bfloat16 *)dev_v;
+    a.slots = dev_slots;
+    a.n_tokens = n_tokens;
+    return launch_move(h, true, a, stream);
+}
+
+mac_status mac_quant_attention(mac_quant_handle h, int batch, int n_query, const void *dev_q, const int32_t *dev_table,
+                               int64_t table_stride, int table_cols, const int32_t *dev_lens, void *dev_out,
+                               float *dev_lse, void *stream)
+{
+    const mac_status st = check_handle(h);
+    if (st != MAC_OK) return st;
+    if (batch < 0 || batch > h->cfg.max_batch || n_query < 1 || n_query > h->cfg.max_query) return MAC_ERR_INVALID_ARG;
+    if (batch == 0) return MAC_OK;
+    if (!dev_q || !dev_table || !dev_lens || !dev_out || !aligned16(dev_q) || !aligned16(dev_out) ||
+        (((uintptr_t)dev_table | (uintptr_t)dev_lens | (uintptr_t)dev_lse) & 3))
+        return MAC_ERR_INVALID_ARG;
+    if (table_cols < 1 || table_cols > (1 << 26) || table_stride < table_cols) return MAC_ERR_INVALID_ARG;
+    QuantAttnArgs a = h->attn;
+    a.n_query = n_query;
+    a.rows = a.G * n_query;
+    a.batch = batch;
+    a.q = (const __nv_bfloat16 *)dev_q;
+    a.table = dev_table;
+    a.table_stride = table_stride;
+    a.table_cols = table_cols;
+    a.lens = dev_lens;
+    a.out = (__nv_bfloat16 *)dev_out;
+    a.lse = dev_lse;
+    const cudaError_t e = launch_quant_attention(a, h->sm_count, (cudaStream_t)stream);
+    return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, "attention launch");
+}
+
+mac_status mac_quant_sync(mac_quant_handle h)
+{
+    mac_status st = check_handle(h);
+    if (st != MAC_OK) return st;
+    cudaError_t e = cudaDeviceSynchronize();
+    uint32_t bits = 0;
+    if (e == cudaSuccess) e = cudaMemcpy(&bits, h->st.err, 4, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && bits) e = cudaMemset(h->st.err, 0, 4);
+    if (e != cudaSuccess) return fail_cuda(h, e, "mac_quant_sync");
+    h->errbuf[0] = 0;
+    if (!bits) return MAC_OK;
+    std::snprintf(h->errbuf, sizeof h->errbuf, "device checks met:%s%s%s%s", bits & kQErrPage ? " a page outside the pool" : "",
+                  bits & kQErrSlot ? " a slot outside the pool" : "",
+                  bits & kQErrLen ? " a length outside the page table" : "",
+                  bits & kQErrTimeout ? " a copy that did not arrive" : "");
+    return MAC_ERR_STATE;
+}
+
+}  // extern "C"

@@ -1,0 +1,63 @@
+"""Page bookkeeping of a serving step on the GPU (mac_page_step of include/mac.h)."""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import _native as N
+from .attention import _check, _dev, _on, _out, _stream_ptr
+
+# bits of PageStep.status
+OUT_OF_PAGES, ROW_FULL, OUT_OF_RANGE, TOO_MANY_TOKENS, RING_FULL = 1, 2, 4, 8, 16
+
+
+class PageStep(NamedTuple):
+    """What page_step returns; all int32 tensors on the GPU."""
+    lengths: torch.Tensor      # [batch] tokens each request holds after the step
+    free_state: torch.Tensor   # [2] head and count of the free ring after the step
+    starts: torch.Tensor       # [batch + 1] request b's new tokens are the packed tokens starts[b]:starts[b+1]
+    positions: torch.Tensor    # [max_tokens] 0-based position of each packed token (0 past the last)
+    slots: torch.Tensor        # [max_tokens] page * 16 + offset, or -1: not stored
+    status: torch.Tensor       # [1] 0, or the bits above
+
+
+def new_page_pool(num_pages, device=None):
+    """(free_pages, free_state) of a pool whose pages are all free."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return (torch.arange(num_pages, dtype=torch.int32, device=device),
+            torch.tensor([0, num_pages], dtype=torch.int32, device=device))
+
+
+def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_tokens, in_place=False,
+              stream=None) -> PageStep:
+    """Pages, positions and slots for one step's new tokens, from the lengths on the GPU.
+
+    lengths, new_tokens int32 [batch]: tokens each request holds and its new
+    ones (negative: the request is finished, its pages are freed).  page_table
+    int32 [batch, columns] and free_pages int32 [num_pages] are updated in
+    place; lengths and free_state come back as new tensors, or, with in_place,
+    in the tensors passed (for a captured step that runs on).
+    """
+    device = lengths.device
+    B = lengths.shape[0]
+    li, ni = _dev(lengths, "lengths", torch.int32, (B,)), _dev(new_tokens, "new_tokens", torch.int32, (B,), device)
+    if not page_table.is_cuda or page_table.device != device or page_table.dtype != torch.int32:
+        raise TypeError("page_table must be an int32 tensor on the requests' GPU")
+    if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be [{B}, columns] with dense rows, got {tuple(page_table.shape)}")
+    cols = page_table.shape[1]
+    stride = page_table.stride(0) if B > 1 else cols
+    n = free_pages.numel()
+    ring = _dev(free_pages, "free_pages", torch.int32, (n,), device)
+    state = _dev(free_state, "free_state", torch.int32, (2,), device)
+    with _on(device, stream):
+        out = (lengths if in_place else _out((B,), device, torch.int32),
+               free_state if in_place else _out((2,), device, torch.int32), _out((B + 1,), device, torch.int32),
+               _out((max_tokens,), device, torch.int32), _out((max_tokens,), device, torch.int32),
+               _out((1,), device, torch.int32))
+        lo, so, starts, pos, slot, status = (t.data_ptr() for t in out)
+        _check("mac_page_step",
+               N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, page_table.data_ptr(), stride, cols, ring, state, so,
+                                     starts, pos, slot, status, _stream_ptr(stream, device)))
+    return PageStep(*out)

@@ -1,0 +1,153 @@
+"""A paged KV store of 4 bits per value and decode attention over it (the
+mac_quant_* calls of include/mac.h)."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native as N
+from .attention import _dev, _on, _out, _stream_ptr
+from .rotary import _rows
+
+
+def _check(fn, status, handle=None):
+    if status != N.MAC_OK:
+        detail = (N.lib().mac_quant_last_error(handle) or b"").decode() if handle is not None and handle.value else ""
+        raise N.MacError(fn, status, detail)
+
+
+def quant_query_sizes(cfg: N.MacQuantConfig):
+    """(store_bytes, scratch_bytes) for a configuration (host only)."""
+    store, scratch = ctypes.c_size_t(), ctypes.c_size_t()
+    _check("mac_quant_query_sizes",
+           N.lib().mac_quant_query_sizes(ctypes.byref(cfg), ctypes.byref(store), ctypes.byref(scratch)))
+    return store.value, scratch.value
+
+
+class QuantKV:
+    """One attention layer's 4-bit paged KV store on the current CUDA device.
+
+    append stores post-RoPE keys and values at slots (page * 16 + offset, as
+    page_step makes them), gather reads them back, attention decodes over the
+    pages of a page table.  max_query new tokens per request and call at most
+    (heads / kv_heads * max_query <= 32).  Calls on one object must be ordered
+    with one another (they share its scratch); layers whose calls are ordered
+    may share scratch: pass another QuantKV as `share`.
+    """
+
+    def __init__(self, heads, kv_heads, num_pages, head_dim=128, page_size=16, max_batch=1, max_query=1, sm_scale=0.0,
+                 k_scale=1.0, v_scale=1.0, device=None, share=None):
+        self.cfg = N.MacQuantConfig(heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_query, float(sm_scale),
+                                    float(k_scale), float(v_scale))
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.num_pages, self.page_size, self.max_batch, self.max_query = num_pages, page_size, max_batch, max_query
+        device = torch.device("cuda" if device is None else device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        self._h = ctypes.c_void_p()
+        store, scratch = quant_query_sizes(self.cfg)
+        self.sizes = dict(store=store, scratch=scratch)
+        with torch.cuda.device(self.device):
+            self._store = torch.empty(store, dtype=torch.uint8, device=self.device)
+            if share is not None:
+                if share.device != self.device or share._scratch.numel() < scratch:
+                    raise ValueError("share must be a QuantKV on the same device with as large a scratch")
+                self._scratch = share._scratch
+            else:
+                self._scratch = torch.empty(scratch, dtype=torch.uint8, device=self.device)
+            h = ctypes.c_void_p()
+            _check("mac_quant_create",
+                   N.lib().mac_quant_create(ctypes.byref(self.cfg), self._store.data_ptr(), store, self._scratch.data_ptr(),
+                                            scratch, ctypes.byref(h)))
+        self._h = h
+
+    # -- lifetime -----------------------------------------------------------
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            N.lib().mac_quant_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # -- store --------------------------------------------------------------
+    def append(self, k, v, slots, stream=None):
+        """Store bf16 k, v [tokens, kv_heads, 128] (tokens may stand apart) at slots int32 [tokens]; negative: skipped."""
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise ValueError("k and v must hold the same tokens")
+        if k.device != self.device or v.device != self.device:
+            raise ValueError(f"k and v must be on {self.device}")
+        kp, ks = _rows(k, "k", self.kv_heads, self.head_dim)
+        vp, vs = _rows(v, "v", self.kv_heads, self.head_dim)
+        s = _dev(slots, "slots", torch.int32, (n,), self.device)
+        with _on(self.device, stream):
+            _check("mac_quant_append", N.lib().mac_quant_append(self._h, n, kp, ks, vp, vs, s,
+                                                                _stream_ptr(stream, self.device)), self._h)
+
+    def gather(self, slots, stream=None):
+        """The stored k, v bf16 [tokens, kv_heads, 128] at slots int32 [tokens]; zeros where negative."""
+        n = slots.shape[0]
+        s = _dev(slots, "slots", torch.int32, (n,), self.device)
+        shape = (n, self.kv_heads, self.head_dim)
+        with _on(self.device, stream):
+            k, v = _out(shape, self.device), _out(shape, self.device)
+            _check("mac_quant_gather", N.lib().mac_quant_gather(self._h, n, s, k.data_ptr(), v.data_ptr(),
+                                                                _stream_ptr(stream, self.device)), self._h)
+        return k, v
+
+    # -- attention ------------------------------------------------------------
+    def attention(self, q, page_table, lengths, out=None, lse=None, want_lse=True, stream=None):
+        """Decode attention: q bf16 [batch, heads, 128] or [batch, n_query, heads, 128] over the tokens that
+        page_table int32 [batch, columns] and lengths int32 [batch] name; query i of n sees the first
+        length - (n - 1) + i tokens.  Returns (out, lse) of q's shape (lse without the last axis)."""
+        B = q.shape[0]
+        if q.dim() not in (3, 4):
+            raise ValueError("q must be [batch, heads, 128] or [batch, n_query, heads, 128]")
+        nq = q.shape[1] if q.dim() == 4 else 1
+        shape = tuple(q.shape[:-2]) + (self.heads, self.head_dim)
+        qp = _dev(q, "q", torch.bfloat16, shape, self.device)
+        if not page_table.is_cuda or page_table.device != self.device or page_table.dtype != torch.int32:
+            raise TypeError(f"page_table must be an int32 tensor on {self.device}")
+        if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError(f"page_table must be [{B}, columns] with dense rows, got {tuple(page_table.shape)}")
+        cols = page_table.shape[1]
+        lp = _dev(lengths, "lengths", torch.int32, (B,), self.device)
+        with _on(self.device, stream):
+            if out is None:
+                out = _out(shape, self.device)
+            if lse is None and want_lse:
+                lse = _out(shape[:-1], self.device, torch.float32)
+            _check("mac_quant_attention",
+                   N.lib().mac_quant_attention(self._h, B, nq, qp, page_table.data_ptr(),
+                                               page_table.stride(0) if B > 1 else cols, cols, lp,
+                                               _dev(out, "out", torch.bfloat16, shape, self.device),
+                                               None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1],
+                                                                             self.device),
+                                               _stream_ptr(stream, self.device)), self._h)
+        return out, lse
+
+    def decode_step_qkv(self, rotary, qkv, positions, slots, page_table, lengths, q_weight=None, k_weight=None,
+                        stream=None):
+        """One layer's step from its QKV projection: norm and rotation, append, attention.
+
+        qkv [batch * n_query, (heads + 2 kv_heads) * 128]; positions, slots and lengths (the tokens after the
+        step) as page_step gives them for n_query new tokens per request.  Returns (out, lse).
+        """
+        B = lengths.shape[0]
+        if B == 0 or qkv.shape[0] % B:
+            raise ValueError("qkv must hold the same number of new tokens for every request")
+        if rotary.heads != self.heads or rotary.kv_heads != self.kv_heads:
+            raise ValueError("rotary was made for other heads")
+        n = qkv.shape[0]
+        _, q, k, v = rotary(qkv, positions[:n], q_weight, k_weight, want_pre=False, stream=stream)
+        self.append(k, v, slots[:n], stream=stream)
+        return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lengths, stream=stream)
+
+    def sync(self):
+        """Wait for the device; raises MacError if its checks met a bad slot, page or length since the last call."""
+        with _on(self.device, None):
+            _check("mac_quant_sync", N.lib().mac_quant_sync(self._h), self._h)
