@@ -24,8 +24,12 @@ def _check(fn, status, handle=None):
 
 
 def _stream_ptr(stream=None, device=None):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if device is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    # the pointer without a torch Stream object around it (2 us a call on the host)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dev(t: torch.Tensor, name, dtype, shape=None, device=None):
@@ -37,9 +41,9 @@ def _dev(t: torch.Tensor, name, dtype, shape=None, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _host(t: torch.Tensor, name, dtype, shape=None):
@@ -76,6 +80,17 @@ def _on(device, stream):
 
 def _out(shape, device, dtype=torch.bfloat16):
     return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _table(t, B, device):
+    """(pointer, row stride, columns) of an int32 page table [B, columns] whose rows are dense but may stand apart."""
+    if not t.is_cuda or t.device != device or t.dtype != torch.int32:
+        raise TypeError(f"page_table must be an int32 tensor on {device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != B or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"page_table must be [{B}, columns] with dense rows, got shape {tuple(shape)}, "
+                         f"strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if B > 1 else shape[1], shape[1]
 
 
 def make_config(heads, kv_heads, head_dim, ring_len, band_r, tau, max_batch, max_ctx, page_size=16,

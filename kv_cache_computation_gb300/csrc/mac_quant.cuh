@@ -38,7 +38,7 @@ enum : uint32_t { kQErrPage = 1u, kQErrSlot = 2u, kQErrLen = 4u, kQErrTimeout = 
 
 constexpr int kQMaxBatch = 1024;        // requests per attention call (one prefix in shared memory)
 constexpr int kQMaxRows = 32;           // query rows per KV head and request: group x query tokens
-constexpr int kQPartRows = 73728;       // rows of partial summaries the scratch holds (38 MB)
+constexpr int kQPartRows = 40960;       // rows of partial summaries the scratch holds (21 MB)
 
 struct QuantStore {
     uint8_t *pages;

@@ -52,6 +52,7 @@ constexpr float kMargin = 6.f;                          // log2: how far a score
 constexpr float kPShift = 9.f;                          // P is held times 2^kPShift: 2^(6 + 9) is below the f16 maximum
 constexpr uint32_t kSpinLimit = 1u << 22;
 constexpr int kMaxPieces = 32;
+constexpr int kParkRow = kD + 4;                        // floats per parked row: its output and summary, padded
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar)
 {
@@ -140,8 +141,9 @@ struct Smem {
     long long pre[kQMaxBatch + 1];      // units of the requests before b (per KV head)
     int len[kQMaxBatch];
     long long scan[32];
-    // parked pieces of the block, in order: their group (-1: none) and where they stand
+    // parked pieces of the block, in order: their group (-1: none)
     int piece_group[kMaxPieces];
+    float2 nothing;                     // the summary of a piece that is not there
     unsigned long long bar[64];
 };
 
@@ -184,27 +186,41 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
     if (write_lse && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
-// Merges n partial rows (their summaries at ml(i), their output at po(i)) into
-// o, m, l; lanes hold four elements each.
-template <typename F>
-__device__ __forceinline__ void merge_rows(const QuantAttnArgs &a, int n, int first, int stride, F row_of, int lane,
-                                           float4 &o, float &m, float &l)
+// Adds n partial rows to (o, m, l), a warp per call: lanes hold four elements
+// of o each.  at(i) gives partial i's summary (max, sum) and its 128 floats;
+// the summaries are read first, one lane each, so the rows' loads depend on
+// nothing and run together.
+// With kOthers the rows come from other blocks: they are read past the L1.
+template <bool kOthers, typename F>
+__device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, float &m, float &l)
 {
-    for (int i = first; i < n; i += stride) {
-        const int64_t row = row_of(i);
-        if (row < 0) continue;
-        const float2 ml = __ldcg(a.part_ml + row);
-        const float4 p = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * kD) + lane);
-        if (ml.y == 0.f) continue;      // saw no token
-        const float top = fmaxf(m, ml.x);
-        // a NaN summary must survive: fmaxf drops it, the weights do not
-        const float wo = m == -CUDART_INF_F ? 0.f : exp2f(m - top), wp = exp2f(ml.x - top);
-        o.x = o.x * wo + p.x * wp;
-        o.y = o.y * wo + p.y * wp;
-        o.z = o.z * wo + p.z * wp;
-        o.w = o.w * wo + p.w * wp;
-        l = l * wo + ml.y * wp;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int k = min(32, n - i0);
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        const float4 *src = nullptr;
+        if (lane < k) {
+            const float2 *summary;
+            at(i0 + lane, summary, src);
+            ml = kOthers ? __ldcg(summary) : *summary;
+        }
+        const bool none = ml.y == 0.f;      // saw no token
+        const float top = fmaxf(m, warp_max(none ? -CUDART_INF_F : ml.x));
+        // a NaN sum survives: its weight is a number or NaN, and the product NaN
+        const float w = none ? 0.f : exp2f(ml.x - top), wo = l == 0.f ? 0.f : exp2f(m - top);
+        l = l * wo + warp_sum(none ? 0.f : ml.y * w);
+        o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
         m = top;
+#pragma unroll 8
+        for (int i = 0; i < k; i++) {
+            const float4 *p = reinterpret_cast<const float4 *>(__shfl_sync(0xffffffffu, (unsigned long long)src, i));
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const int skip = __shfl_sync(0xffffffffu, (int)none, i);
+            const float4 x = skip ? make_float4(0.f, 0.f, 0.f, 0.f) : kOthers ? __ldcg(p + lane) : p[lane];
+            o.x += x.x * wi;
+            o.y += x.y * wi;
+            o.z += x.z * wi;
+            o.w += x.w * wi;
+        }
     }
 }
 
@@ -216,6 +232,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
     constexpr int TEAMS = WARPS / RW;
     constexpr int PADROWS = NT * 8 * RW;
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
+    static_assert(PADROWS * kParkRow * 4 <= STAGES * kUnitBytes, "a parked piece fits the team's ring");
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Smem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -269,6 +286,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (tid < 2 * TEAMS) sm.piece_group[tid] = -1;
+    if (tid == 0) sm.nothing = make_float2(-CUDART_INF_F, 0.f);
     __syncthreads();
 
     // the block's and the team's range of units
@@ -284,8 +302,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
     const long long teams = (long long)grid * TEAMS, me = (long long)cta * TEAMS + team;
     const long long lo = U * me / teams, hi = U * (me + 1) / teams;
     const long long cta_lo = U * cta / grid, cta_hi = U * (cta + 1) / grid;
-    const int64_t park = ((int64_t)cta * TEAMS + team) * 2 * PADROWS;                 // two parked pieces per team
-    const int64_t crossing = (int64_t)gridDim.x * TEAMS * 2 * PADROWS + (int64_t)cta * 2 * PADROWS;   // two per block
+    // partial rows: the block's two crossing groups, then its teams' first pieces.  A team's last piece is parked in
+    // its own ring, which it has read to the end by then.
+    const int64_t crossing = (int64_t)cta * 2 * PADROWS;
+    const int64_t park = ((int64_t)gridDim.x * 2 + (int64_t)cta * TEAMS) * PADROWS;
+
+    auto parked_o = [&](int t, int r) { return reinterpret_cast<float *>(dyn + (size_t)t * STAGES * kUnitBytes) + r * kParkRow; };
+    auto parked_ml = [&](int t, int r) { return reinterpret_cast<float2 *>(parked_o(t, r) + kD); };
 
     if (lo < hi) {
         Cursor at = cursor_at(sm, a.batch, Hkv, lo);
@@ -572,12 +595,12 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
                         if (a.lse && g8 == 0)
                             a.lse[row] = l == 0.f ? -CUDART_INF_F : (ref[nt][h] - kPShift + log2f(l)) * kLn2;
                     } else {
-                        const int64_t row = park + which * PADROWS + r;
+                        const int64_t row = park + (int64_t)team * PADROWS + r;
+                        float *dst = which ? parked_o(team, r) : a.part_o + row * kD;
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            *reinterpret_cast<float2 *>(a.part_o + row * kD + 16 * j + 2 * g8) =
-                                make_float2(o[nt][j][h], o[nt][j][2 + h]);
-                        if (g8 == 0) a.part_ml[row] = make_float2(ref[nt][h] - kPShift, l);
+                            *reinterpret_cast<float2 *>(dst + 16 * j + 2 * g8) = make_float2(o[nt][j][h], o[nt][j][2 + h]);
+                        if (g8 == 0) *(which ? parked_ml(team, r) : a.part_ml + row) = make_float2(ref[nt][h] - kPShift, l);
                     }
                 }
         }
@@ -607,10 +630,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
         for (int r = warp; r < a.rows; r += WARPS) {
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             float m = -CUDART_INF_F, l = 0.f;
-            const int64_t base = (int64_t)cta * TEAMS * 2 * PADROWS + r;
-            merge_rows(a, j - i, 0, 1,
-                       [&](int k) { return sm.piece_group[i + k] < 0 ? (int64_t)-1 : base + (int64_t)(i + k) * PADROWS; },
-                       lane, o, m, l);
+            merge_rows<false>(j - i, [&](int k, const float2 *&ml, const float4 *&src) {
+                const int t = (i + k) >> 1;
+                const int64_t row = park + (int64_t)t * PADROWS + r;
+                const bool last = (i + k) & 1;
+                ml = sm.piece_group[i + k] < 0 ? &sm.nothing : last ? parked_ml(t, r) : a.part_ml + row;
+                src = reinterpret_cast<const float4 *>(last ? parked_o(t, r) : a.part_o + row * kD);
+            }, lane, o, m, l);
             if (whole) {
                 finish4(a, b, g, r, lane * 4, o, m, l, lane == 0);
             } else {
@@ -628,8 +654,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
 // grid and runs on into the blocks up to meta.y.
 constexpr int kCombineWarps = 4;
 
-__global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const __grid_constant__ QuantAttnArgs a, int grid,
-                                                                          int teams, int padrows)
+__global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const __grid_constant__ QuantAttnArgs a,
+                                                                          int padrows)
 {
     __shared__ float4 so[kCombineWarps][32];
     __shared__ float2 sml[kCombineWarps];
@@ -638,26 +664,26 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
     if (meta.x < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
     const int n = meta.y - (int)blockIdx.x + 1;
-    const int64_t base = (int64_t)grid * teams * 2 * padrows + r;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -CUDART_INF_F, l = 0.f;
-    merge_rows(a, n, warp, kCombineWarps,
-               [&](int k) { return base + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows; }, lane, o, m, l);
+    // warp w takes partials w, w + 4, ...; then lane w of warp 0 the four warps' results
+    merge_rows<true>((n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
+        const int k = i * kCombineWarps + warp;
+        const int64_t row = ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r;
+        ml = a.part_ml + row;
+        src = reinterpret_cast<const float4 *>(a.part_o + row * kD);
+    }, lane, o, m, l);
     so[warp][lane] = o;
     if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
     if (warp) return;
-#pragma unroll
-    for (int w = 1; w < kCombineWarps; w++) {
-        const float2 ml = sml[w];
-        const float4 p = so[w][lane];
-        if (ml.y == 0.f) continue;
-        const float top = fmaxf(m, ml.x);
-        const float wo = m == -CUDART_INF_F ? 0.f : exp2f(m - top), wp = exp2f(ml.x - top);
-        o = make_float4(o.x * wo + p.x * wp, o.y * wo + p.y * wp, o.z * wo + p.z * wp, o.w * wo + p.w * wp);
-        l = l * wo + ml.y * wp;
-        m = top;
-    }
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    m = -CUDART_INF_F;
+    l = 0.f;
+    merge_rows<false>(kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
+        ml = &sml[i];
+        src = so[i];
+    }, lane, o, m, l);
     const int b = meta.x / a.st.kv_heads;
     finish4(a, b, meta.x - b * a.st.kv_heads, r, lane * 4, o, m, l, lane == 0);
 }
@@ -680,13 +706,13 @@ Variant variant_for(int rows)
 {
     if (rows <= 8) return variant<1, 1, 8, 2, 2>();
     if (rows <= 16) return variant<2, 1, 12, 3, 1>();
-    return variant<2, 2, 12, 3, 1>();
+    return variant<2, 2, 12, 4, 1>();
 }
 
 int grid_of(const Variant &v, int sm_count)
 {
     int grid = sm_count * v.blocks_per_sm;
-    const int fit = kQPartRows / (2 * (v.teams + 1) * v.padrows);     // blocks whose partial rows the scratch holds
+    const int fit = kQPartRows / ((v.teams + 2) * v.padrows);     // blocks whose partial rows the scratch holds
     grid = grid < fit ? grid : fit;
     return grid < kMaxCtas ? grid : kMaxCtas;
 }
@@ -711,8 +737,7 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, int sm_count, cudaStr
     const int grid = grid_of(v, sm_count);
     cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, s, true, a);
     if (e != cudaSuccess) return e;
-    return launch_maybe_pdl(quant_combine_kernel, dim3(grid, a.rows), dim3(kCombineWarps * 32), 0, s, true, a, grid, v.teams,
-                            v.padrows);
+    return launch_maybe_pdl(quant_combine_kernel, dim3(grid, a.rows), dim3(kCombineWarps * 32), 0, s, true, a, v.padrows);
 }
 
 }  // namespace macgpu

@@ -6,7 +6,7 @@ from typing import NamedTuple
 import torch
 
 from . import _native as N
-from .attention import _check, _dev, _on, _out, _stream_ptr
+from .attention import _check, _dev, _on, _out, _stream_ptr, _table
 
 # bits of PageStep.status
 OUT_OF_PAGES, ROW_FULL, OUT_OF_RANGE, TOO_MANY_TOKENS, RING_FULL = 1, 2, 4, 8, 16
@@ -42,12 +42,7 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     device = lengths.device
     B = lengths.shape[0]
     li, ni = _dev(lengths, "lengths", torch.int32, (B,)), _dev(new_tokens, "new_tokens", torch.int32, (B,), device)
-    if not page_table.is_cuda or page_table.device != device or page_table.dtype != torch.int32:
-        raise TypeError("page_table must be an int32 tensor on the requests' GPU")
-    if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be [{B}, columns] with dense rows, got {tuple(page_table.shape)}")
-    cols = page_table.shape[1]
-    stride = page_table.stride(0) if B > 1 else cols
+    table, row, cols = _table(page_table, B, device)
     n = free_pages.numel()
     ring = _dev(free_pages, "free_pages", torch.int32, (n,), device)
     state = _dev(free_state, "free_state", torch.int32, (2,), device)
@@ -58,6 +53,6 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
                _out((1,), device, torch.int32))
         lo, so, starts, pos, slot, status = (t.data_ptr() for t in out)
         _check("mac_page_step",
-               N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, page_table.data_ptr(), stride, cols, ring, state, so,
+               N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so,
                                      starts, pos, slot, status, _stream_ptr(stream, device)))
     return PageStep(*out)

@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from . import _native as N
-from .attention import _dev, _on, _out, _stream_ptr
+from .attention import _dev, _on, _out, _stream_ptr, _table
 from .rotary import _rows
 
 
@@ -110,11 +110,7 @@ class QuantKV:
         nq = q.shape[1] if q.dim() == 4 else 1
         shape = tuple(q.shape[:-2]) + (self.heads, self.head_dim)
         qp = _dev(q, "q", torch.bfloat16, shape, self.device)
-        if not page_table.is_cuda or page_table.device != self.device or page_table.dtype != torch.int32:
-            raise TypeError(f"page_table must be an int32 tensor on {self.device}")
-        if page_table.dim() != 2 or page_table.shape[0] != B or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-            raise ValueError(f"page_table must be [{B}, columns] with dense rows, got {tuple(page_table.shape)}")
-        cols = page_table.shape[1]
+        table, row, cols = _table(page_table, B, self.device)
         lp = _dev(lengths, "lengths", torch.int32, (B,), self.device)
         with _on(self.device, stream):
             if out is None:
@@ -122,8 +118,7 @@ class QuantKV:
             if lse is None and want_lse:
                 lse = _out(shape[:-1], self.device, torch.float32)
             _check("mac_quant_attention",
-                   N.lib().mac_quant_attention(self._h, B, nq, qp, page_table.data_ptr(),
-                                               page_table.stride(0) if B > 1 else cols, cols, lp,
+                   N.lib().mac_quant_attention(self._h, B, nq, qp, table, row, cols, lp,
                                                _dev(out, "out", torch.bfloat16, shape, self.device),
                                                None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1],
                                                                              self.device),

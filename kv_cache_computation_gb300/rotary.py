@@ -17,16 +17,16 @@ def _rows(t, name, heads, head_dim):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() == 3:
-        ok = t.shape[1:] == (heads, head_dim) and (t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim))
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1:] == (heads, head_dim) and stride[2] == 1 and (heads == 1 or stride[1] == head_dim)
     else:
-        ok = t.dim() == 2 and t.shape[1] == heads * head_dim and t.stride(1) == 1
+        ok = len(shape) == 2 and shape[1] == heads * head_dim and stride[1] == 1
     if not ok and t.numel():
-        raise ValueError(f"{name} must be [tokens, {heads} x {head_dim}] with dense tokens, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
+        raise ValueError(f"{name} must be [tokens, {heads} x {head_dim}] with dense tokens, got shape {tuple(shape)}, "
+                         f"strides {stride}")
     # a single token's stride is never used; torch may report anything for it
-    stride = t.stride(0) if t.shape[0] > 1 else heads * head_dim
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * head_dim
 
 
 class QkvRotary:
@@ -51,10 +51,9 @@ class QkvRotary:
 
     def __call__(self, qkv, positions, q_weight=None, k_weight=None, want_pre=True, stream=None):
         H, Hkv, d = self.heads, self.kv_heads, self.head_dim
-        p, stride = _rows(qkv, "qkv", H + 2 * Hkv, d)
-        at = p.value or 0
-        return self._run(qkv.shape[0], qkv.device, ctypes.c_void_p(at), stride, ctypes.c_void_p(at + 2 * H * d), stride,
-                         ctypes.c_void_p(at + 2 * (H + Hkv) * d), stride, positions, q_weight, k_weight, want_pre, stream)
+        at, stride = _rows(qkv, "qkv", H + 2 * Hkv, d)
+        return self._run(qkv.shape[0], qkv.device, at, stride, at + 2 * H * d, stride, at + 2 * (H + Hkv) * d, stride,
+                         positions, q_weight, k_weight, want_pre, stream)
 
     def split(self, q, k, v, positions, q_weight=None, k_weight=None, want_pre=True, stream=None):
         """The same from separate projections q [tokens, heads * 128], k and v [tokens, kv_heads * 128]."""
@@ -71,8 +70,8 @@ class QkvRotary:
     def _run(self, T, device, q, qs, k, ks, v, vs, positions, q_weight, k_weight, want_pre, stream):
         H, Hkv, d = self.heads, self.kv_heads, self.head_dim
         pos = _dev(positions, "positions", torch.int32, (T,), device)
-        wq, wk = (ctypes.c_void_p(None) if w is None else _dev(w, n, torch.bfloat16, (d,), device)
-                  for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")))
+        wq = None if q_weight is None else _dev(q_weight, "q_weight", torch.bfloat16, (d,), device)
+        wk = None if k_weight is None else _dev(k_weight, "k_weight", torch.bfloat16, (d,), device)
         with _on(device, stream):
             q_post, k_out, v_out = _out((T, H, d), device), _out((T, Hkv, d), device), _out((T, Hkv, d), device)
             q_pre = _out((T, H, d), device) if want_pre else None
