@@ -66,7 +66,7 @@ __device__ __forceinline__ void quantise(const uint4 (&u)[2], float inv, uint32_
         top = max(top, w[i] & 0x7fffu);
         top = max(top, (w[i] >> 16) & 0x7fffu);
     }
-    scale = 0x7f;       // NaN
+    scale = 0xff;       // NaN
     codes = make_uint2(0, 0);
     if (top >= 0x7f80u) return;
     scale = to_e4m3(__uint_as_float(top << 16) * inv / 6.f);
@@ -87,15 +87,6 @@ __device__ __forceinline__ void quantise(const uint4 (&u)[2], float inv, uint32_
     codes.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
 }
 
-// 4 x 4 bytes across four neighbouring lanes: byte k of lane i <-> byte i of lane k.
-__device__ __forceinline__ uint32_t transpose4(uint32_t x, int lane)
-{
-    uint32_t y = __shfl_xor_sync(0xffffffffu, x, 1);
-    x = (lane & 1) ? __byte_perm(x, y, 0x3715) : __byte_perm(x, y, 0x6240);
-    y = __shfl_xor_sync(0xffffffffu, x, 2);
-    return (lane & 2) ? __byte_perm(x, y, 0x3276) : __byte_perm(x, y, 0x5410);
-}
-
 struct MoveArgs {
     QuantStore st;
     const __nv_bfloat16 *k, *v;         // append: sources with a token stride
@@ -110,7 +101,7 @@ struct MoveArgs {
 __global__ void __launch_bounds__(kThreads) quant_append_kernel(const __grid_constant__ MoveArgs a)
 {
     pdl_wait();
-    const int lane = threadIdx.x & 31, j = threadIdx.x & 7;
+    const int j = threadIdx.x & 7;
     const int Hkv = a.st.kv_heads;
     const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
     const bool in = row < a.rows;
@@ -124,27 +115,23 @@ __global__ void __launch_bounds__(kThreads) quant_append_kernel(const __grid_con
         ok = false;
         if (j == 0) atomicOr(a.st.err, kQErrSlot);
     }
-    uint32_t scale = 0;
-    uint2 codes = make_uint2(0, 0);
-    if (ok) {
-        const __nv_bfloat16 *x = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * kD + j * kQBlock;
-        const uint4 u[2] = {reinterpret_cast<const uint4 *>(x)[0], reinterpret_cast<const uint4 *>(x)[1]};
-        quantise(u, is_v ? a.st.v_inv : a.st.k_inv, scale, codes);
-    }
-    const uint32_t lo = transpose4(codes.x, lane), hi = transpose4(codes.y, lane);
     if (!ok) return;
+    uint32_t scale;
+    uint2 codes;
+    const __nv_bfloat16 *x = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * kD + j * kQBlock;
+    const uint4 u[2] = {reinterpret_cast<const uint4 *>(x)[0], reinterpret_cast<const uint4 *>(x)[1]};
+    quantise(u, is_v ? a.st.v_inv : a.st.k_inv, scale, codes);
     uint8_t *page = a.st.pages + ((size_t)(slot / kPage) * Hkv + h) * kQPageBytes;
     const int tok = slot % kPage;
     if (!is_v) {
         *reinterpret_cast<uint2 *>(page + tok * (kD / 2) + j * 8) = codes;
         page[kQKScale + tok * kQBlocks + j] = (uint8_t)scale;
     } else {
-        // lane 4 w + i of the row holds the words (w, g = i) and (w, g = 4 + i)
         const int c = tok >> 2, tt = tok & 3;
-        uint8_t *p = page + kQV + (j >> 2) * 512 + c * 16 + tt * 4;
-        *reinterpret_cast<uint32_t *>(p + (j & 3) * 64) = lo;
-        *reinterpret_cast<uint32_t *>(p + (4 + (j & 3)) * 64) = hi;
-        page[kQVScale + c * 32 + j * 4 + tt] = (uint8_t)scale;
+        uint8_t *p = page + kQV + (j * 4 + c) * 16 + tt * 4;
+        *reinterpret_cast<uint32_t *>(p) = codes.x;
+        *reinterpret_cast<uint32_t *>(p + 512) = codes.y;
+        page[kQVScale + c * 32 + j * 4 + q_scale_byte(tt)] = (uint8_t)scale;
     }
 }
 
@@ -166,7 +153,7 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float s)
 __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_constant__ MoveArgs a)
 {
     pdl_wait();
-    const int lane = threadIdx.x & 31, j = threadIdx.x & 7;
+    const int j = threadIdx.x & 7;
     const int Hkv = a.st.kv_heads;
     const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
     const bool in = row < a.rows;
@@ -190,15 +177,12 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
             scale = page[kQKScale + tok * kQBlocks + j];
         } else {
             const int c = tok >> 2, tt = tok & 3;
-            const uint8_t *p = page + kQV + (j >> 2) * 512 + c * 16 + tt * 4;
-            codes.x = *reinterpret_cast<const uint32_t *>(p + (j & 3) * 64);
-            codes.y = *reinterpret_cast<const uint32_t *>(p + (4 + (j & 3)) * 64);
-            scale = page[kQVScale + c * 32 + j * 4 + tt];
+            const uint8_t *p = page + kQV + (j * 4 + c) * 16 + tt * 4;
+            codes = make_uint2(*reinterpret_cast<const uint32_t *>(p), *reinterpret_cast<const uint32_t *>(p + 512));
+            scale = page[kQVScale + c * 32 + j * 4 + q_scale_byte(tt)];
         }
     }
-    const uint32_t lo = transpose4(codes.x, lane), hi = transpose4(codes.y, lane);
     if (!in) return;
-    if (is_v) codes = make_uint2(lo, hi);
     const uint32_t sh = e4m3x2_to_f16x2(scale);
     const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * (is_v ? a.st.v_scale : a.st.k_scale);
     uint32_t x[4], y[4];
@@ -344,7 +328,8 @@ mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t
     a.heads = cfg->heads;
     a.G = cfg->heads / cfg->kv_heads;
     const double scale = cfg->sm_scale > 0.f ? (double)cfg->sm_scale : 1.0 / std::sqrt((double)kD);
-    a.scale_log2 = (float)(scale * 1.4426950408889634 * cfg->k_scale);
+    a.scale_log2 = (float)(scale * 1.4426950408889634 * cfg->k_scale * 256.0);
+    a.v_out_scale = cfg->v_scale * 256.f;
     a.part_o = (float *)(sc + z.part_o);
     a.part_ml = (float2 *)(sc + z.part_ml);
     a.meta = (int4 *)(sc + z.meta);

@@ -3,10 +3,13 @@
 //
 // Values.  16 consecutive elements of a head share a scale s, an e4m3 value:
 // s = max|x| / 6 rounded to nearest even, at most 448; an element is s times an
-// e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).  A block that
-// holds a NaN or an infinity stores a NaN scale, so it reads back as NaN.  An
-// e2m1 value times an e4m3 scale has at most six significant bits and lies in
+// e2m1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).  An e2m1 value
+// times an e4m3 scale has at most six significant bits and lies in
 // [2^-10, 2688] (or is 0), so every stored value is exact in bf16 and in f16.
+// A scale is never negative, so bit 7 of its byte is free: shifted to bits 7
+// .. 14 of an f16 the byte is the f16 of 2^-8 times the scale, subnormals
+// included, and 0xff is an f16 NaN.  That byte marks a block that holds a NaN or
+// an infinity, which then reads back as NaN.
 //
 // Layout.  One 16-token page of one KV head is 2304 contiguous bytes (144 per
 // token against 512 in bf16), [num_pages][kv_heads][2304], so a page is one
@@ -16,9 +19,10 @@
 // converted (g = lane / 4, c = lane % 4):
 //   K codes   [token 16][64 B]: byte i of a token = elements 2 i, 2 i + 1
 //   K scales  [token 16][block 8]
-//   V codes   [w 2][g 8][c 4][tt 4][i 4]: token 4 c + tt, block 4 w + i of the
-//             head, elements 2 g and 2 g + 1 of that block
-//   V scales  [c 4][block 8][tt 4]: token 4 c + tt
+//   V codes   [w 2][block 8][c 4][tt 4][i 4]: token 4 c + tt, elements 8 w + 2 i
+//             and 8 w + 2 i + 1 of the block
+//   V scales  [c 4][block 8][4]: tokens 4 c, 4 c + 2, 4 c + 1, 4 c + 3 (two
+//             masks then leave the f16 pairs of tokens 0, 1 and 2, 3)
 // In a byte the lower element stands in the low four bits.
 #pragma once
 #include "mac_internal.cuh"
@@ -36,9 +40,12 @@ static_assert(kQPageBytes == 2304 && kQV % 128 == 0 && kQVScale % 128 == 0, "pag
 // bits of the device error word
 enum : uint32_t { kQErrPage = 1u, kQErrSlot = 2u, kQErrLen = 4u, kQErrTimeout = 8u };
 
+// the byte of token t % 4 among a block's four V scales
+__host__ __device__ inline int q_scale_byte(int tt) { return (tt >> 1) | (tt & 1) << 1; }
+
 constexpr int kQMaxBatch = 1024;        // requests per attention call (one prefix in shared memory)
 constexpr int kQMaxRows = 32;           // query rows per KV head and request: group x query tokens
-constexpr int kQPartRows = 40960;       // rows of partial summaries the scratch holds (21 MB)
+constexpr int kQPartRows = 49152;       // rows of partial summaries the scratch holds (25 MB)
 
 struct QuantStore {
     uint8_t *pages;
@@ -58,7 +65,8 @@ struct QuantAttnArgs {
     const int32_t *lens;
     __nv_bfloat16 *out;
     float *lse;
-    float scale_log2;                   // score scale x log2(e) x k_scale
+    float scale_log2;                   // score scale x log2(e) x k_scale x 2^8
+    float v_out_scale;                  // v_scale x 2^8
     float *part_o;                      // [kQPartRows][128]
     float2 *part_ml;                    // [kQPartRows]
     int4 *meta;                         // [grid]: group that starts in the block and runs on, its last block

@@ -19,10 +19,10 @@
 //    dims) fill M, and 1 to 8 rows cost one N tile.  tcgen05 would need the
 //    unpacked page written to shared memory and read back, 512 B per token
 //    against the 144 that are read here, which alone is 60 % of the budget;
-//  - the order of the contraction index is free, so a thread's K words are 32
-//    consecutive elements of a token, and its V words the same 16 elements of
-//    four consecutive tokens, whose codes are paired by token with two logic
-//    operations per eight codes.
+//  - the orders of the contraction index and of the output's rows are free, so a
+//    thread's K words are 32 consecutive elements of a token (two scales), and
+//    its V words one 16-element block of four consecutive tokens (four scales),
+//    whose codes are paired by token with two logic operations per eight codes.
 // Roundings: Q is bf16 and becomes f16 with a power of two per row (exact
 // unless an element is 2^-28 of the row's largest); stored values are exact in
 // f16; the weights P, at most 2^15, are rounded to f16 (2^-11 of each) and
@@ -107,13 +107,6 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&h)[4])
         : "r"(w));
 }
 
-__device__ __forceinline__ uint32_t scales2(uint32_t two)
-{
-    uint32_t r;
-    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(r) : "r"(two));
-    return r;
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
     uint4 v;
@@ -121,10 +114,27 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ uint32_t lds2(uint32_t addr)
+__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4])
 {
-    unsigned short v;
-    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds4(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;\n" :: "r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds1(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
@@ -132,10 +142,11 @@ __device__ __forceinline__ uint32_t lds2(uint32_t addr)
 // still has to be written).
 __device__ __forceinline__ int units_of(int len) { return len > kUnitTok ? (len - 1) / kUnitTok + 1 : 1; }
 
-// A position on the line of units: request, KV head, unit of the group.
-struct Cursor {
-    int b, g, u, n;     // n: units of the request
-};
+// A warp's shared memory: its ring and, where Q does not stay in registers, Q.
+__host__ __device__ constexpr int team_bytes(int q_tiles, int stages)
+{
+    return stages * kUnitBytes + q_tiles * 2048;
+}
 
 struct Smem {
     long long pre[kQMaxBatch + 1];      // units of the requests before b (per KV head)
@@ -147,30 +158,16 @@ struct Smem {
     unsigned long long bar[64];
 };
 
-__device__ __forceinline__ Cursor cursor_at(const Smem &sm, int batch, int Hkv, long long unit)
+// The request that holds a unit of the line: the last b with pre[b] * Hkv <= unit.
+__device__ __forceinline__ int request_of(const Smem &sm, int batch, int Hkv, long long unit)
 {
-    int lo = 0, hi = batch;             // last b with pre[b] * Hkv <= unit
+    int lo = 0, hi = batch;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sm.pre[mid] * Hkv <= unit) lo = mid;
         else hi = mid;
     }
-    Cursor c;
-    c.b = lo;
-    c.n = (int)(sm.pre[lo + 1] - sm.pre[lo]);
-    const long long in = unit - sm.pre[lo] * Hkv;
-    c.g = (int)(in / c.n);
-    c.u = (int)(in - (long long)c.g * c.n);
-    return c;
-}
-
-__device__ __forceinline__ void step(Cursor &c, const Smem &sm, int batch, int Hkv)
-{
-    if (++c.u < c.n) return;
-    c.u = 0;
-    if (++c.g < Hkv) return;
-    c.g = 0;
-    if (++c.b < batch) c.n = (int)(sm.pre[c.b + 1] - sm.pre[c.b]);
+    return lo;
 }
 
 // Writes a row's finished output (four elements at d0) and its lse.
@@ -179,7 +176,7 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
 {
     const int qt = r / a.G, head = g * a.G + (r - qt * a.G);
     const int64_t row = ((int64_t)b * a.n_query + qt) * a.heads + head;
-    const float inv = l == 0.f ? 0.f : a.st.v_scale / l;
+    const float inv = l == 0.f ? 0.f : a.v_out_scale / l;
     if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<uint2 *>(a.out + row * kD + d0) = make_uint2(
         bf16x2_bits(__floats2bfloat162_rn(o.x * inv, o.y * inv)), bf16x2_bits(__floats2bfloat162_rn(o.z * inv, o.w * inv)));
@@ -191,7 +188,7 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
 // the summaries are read first, one lane each, so the rows' loads depend on
 // nothing and run together.
 // With kOthers the rows come from other blocks: they are read past the L1.
-template <bool kOthers, typename F>
+template <bool kOthers, int kUnroll, typename F>
 __device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, float &m, float &l)
 {
     for (int i0 = 0; i0 < n; i0 += 32) {
@@ -210,7 +207,7 @@ __device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, flo
         l = l * wo + warp_sum(none ? 0.f : ml.y * w);
         o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
         m = top;
-#pragma unroll 8
+#pragma unroll kUnroll
         for (int i = 0; i < k; i++) {
             const float4 *p = reinterpret_cast<const float4 *>(__shfl_sync(0xffffffffu, (unsigned long long)src, i));
             const float wi = __shfl_sync(0xffffffffu, w, i);
@@ -224,19 +221,64 @@ __device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, flo
     }
 }
 
-// NT: N tiles (8 rows each) per warp; RW: warps that share a page and split
-// the rows; WARPS per block; STAGES units in a team's ring.
-template <int NT, int RW, int WARPS, int STAGES, int MINB>
-__global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const __grid_constant__ QuantAttnArgs a)
+// Row r of a group's queries as f16, the lane's 32 elements from 32 c on in
+// four words of eight, times the power of two that brings the row's largest
+// element into [2^14, 2^15) (zeros past the rows).  Returns what takes a raw
+// score of the row to log2 units.
+template <typename F>
+__device__ __forceinline__ float load_q(const QuantAttnArgs &a, int b, int g, int r, int c, F put)
 {
-    constexpr int TEAMS = WARPS / RW;
-    constexpr int PADROWS = NT * 8 * RW;
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = make_uint4(0, 0, 0, 0);
+    if (r < a.rows) {
+        const int qt = r / a.G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.q + (((int64_t)b * a.n_query + qt) * a.heads + g * a.G + (r - qt * a.G)) * kD + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = src[i];
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            top = max(top, x[k] & 0x7fffu);
+            top = max(top, (x[k] >> 16) & 0x7fffu);
+        }
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int shift = 14 - ((int)(top >> 7) - 127);
+    if (top == 0 || top >= 0x7f80u) shift = 0;
+    shift = shift > 126 ? 126 : shift;
+    const float up = __int_as_float((shift + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            f[k] = f16x2(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
+        put(i, f);
+    }
+    return fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
+}
+
+// NT: N tiles (8 rows each), TEAMS warps per block, STAGES units in a warp's
+// ring.  Up to 16 rows a lane keeps its part of Q in registers, beyond that in
+// shared memory (one 16-byte load per tile serves both pages of a unit).
+template <int NT, int TEAMS, int STAGES, int MINB, bool QREG>
+__global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const __grid_constant__ QuantAttnArgs a)
+{
+    constexpr int PADROWS = NT * 8;
+    constexpr int TEAM_BYTES = team_bytes(QREG ? 0 : NT, STAGES);
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
-    static_assert(PADROWS * kParkRow * 4 <= STAGES * kUnitBytes, "a parked piece fits the team's ring");
+    static_assert(PADROWS * kParkRow * 4 <= TEAM_BYTES, "a parked piece fits the warp's shared memory");
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Smem sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / RW, part = warp % RW;   // part: which rows of the group
+    const int tid = threadIdx.x, lane = tid & 31, team = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;
     const int Hkv = a.st.kv_heads;
     pdl_wait();
@@ -246,7 +288,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
     {
         const long long cap = (long long)a.table_cols * kPage;
         long long carry = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += WARPS * 32) {
+        for (int b0 = 0; b0 < a.batch; b0 += TEAMS * 32) {
             const int b = b0 + tid;
             int len = 0;
             if (b < a.batch) {
@@ -264,12 +306,12 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
                 const long long y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            if (lane == 31) sm.scan[warp] = x;
+            if (lane == 31) sm.scan[team] = x;
             __syncthreads();
             long long before = carry, all = carry;
 #pragma unroll
-            for (int w = 0; w < WARPS; w++) {
-                if (w < warp) before += sm.scan[w];
+            for (int w = 0; w < TEAMS; w++) {
+                if (w < team) before += sm.scan[w];
                 all += sm.scan[w];
             }
             if (b < a.batch) sm.pre[b] = before + x - own;
@@ -279,7 +321,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
         if (tid == 0) sm.pre[a.batch] = carry;
     }
     const uint32_t bar0 = smem_u32(&sm.bar[team * STAGES]);
-    const uint32_t ring = smem_u32(dyn) + (uint32_t)team * STAGES * kUnitBytes;
+    const uint32_t ring = smem_u32(dyn) + (uint32_t)team * TEAM_BYTES;
     if (tid == 0) {
         for (int i = 0; i < TEAMS * STAGES; i++)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" :: "r"(smem_u32(&sm.bar[i])) : "memory");
@@ -289,126 +331,126 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
     if (tid == 0) sm.nothing = make_float2(-CUDART_INF_F, 0.f);
     __syncthreads();
 
-    // the block's and the team's range of units
+    // the block's and the warp's range of units
     const long long U = sm.pre[a.batch] * Hkv;
-    // every team of an active block has work: blocks beyond that stay idle
-    const long long most = U / TEAMS > 0 ? U / TEAMS : 1;
+    // every warp of an active block has work: blocks beyond that stay idle
+    const long long most = U >= TEAMS ? U / TEAMS : 1;
     const int grid = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
     const int cta = blockIdx.x;
     if (cta >= grid) {
         if (tid == 0) a.meta[cta] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const long long teams = (long long)grid * TEAMS, me = (long long)cta * TEAMS + team;
-    const long long lo = U * me / teams, hi = U * (me + 1) / teams;
-    const long long cta_lo = U * cta / grid, cta_hi = U * (cta + 1) / grid;
-    // partial rows: the block's two crossing groups, then its teams' first pieces.  A team's last piece is parked in
-    // its own ring, which it has read to the end by then.
+    const int teams = grid * TEAMS, me = cta * TEAMS + team;
+    // the first unit of warp i of the grid, floor(U i / teams): the remainder's share fits 32 bits, and U almost always
+    const long long per = U >> 32 ? U / teams : (long long)((uint32_t)U / (uint32_t)teams);
+    const uint32_t rest = (uint32_t)(U - per * teams);
+    auto first_unit = [&](int i) { return per * i + (long long)(rest * (uint32_t)i / (uint32_t)teams); };
+    const long long lo = first_unit(me), hi = first_unit(me + 1);
+    const long long cta_lo = first_unit(cta * TEAMS), cta_hi = first_unit((cta + 1) * TEAMS);
+    // partial rows: the block's two crossing groups, then its warps' first pieces.  A warp's last piece is parked in
+    // its own shared memory, which it has read to the end by then.
     const int64_t crossing = (int64_t)cta * 2 * PADROWS;
     const int64_t park = ((int64_t)gridDim.x * 2 + (int64_t)cta * TEAMS) * PADROWS;
-
-    auto parked_o = [&](int t, int r) { return reinterpret_cast<float *>(dyn + (size_t)t * STAGES * kUnitBytes) + r * kParkRow; };
+    auto parked_o = [&](int t, int r) { return reinterpret_cast<float *>(dyn + (size_t)t * TEAM_BYTES) + r * kParkRow; };
     auto parked_ml = [&](int t, int r) { return reinterpret_cast<float2 *>(parked_o(t, r) + kD); };
 
     if (lo < hi) {
-        Cursor at = cursor_at(sm, a.batch, Hkv, lo);
-        Cursor ld = at;                 // the next unit to copy
-        long long ld_pos = lo;
-        // page of the unit `ld` stands at (lane i < kPP: its i-th page; -1: none)
-        auto page_of = [&](const Cursor &c) {
-            int id = -1;
-            const int p = c.u * kPP + lane;
-            if (lane < kPP && p * (long long)kPage < sm.len[c.b]) {
-                id = a.table[c.b * a.table_stride + p];
-                if ((unsigned)id >= (unsigned)a.st.num_pages) {
+        int left = (int)(hi - lo);      // units to go
+        int b = request_of(sm, a.batch, Hkv, lo);
+        int n_units = (int)(sm.pre[b + 1] - sm.pre[b]);
+        const long long in = lo - sm.pre[b] * Hkv;      // below Hkv * n_units
+        int g = in >> 32 ? (int)(in / n_units) : (int)((uint32_t)in / (uint32_t)n_units);
+        int u0 = (int)(in - (long long)g * n_units);
+
+        // The copies run ahead of the reading over the same units: ld_group units of (ld_b, ld_g) to go, tokens from
+        // the next unit on in the request, and the lane's page id of that unit, read one unit ahead.
+        const size_t page_stride = (size_t)Hkv * kQPageBytes;
+        int ld_left = left, ld_b = b, ld_g = g, ld_group = n_units - u0, ld_tok = sm.len[b] - u0 * kUnitTok;
+        const int32_t *ld_ids = a.table + (int64_t)b * a.table_stride + u0 * kPP + lane;
+        int next_id = 0;
+        auto fetch = [&]() {
+            next_id = 0;
+            if (lane < kPP && lane * kPage < ld_tok) {
+                next_id = *ld_ids;
+                if ((unsigned)next_id >= (unsigned)a.st.num_pages) {
                     atomicOr(a.st.err, kQErrPage);
-                    id = 0;             // stays inside the store; the request's output is wrong
+                    next_id = 0;        // stays inside the store; the request's output is wrong
                 }
             }
-            return id;
         };
-        int next_id = page_of(ld);
-        // copies the unit at `ld` into stage s and moves on; the page after it is looked up a step ahead
         auto issue = [&](int s) {
-            if (ld_pos >= hi) return;
-            const uint32_t bar = bar0 + 8 * s, dst = ring + (uint32_t)s * kUnitBytes;
-            const int id = next_id, head = ld.g;
-            const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-            step(ld, sm, a.batch, Hkv);
-            ld_pos++;
-            if (ld_pos < hi) next_id = page_of(ld);
-            if (part == 0) {
-                if (lane == 0)
-                    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n"
-                                 :: "r"(bar), "r"((uint32_t)__popc(have) * kQPageBytes)
-                                 : "memory");
-                __syncwarp();
-                if (id >= 0)
-                    bulk_load(dst + lane * kQPageBytes, a.st.pages + ((size_t)id * Hkv + head) * kQPageBytes, kQPageBytes, bar);
+            if (ld_left == 0) return;
+            const uint32_t bar = bar0 + 8 * s;
+            const int pages = ld_tok > kPage ? kPP : ld_tok > 0 ? 1 : 0;
+            if (lane == 0)
+                asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n"
+                             :: "r"(bar), "r"((uint32_t)pages * kQPageBytes)
+                             : "memory");
+            __syncwarp();
+            if (lane < pages)
+                bulk_load(ring + (uint32_t)s * kUnitBytes + lane * kQPageBytes,
+                          a.st.pages + (size_t)(unsigned)next_id * page_stride + (size_t)ld_g * kQPageBytes, kQPageBytes, bar);
+            if (--ld_left == 0) return;
+            if (--ld_group == 0) {
+                if (++ld_g == Hkv) {
+                    ld_g = 0;
+                    ld_b++;
+                }
+                ld_group = (int)(sm.pre[ld_b + 1] - sm.pre[ld_b]);
+                ld_tok = sm.len[ld_b];
+                ld_ids = a.table + (int64_t)ld_b * a.table_stride + lane;
+            } else {
+                ld_tok -= kUnitTok;
+                ld_ids += kPP;
             }
+            fetch();
         };
+        static_assert(kPP == 2, "a unit has one or two pages");
+        fetch();
 #pragma unroll
         for (int s = 0; s < STAGES; s++) issue(s);
 
         int stage = 0;
         uint32_t phase = 0;
-        long long pos = lo;
-        while (pos < hi) {
-            // one piece: units [at.u, at.u + n) of group (at.b, at.g)
-            const int b = at.b, g = at.g, n_units = at.n, u0 = at.u;
-            const int n = (int)(hi - pos < n_units - u0 ? hi - pos : n_units - u0);
+        const int tk = 4 * (g8 >> 1) + (g8 & 1);    // token of matrix row g; row g + 8 is token tk + 2
+        while (left > 0) {
+            // one piece: units [u0, u0 + n) of group (b, g)
+            const int n = min(left, n_units - u0);
             const int len = sm.len[b];
-            const int full = len - (a.n_query - 1) > 0 ? len - (a.n_query - 1) : 0;   // tokens every row sees
-            const int row0 = part * NT * 8;
-            uint32_t qf[NT][16];
-            float sc[NT][2], ref[NT][2], sum[NT][2], o[NT][8][4];
-            int lim[NT][2];
+            const int full = max(len - (a.n_query - 1), 0);     // tokens every row sees
+            uint32_t qf[QREG ? NT : 1][16];
+            float sc[NT][2], ref[NT][2], top_raw[NT][2], sum[NT][2], o[NT][8][4];
+            if (QREG) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    const float rs = load_q(a, b, g, nt * 8 + g8, c4, [&](int i, const uint32_t (&f)[4]) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) qf[nt][4 * i + k] = f[k];
+                    });
+#pragma unroll
+                    for (int h = 0; h < 2; h++) sc[nt][h] = __shfl_sync(0xffffffffu, rs, (2 * c4 + h) * 4);
+                }
+            } else {
+                const uint32_t q0 = ring + STAGES * kUnitBytes + lane * 16;
+                float rs_all = 0.f;         // lane 8 nt + g: the scale of row 8 nt + g
+#pragma unroll 1
+                for (int nt = 0; nt < NT; nt++) {
+                    const float rs = load_q(a, b, g, nt * 8 + g8, c4,
+                                            [&](int i, const uint32_t (&f)[4]) { sts16(q0 + (nt * 4 + i) * 512, f); });
+                    const float mine = __shfl_sync(0xffffffffu, rs, (lane & 7) * 4);
+                    if ((lane >> 3) == nt) rs_all = mine;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) sc[nt][h] = __shfl_sync(0xffffffffu, rs_all, nt * 8 + 2 * c4 + h);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                const int r = row0 + nt * 8 + g8;
-                float rs = 0.f;
-                uint4 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) w[i] = make_uint4(0, 0, 0, 0);
-                if (r < a.rows) {
-                    const int qt = r / a.G;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        a.q + (((int64_t)b * a.n_query + qt) * a.heads + g * a.G + (r - qt * a.G)) * kD + 32 * c4);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) w[i] = src[i];
-                }
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        top = max(top, x[k] & 0x7fffu);
-                        top = max(top, (x[k] >> 16) & 0x7fffu);
-                    }
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^shift brings the row's largest element into [2^14, 2^15)
-                int shift = 14 - ((int)(top >> 7) - 127);
-                if (top == 0 || top >= 0x7f80u) shift = 0;
-                shift = shift > 126 ? 126 : shift;
-                const float up = __int_as_float((shift + 127) << 23);
-                rs = fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        qf[nt][4 * i + k] = f16x2(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
-                }
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    const int col = 2 * c4 + h, rr = row0 + nt * 8 + col;
-                    sc[nt][h] = __shfl_sync(0xffffffffu, rs, col * 4);
-                    const int l = len - (a.n_query - 1) + rr / a.G;
-                    lim[nt][h] = rr < a.rows && l > 0 ? l : 0;
-                    ref[nt][h] = -CUDART_INF_F;
+                    ref[nt][h] = top_raw[nt][h] = -CUDART_INF_F;
                     sum[nt][h] = 0.f;
                 }
 #pragma unroll
@@ -423,76 +465,105 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
                 const int tok0 = (u0 + i) * kUnitTok;
                 const bool tail = tok0 + kUnitTok > full;
 
-                // scores
+                // scores of both pages
                 float s[kPP][NT][4];
 #pragma unroll
-                for (int pp = 0; pp < kPP; pp++) {
-                    const uint32_t page = unit + pp * kQPageBytes;
-                    const int tk = 4 * (g8 >> 1) + (g8 & 1);     // token of matrix row g; row g + 8 is token tk + 2
-                    const uint4 ka = lds16(page + tk * 64 + c4 * 16), kb = lds16(page + (tk + 2) * 64 + c4 * 16);
-                    const uint32_t sa = scales2(lds2(page + kQKScale + tk * 8 + 2 * c4));
-                    const uint32_t sb = scales2(lds2(page + kQKScale + (tk + 2) * 8 + 2 * c4));
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                for (int pp = 0; pp < kPP; pp++)
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) s[pp][nt][k] = 0.f;
+                uint32_t wa[kPP][4], wb[kPP][4], xa[kPP][2], xb[kPP][2];
 #pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        uint32_t ha[4], hb[4];
-                        unpack8(wa[w], ha);
-                        unpack8(wb[w], hb);
-                        const uint32_t xa = __byte_perm(sa, sa, w < 2 ? 0x1010 : 0x3232);
-                        const uint32_t xb = __byte_perm(sb, sb, w < 2 ? 0x1010 : 0x3232);
+                for (int pp = 0; pp < kPP; pp++) {
+                    const uint32_t page = unit + pp * kQPageBytes;
+                    const uint4 ka = lds16(page + tk * 64 + c4 * 16), kb = lds16(page + (tk + 2) * 64 + c4 * 16);
+                    wa[pp][0] = ka.x, wa[pp][1] = ka.y, wa[pp][2] = ka.z, wa[pp][3] = ka.w;
+                    wb[pp][0] = kb.x, wb[pp][1] = kb.y, wb[pp][2] = kb.z, wb[pp][3] = kb.w;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        // the scale's f16 (times 2^-8) in both halves
+                        xa[pp][h] = lds1(page + kQKScale + tk * 8 + 2 * c4 + h) * 0x00800080u;
+                        xb[pp][h] = lds1(page + kQKScale + (tk + 2) * 8 + 2 * c4 + h) * 0x00800080u;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    uint32_t ha[kPP][4], hb[kPP][4];
+#pragma unroll
+                    for (int pp = 0; pp < kPP; pp++) {
+                        unpack8(wa[pp][w], ha[pp]);
+                        unpack8(wb[pp][w], hb[pp]);
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            ha[k] = hmul2(ha[k], xa);
-                            hb[k] = hmul2(hb[k], xb);
+                            ha[pp][k] = hmul2(ha[pp][k], xa[pp][w >> 1]);
+                            hb[pp][k] = hmul2(hb[pp][k], xb[pp][w >> 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        uint32_t f[4];
+                        if (QREG) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) f[k] = qf[nt][4 * w + k];
+                        } else {
+                            const uint4 v = lds16(ring + STAGES * kUnitBytes + ((nt * 4 + w) * 32 + lane) * 16);
+                            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
                         }
 #pragma unroll
                         for (int k = 0; k < 2; k++)
 #pragma unroll
-                            for (int nt = 0; nt < NT; nt++)
-                                mma_f16(s[pp][nt], ha[2 * k], hb[2 * k], ha[2 * k + 1], hb[2 * k + 1], qf[nt][4 * w + 2 * k],
-                                        qf[nt][4 * w + 2 * k + 1]);
+                            for (int pp = 0; pp < kPP; pp++)
+                                mma_f16(s[pp][nt], ha[pp][2 * k], hb[pp][2 * k], ha[pp][2 * k + 1], hb[pp][2 * k + 1],
+                                        f[2 * k], f[2 * k + 1]);
                     }
                 }
                 if (tail) {
+                    // tokens nobody sees: their value scales may be NaN and are made zero in the ring
+                    // (lane: word (page, c, block) of the unit's scales, bytes of tokens 0, 2, 1, 3)
+#pragma unroll 1
+                    for (int k = lane; k < kPP * 32; k += 32) {
+                        const int seen = len - (tok0 + (k >> 5) * kPage + 4 * ((k >> 3) & 3));
+                        const uint32_t keep = (seen > 0 ? 0xffu : 0u) | (seen > 2 ? 0xff00u : 0u) |
+                                              (seen > 1 ? 0xff0000u : 0u) | (seen > 3 ? 0xff000000u : 0u);
+                        const uint32_t at = unit + (k >> 5) * kQPageBytes + kQVScale + (k & 31) * 4;
+                        sts4(at, lds4(at) & keep);
+                    }
+                    __syncwarp();
 #pragma unroll
-                    for (int pp = 0; pp < kPP; pp++)
+                    for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
+                        for (int h = 0; h < 2; h++) {
+                            const int r = nt * 8 + 2 * c4 + h, lim = r < a.rows ? len - (a.n_query - 1) + r / a.G : 0;
 #pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const int tok = tok0 + pp * kPage + 4 * (g8 >> 1) + (g8 & 1) + (k & 2);
-                                if (tok >= lim[nt][k & 1]) s[pp][nt][k] = -CUDART_INF_F;
-                            }
+                            for (int pp = 0; pp < kPP; pp++)
+#pragma unroll
+                                for (int k = 0; k < 2; k++)
+                                    if (tok0 + pp * kPage + tk + 2 * k >= lim) s[pp][nt][2 * k + h] = -CUDART_INF_F;
+                        }
                 }
                 // softmax: the reference moves only when a score passes it by more than the margin
+                float x[NT][2];
                 bool moves = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        float x = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
-#pragma unroll
-                        for (int pp = 1; pp < kPP; pp++) x = fmaxf(x, fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
-                        moves |= x * sc[nt][h] > ref[nt][h] + kMargin;
+                        x[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+                        moves |= x[nt][h] > top_raw[nt][h];
                     }
                 if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            float x = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
+                            float y = x[nt][h] * sc[nt][h];
 #pragma unroll
-                            for (int pp = 1; pp < kPP; pp++) x = fmaxf(x, fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
-                            x *= sc[nt][h];
-#pragma unroll
-                            for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                            const float top = fmaxf(ref[nt][h], x);
-                            const float f = ref[nt][h] == -CUDART_INF_F ? 0.f : ex2_approx(ref[nt][h] - top);
-                            ref[nt][h] = top;
+                            for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+                            y = fmaxf(ref[nt][h], y);
+                            const float f = ref[nt][h] == -CUDART_INF_F ? 0.f : ex2_approx(ref[nt][h] - y);
+                            ref[nt][h] = y;
+                            top_raw[nt][h] = (y + kMargin) / sc[nt][h];
                             sum[nt][h] *= f;
 #pragma unroll
                             for (int j = 0; j < 8; j++) {
@@ -523,18 +594,12 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
 #pragma unroll
                 for (int pp = 0; pp < kPP; pp++) {
                     const uint32_t page = unit + pp * kQPageBytes;
-                    uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
-                    if (tail) {
-                        // tokens nobody sees: their scales may be NaN
-                        const int left = len - (tok0 + pp * kPage + 4 * c4);
-                        keep01 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-                        keep23 = (left > 2 ? 0xffffu : 0u) | (left > 3 ? 0xffff0000u : 0u);
-                    }
+                    const uint32_t sv = lds4(page + kQVScale + c4 * 32 + g8 * 4);
+                    // f16 pairs of the scales of tokens 0, 1 and 2, 3, times 2^-8
+                    const uint32_t s01 = (sv & 0x00ff00ffu) << 7, s23 = (sv & 0xff00ff00u) >> 1;
 #pragma unroll
                     for (int w = 0; w < 2; w++) {
                         const uint4 t = lds16(page + kQV + w * 512 + lane * 16);
-                        const uint4 sv = lds16(page + kQVScale + c4 * 32 + w * 16);
-                        const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
                         uint32_t a0[4], a1[4], a2[4], a3[4];
                         unpack8((t.x & 0x0f0f0f0fu) | ((t.y << 4) & 0xf0f0f0f0u), a0);
                         unpack8(((t.x >> 4) & 0x0f0f0f0fu) | (t.y & 0xf0f0f0f0u), a1);
@@ -542,7 +607,6 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
                         unpack8(((t.z >> 4) & 0x0f0f0f0fu) | (t.w & 0xf0f0f0f0u), a3);
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const uint32_t s01 = scales2(sw[j]) & keep01, s23 = scales2(sw[j] >> 16) & keep23;
                             const uint32_t v0 = hmul2(a0[j], s01), v1 = hmul2(a1[j], s01), v2 = hmul2(a2[j], s23),
                                            v3 = hmul2(a3[j], s23);
 #pragma unroll
@@ -551,18 +615,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
                         }
                     }
                 }
-                // the stage is free once the team has read it
-                if (RW > 1) named_bar(1 + team, RW * 32);
-                else __syncwarp();
+                __syncwarp();       // the stage is free once the warp has read it
                 issue(stage);
                 if (++stage == STAGES) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
-            pos += n;
-            at.u = u0 + n - 1;
-            step(at, sm, a.batch, Hkv);
+            left -= n;
 
             // the piece's sums over its tokens
 #pragma unroll
@@ -572,37 +632,46 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) sum[nt][h] += __shfl_xor_sync(0xffffffffu, sum[nt][h], off);
                 }
-            const bool whole = u0 == 0 && n == n_units;
-            const int which = u0 + n == n_units ? 0 : 1;    // continues to the next team: the team's last piece
-            if (!whole && part == 0 && lane == 0) sm.piece_group[2 * team + which] = b * Hkv + g;
+            const bool ends = u0 + n == n_units, whole = u0 == 0 && ends;
+            const int which = ends ? 0 : 1;     // 1: the group runs on into the next warp's range
+            if (!whole && lane == 0) sm.piece_group[2 * team + which] = b * Hkv + g;
+            if (which) __syncwarp();            // the parked piece takes the place of what the warp has read
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    const int r = row0 + nt * 8 + 2 * c4 + h;
+                    const int r = nt * 8 + 2 * c4 + h;
                     if (r >= a.rows) continue;
                     const float l = sum[nt][h];
                     if (whole) {
                         const int qt = r / a.G;
                         const int64_t row = ((int64_t)b * a.n_query + qt) * a.heads + g * a.G + (r - qt * a.G);
-                        const float inv = l == 0.f ? 0.f : a.st.v_scale / l;
+                        const float inv = l == 0.f ? 0.f : a.v_out_scale / l;
+                        uint32_t y[8];
 #pragma unroll
-                        for (int j = 0; j < 8; j++) {
-                            const float x = l == 0.f ? 0.f : o[nt][j][h] * inv, y = l == 0.f ? 0.f : o[nt][j][2 + h] * inv;
-                            *reinterpret_cast<uint32_t *>(a.out + row * kD + 16 * j + 2 * g8) =
-                                bf16x2_bits(__floats2bfloat162_rn(x, y));
-                        }
+                        for (int j = 0; j < 8; j++)
+                            y[j] = l == 0.f ? 0u : bf16x2_bits(__floats2bfloat162_rn(o[nt][j][h] * inv, o[nt][j][2 + h] * inv));
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * kD + 16 * g8);
+                        dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                        dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
                         if (a.lse && g8 == 0)
                             a.lse[row] = l == 0.f ? -CUDART_INF_F : (ref[nt][h] - kPShift + log2f(l)) * kLn2;
                     } else {
                         const int64_t row = park + (int64_t)team * PADROWS + r;
                         float *dst = which ? parked_o(team, r) : a.part_o + row * kD;
 #pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            *reinterpret_cast<float2 *>(dst + 16 * j + 2 * g8) = make_float2(o[nt][j][h], o[nt][j][2 + h]);
+                        for (int j = 0; j < 8; j += 2)
+                            *reinterpret_cast<float4 *>(dst + 16 * g8 + 2 * j) =
+                                make_float4(o[nt][j][h], o[nt][j][2 + h], o[nt][j + 1][h], o[nt][j + 1][2 + h]);
                         if (g8 == 0) *(which ? parked_ml(team, r) : a.part_ml + row) = make_float2(ref[nt][h] - kPShift, l);
                     }
                 }
+            // the next group
+            u0 = 0;
+            if (++g == Hkv) {
+                g = 0;
+                if (++b < a.batch) n_units = (int)(sm.pre[b + 1] - sm.pre[b]);
+            }
         }
     }
     __threadfence_block();
@@ -625,12 +694,16 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) quant_attention_kernel(const
         const int slot = start < cta_lo ? 0 : 1;
         if (!whole && slot == 1) {
             owner = grp;
-            owner_last = (int)((end * grid - 1) / U);
+            // the block that holds the group's last unit: a float guess, put right by the exact ranges
+            int c = min(grid - 1, (int)((float)(end - 1) / (float)U * (float)grid));
+            while (first_unit(c * TEAMS) >= end) c--;
+            while (first_unit((c + 1) * TEAMS) < end) c++;
+            owner_last = c;
         }
-        for (int r = warp; r < a.rows; r += WARPS) {
+        for (int r = team; r < a.rows; r += TEAMS) {
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             float m = -CUDART_INF_F, l = 0.f;
-            merge_rows<false>(j - i, [&](int k, const float2 *&ml, const float4 *&src) {
+            merge_rows<false, 2>(j - i, [&](int k, const float2 *&ml, const float4 *&src) {
                 const int t = (i + k) >> 1;
                 const int64_t row = park + (int64_t)t * PADROWS + r;
                 const bool last = (i + k) & 1;
@@ -667,7 +740,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -CUDART_INF_F, l = 0.f;
     // warp w takes partials w, w + 4, ...; then lane w of warp 0 the four warps' results
-    merge_rows<true>((n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
+    merge_rows<true, 8>((n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
         const int k = i * kCombineWarps + warp;
         const int64_t row = ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r;
         ml = a.part_ml + row;
@@ -680,7 +753,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
     o = make_float4(0.f, 0.f, 0.f, 0.f);
     m = -CUDART_INF_F;
     l = 0.f;
-    merge_rows<false>(kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
+    merge_rows<false, 1>(kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
         ml = &sml[i];
         src = so[i];
     }, lane, o, m, l);
@@ -690,23 +763,24 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
 
 struct Variant {
     void (*kernel)(QuantAttnArgs);
-    int teams, padrows, threads, blocks_per_sm;
+    int teams, padrows, blocks_per_sm;
     size_t smem;
 };
 
-// rows 1..8, 9..16, 17..32
-template <int NT, int RW, int WARPS, int STAGES, int MINB>
+template <int NT, int TEAMS, int STAGES, int MINB, bool QREG>
 Variant variant()
 {
-    return {quant_attention_kernel<NT, RW, WARPS, STAGES, MINB>, WARPS / RW, NT * 8 * RW, WARPS * 32, MINB,
-            (size_t)(WARPS / RW) * STAGES * kUnitBytes};
+    return {quant_attention_kernel<NT, TEAMS, STAGES, MINB, QREG>, TEAMS, NT * 8, MINB,
+            (size_t)TEAMS * team_bytes(QREG ? 0 : NT, STAGES)};
 }
 
+// As many warps as the registers of an output tile of 8 NT rows leave room for.
 Variant variant_for(int rows)
 {
-    if (rows <= 8) return variant<1, 1, 8, 2, 2>();
-    if (rows <= 16) return variant<2, 1, 12, 3, 1>();
-    return variant<2, 2, 12, 4, 1>();
+    if (rows <= 8) return variant<1, 8, 2, 2, true>();
+    if (rows <= 16) return variant<2, 12, 3, 1, true>();
+    if (rows <= 24) return variant<3, 8, 3, 1, false>();
+    return variant<4, 8, 3, 1, false>();
 }
 
 int grid_of(const Variant &v, int sm_count)
@@ -721,7 +795,7 @@ int grid_of(const Variant &v, int sm_count)
 
 cudaError_t quant_attention_config(int sm_count)
 {
-    const int rows[3] = {8, 16, 32};
+    const int rows[4] = {8, 16, 24, 32};
     for (int r : rows) {
         const Variant v = variant_for(r);
         const cudaError_t e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)v.smem);
@@ -735,7 +809,7 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, int sm_count, cudaStr
 {
     const Variant v = variant_for(a.rows);
     const int grid = grid_of(v, sm_count);
-    cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, s, true, a);
+    cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.teams * 32), v.smem, s, true, a);
     if (e != cudaSuccess) return e;
     return launch_maybe_pdl(quant_combine_kernel, dim3(grid, a.rows), dim3(kCombineWarps * 32), 0, s, true, a, v.padrows);
 }

@@ -147,11 +147,11 @@ def test_store_layout_covers_a_page_once():
         for e in range(128):
             j, c, tt = e // 16, tok // 4, tok % 4
             nib.setdefault(2 * (tok * 64 + e // 2) + e % 2, []).append(("k", tok, e))
-            g = e % 16 // 2
-            byte = 1152 + (j // 4) * 512 + (g * 4 + c) * 16 + tt * 4 + j % 4
+            i = e % 16 // 2
+            byte = 1152 + (i // 4) * 512 + (j * 4 + c) * 16 + tt * 4 + i % 4
             nib.setdefault(2 * byte + e % 2, []).append(("v", tok, e))
             scale.setdefault(1024 + tok * 8 + j, set()).add(("k", tok, j))
-            scale.setdefault(2176 + c * 32 + j * 4 + tt, set()).add(("v", tok, j))
+            scale.setdefault(2176 + c * 32 + j * 4 + (0, 2, 1, 3)[tt], set()).add(("v", tok, j))
     assert all(len(x) == 1 for x in nib.values()) and all(len(x) == 1 for x in scale.values())
     assert sorted(nib) == list(range(0, 2 * 1024)) + list(range(2 * 1152, 2 * 2176))
     assert sorted(scale) == list(range(1024, 1152)) + list(range(2176, 2304))
@@ -166,7 +166,10 @@ def test_store_layout_covers_a_page_once():
                     assert nib[2 * (tok * 64 + c * 16 + i) + h] == [("k", tok, 32 * c + 2 * i + h)]
         for w in range(2):
             for tt in range(4):
-                for i in range(4):                               # V word tt of load w, byte i: block 4 w + i
+                for i in range(4):                               # V word tt of load w, byte i: elements of block g
                     for h in range(2):
                         at = 1152 + w * 512 + lane * 16 + tt * 4 + i
-                        assert nib[2 * at + h] == [("v", 4 * c + tt, 16 * (4 * w + i) + 2 * g + h)]
+                        assert nib[2 * at + h] == [("v", 4 * c + tt, 16 * g + 8 * w + 2 * i + h)]
+        # the word of value scales that the lane loads: its block, its four tokens in the order 0, 2, 1, 3
+        for k, tt in enumerate((0, 2, 1, 3)):
+            assert scale[2176 + c * 32 + g * 4 + k] == {("v", 4 * c + tt, g)}
