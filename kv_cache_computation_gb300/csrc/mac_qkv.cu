@@ -17,14 +17,19 @@
 // pos * turns[i] mod 2^64 drops the whole turns exactly for any position.
 //
 // What bounds it: many tokens, the memory (256 B in and 256 to 512 B out per
-// row, nothing read twice); few tokens, the launch and one round trip.  A
-// half-warp owns a row: lane l holds the two 4-element chunks whose elements
+// row, nothing read twice); few tokens, the launch and one round trip.  A row
+// belongs to 8 (or 16) lanes: a lane holds the two chunks whose elements
 // rotate with each other, so the rotation needs no shuffle and the mean of
-// squares four.  A block takes kTile tokens and first makes their sines and
-// cosines (one sincospi per thread for four tokens), which all their heads
-// share.  Few tokens spread over more blocks (gridDim.y splits a token's
-// rows), so that each half-warp has one to three rows and one token's latency
-// is a single row's.
+// squares three or four.  A block takes four tokens and first makes their
+// sines and cosines (one sincospi per thread), which all their heads share; a
+// thread stays with one token and keeps its part in registers.  Few tokens
+// spread over more blocks (gridDim.y splits a token's rows), so that each row of
+// lanes has one to three rows and one token's latency is a single row's.
+// Measured, 32 over 8 heads with norms and pre-rotation queries: 1 token 2.1 us,
+// 37 tokens 2.2, 600 tokens 4.0 (in a captured graph); 32768 tokens 177 us, 6.06
+// TB/s.  8-byte chunks with the sines read from shared memory per row took 195 us;
+// two rows in flight per lane at three blocks per SM beat one (190 us), three
+// (182, two blocks) and six (245).
 #include "../../include/mac.h"
 #include "mac_device.cuh"
 
@@ -37,9 +42,8 @@ namespace macgpu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowLanes = 16;                       // lanes per row
-constexpr int kRows = kThreads / kRowLanes;         // rows a block works on at once
 constexpr int kPairs = kD / 2;
+constexpr int kTileTokens = 608;                    // from here on a block takes four tokens
 
 struct QkvArgs {
     const __nv_bfloat16 *q, *k, *v;
@@ -56,30 +60,64 @@ struct Turns {
     uint64_t t[kPairs];
 };
 
-__device__ __forceinline__ uint2 load8(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+// W (4 or 8) bf16 elements as W / 2 words
+template <int W>
+struct Chunk {
+    uint32_t w[W / 2];
+};
 
-__device__ __forceinline__ void unpack4(uint2 u, float (&x)[4])
+template <int W>
+__device__ __forceinline__ Chunk<W> load(const __nv_bfloat16 *p)
 {
-    x[0] = __uint_as_float(u.x << 16);
-    x[1] = __uint_as_float(u.x & 0xffff0000u);
-    x[2] = __uint_as_float(u.y << 16);
-    x[3] = __uint_as_float(u.y & 0xffff0000u);
+    Chunk<W> c;
+    if (W == 8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        c.w[0] = u.x, c.w[1] = u.y, c.w[W / 2 - 2] = u.z, c.w[W / 2 - 1] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        c.w[0] = u.x, c.w[1] = u.y;
+    }
+    return c;
 }
 
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4])
+template <int W>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const Chunk<W> &c)
 {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2_bits(__floats2bfloat162_rn(x[0], x[1])),
-                                               bf16x2_bits(__floats2bfloat162_rn(x[2], x[3])));
+    if (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(c.w[0], c.w[1], c.w[W / 2 - 2], c.w[W / 2 - 1]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(c.w[0], c.w[1]);
 }
 
-// Rows of kBatch half-warp turns are loaded together before the first is used.
-template <int kTile, int kBatch>
-__global__ void __launch_bounds__(kThreads) qkv_norm_rope_kernel(const __grid_constant__ QkvArgs a,
+template <int W>
+__device__ __forceinline__ void unpack(const Chunk<W> &c, float (&x)[W])
+{
+#pragma unroll
+    for (int i = 0; i < W / 2; i++) {
+        x[2 * i] = __uint_as_float(c.w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(c.w[i] & 0xffff0000u);
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&x)[W])
+{
+    Chunk<W> c;
+#pragma unroll
+    for (int i = 0; i < W / 2; i++) c.w[i] = bf16x2_bits(__floats2bfloat162_rn(x[2 * i], x[2 * i + 1]));
+    store<W>(p, c);
+}
+
+// LANES lanes own a row, a lane two chunks of W = 64 / LANES elements.  The
+// block's kTile tokens share its rows of lanes evenly, so a thread stays with
+// one token and keeps its sines and cosines in registers.  kBatch rows are
+// loaded together before the first is used.
+template <int LANES, int kTile, int kBatch, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_kernel(const __grid_constant__ QkvArgs a,
                                                                  const __grid_constant__ Turns turns)
 {
+    constexpr int W = kPairs / LANES, kPer = kThreads / LANES / kTile;   // kPer: rows of a token worked on at once
     __shared__ float2 cs[kTile][kPairs];
     pdl_wait();
-    const int lane = threadIdx.x % kRowLanes, unit = threadIdx.x / kRowLanes;
+    const int lane = threadIdx.x % LANES, unit = threadIdx.x / LANES;
     const int t0 = blockIdx.x * kTile;
     const int pairs = a.rotary >> 1;
     for (int i = threadIdx.x; i < kTile * kPairs; i += kThreads) {
@@ -93,92 +131,75 @@ __global__ void __launch_bounds__(kThreads) qkv_norm_rope_kernel(const __grid_co
         cs[t][j] = make_float2(c, s);
     }
     // the lane's two chunks of a row, and whether they rotate
-    int da, db;
-    const bool turn = lane < (a.rotary >> 3);
-    if (a.interleaved) {
-        da = 8 * lane;
-        db = da + 4;
-    } else if (turn) {
-        da = 4 * lane;
-        db = da + pairs;
-    } else {
-        da = a.rotary + 4 * (lane - (a.rotary >> 3));
-        db = da + ((kD - a.rotary) >> 1);
-    }
-    float wqa[4], wqb[4], wka[4], wkb[4];
-    if (a.wq) {
-        unpack4(load8(a.wq + da), wqa);
-        unpack4(load8(a.wq + db), wqb);
-    }
-    if (a.wk) {
-        unpack4(load8(a.wk + da), wka);
-        unpack4(load8(a.wk + db), wkb);
-    }
+    const int turning = a.rotary / (2 * W);       // lanes that rotate
+    const bool turn = lane < turning;
+    const int da = a.interleaved ? 2 * W * lane : turn ? W * lane : a.rotary + W * (lane - turning);
+    const int db = da + (a.interleaved ? W : turn ? pairs : (kD - a.rotary) >> 1);
+    Chunk<W> wqa{}, wqb{}, wka{}, wkb{};
+    if (a.wq) wqa = load<W>(a.wq + da), wqb = load<W>(a.wq + db);
+    if (a.wk) wka = load<W>(a.wk + da), wkb = load<W>(a.wk + db);
     __syncthreads();
 
-    const int tokens = min(kTile, a.n_tokens - t0);
-    const int total = tokens * a.rows;
-    const int step = kRows * gridDim.y;
-    for (int base = blockIdx.y * kRows + unit; base - unit < total; base += step * kBatch) {
-        uint2 ra[kBatch], rb[kBatch];
-        int tok[kBatch], row[kBatch];
+    const int t = unit / kPer, tok = t0 + t;
+    float2 rot[W];
+#pragma unroll
+    for (int j = 0; j < W; j++) rot[j] = turn ? cs[t][W * lane + j] : make_float2(1.f, 0.f);
+    const int total = tok < a.n_tokens ? a.rows : 0;
+    const int step = kPer * gridDim.y, first = blockIdx.y * kPer + unit % kPer;
+    // every lane of a warp takes part in every turn of the loop (the shuffles): it runs for the block's first row
+    for (int base = 0; base + blockIdx.y * kPer < a.rows; base += step * kBatch) {
+        Chunk<W> ra[kBatch], rb[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; i++) {
-            const int it = base + i * step;
-            tok[i] = -1;
-            ra[i] = rb[i] = make_uint2(0, 0);
-            if (it < total) {
-                const int t = kTile == 1 ? 0 : it / a.rows;
-                tok[i] = t0 + t;
-                row[i] = it - t * a.rows;
-                const int r = row[i];
-                const __nv_bfloat16 *p = r < a.H           ? a.q + tok[i] * a.q_stride + (int64_t)r * kD
-                                         : r < a.H + a.Hkv ? a.k + tok[i] * a.k_stride + (int64_t)(r - a.H) * kD
-                                                           : a.v + tok[i] * a.v_stride + (int64_t)(r - a.H - a.Hkv) * kD;
-                ra[i] = load8(p + da);
-                rb[i] = load8(p + db);
+            const int r = first + base + i * step;
+            ra[i] = rb[i] = Chunk<W>{};
+            if (r < total) {
+                const __nv_bfloat16 *p = r < a.H           ? a.q + tok * a.q_stride + (int64_t)r * kD
+                                         : r < a.H + a.Hkv ? a.k + tok * a.k_stride + (int64_t)(r - a.H) * kD
+                                                           : a.v + tok * a.v_stride + (int64_t)(r - a.H - a.Hkv) * kD;
+                ra[i] = load<W>(p + da);
+                rb[i] = load<W>(p + db);
             }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; i++) {
-            const int r = row[i];
-            const bool live = tok[i] >= 0;
-            float x[4], y[4];
-            unpack4(ra[i], x);
-            unpack4(rb[i], y);
+            const int r = first + base + i * step;
+            const bool live = r < total;
+            float x[W], y[W];
+            unpack<W>(ra[i], x);
+            unpack<W>(rb[i], y);
             float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; j++) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+            for (int j = 0; j < W; j++) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
 #pragma unroll
-            for (int o = kRowLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (!live) continue;
-            if (r >= a.H + a.Hkv) {
-                __nv_bfloat16 *o = a.v_out + ((int64_t)tok[i] * a.Hkv + (r - a.H - a.Hkv)) * kD;
-                *reinterpret_cast<uint2 *>(o + da) = ra[i];
-                *reinterpret_cast<uint2 *>(o + db) = rb[i];
-                continue;
-            }
-            const bool is_q = r < a.H;
-            const __nv_bfloat16 *w = is_q ? a.wq : a.wk;
-            if (w) {
-                const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
+            for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (live && r >= a.H + a.Hkv) {
+                __nv_bfloat16 *o = a.v_out + ((int64_t)tok * a.Hkv + (r - a.H - a.Hkv)) * kD;
+                store<W>(o + da, ra[i]);
+                store<W>(o + db, rb[i]);
+            } else if (live) {
+                const bool is_q = r < a.H;
+                if (is_q ? a.wq != nullptr : a.wk != nullptr) {
+                    const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
+                    float wa[W], wb[W];
+                    unpack<W>(is_q ? wqa : wka, wa);
+                    unpack<W>(is_q ? wqb : wkb, wb);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    x[j] *= inv * (is_q ? wqa[j] : wka[j]);
-                    y[j] *= inv * (is_q ? wqb[j] : wkb[j]);
+                    for (int j = 0; j < W; j++) {
+                        x[j] *= inv * wa[j];
+                        y[j] *= inv * wb[j];
+                    }
                 }
-            }
-            const int64_t at = is_q ? ((int64_t)tok[i] * a.H + r) * kD : ((int64_t)tok[i] * a.Hkv + (r - a.H)) * kD;
-            if (is_q && a.q_pre) {
-                store4(a.q_pre + at + da, x);
-                store4(a.q_pre + at + db, y);
-            }
-            if (turn) {
-                const float2 *c = &cs[kTile == 1 ? 0 : tok[i] - t0][4 * lane];
+                const int64_t at =
+                    is_q ? ((int64_t)tok * a.H + r) * kD : ((int64_t)tok * a.Hkv + (r - a.H)) * kD;
+                if (is_q && a.q_pre) {
+                    put<W>(a.q_pre + at + da, x);
+                    put<W>(a.q_pre + at + db, y);
+                }
                 if (a.interleaved) {
 #pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const float2 c0 = c[j], c1 = c[j + 2];
+                    for (int j = 0; j < W / 2; j++) {
+                        const float2 c0 = rot[j], c1 = rot[j + W / 2];
                         const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
                         x[2 * j] = x0 * c0.x - x1 * c0.y;
                         x[2 * j + 1] = x1 * c0.x + x0 * c0.y;
@@ -187,17 +208,16 @@ __global__ void __launch_bounds__(kThreads) qkv_norm_rope_kernel(const __grid_co
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float2 c0 = c[j];
+                    for (int j = 0; j < W; j++) {
                         const float x0 = x[j], y0 = y[j];
-                        x[j] = x0 * c0.x - y0 * c0.y;
-                        y[j] = y0 * c0.x + x0 * c0.y;
+                        x[j] = x0 * rot[j].x - y0 * rot[j].y;
+                        y[j] = y0 * rot[j].x + x0 * rot[j].y;
                     }
                 }
+                __nv_bfloat16 *o = (is_q ? a.q_post : a.k_out) + at;
+                put<W>(o + da, x);
+                put<W>(o + db, y);
             }
-            __nv_bfloat16 *o = (is_q ? a.q_post : a.k_out) + at;
-            store4(o + da, x);
-            store4(o + db, y);
         }
     }
 }
@@ -275,14 +295,17 @@ extern "C" mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, cons
     for (int i = 0; i < kPairs; i++) t.t[i] = rope->turns[i];
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (n_tokens < 608) {
+    if (n_tokens < kTileTokens) {
         // few tokens: one to a block, its rows over as many blocks as keep the grid near four blocks per SM
-        int split = 608 / n_tokens;
-        const int most = (a.rows + kRows - 1) / kRows;
+        int split = kTileTokens / n_tokens;
+        const int most = (a.rows + 15) / 16;
         split = split < 1 ? 1 : split > most ? most : split;
-        e = launch_maybe_pdl(qkv_norm_rope_kernel<1, 3>, dim3(n_tokens, split), dim3(kThreads), 0, s, true, a, t);
+        e = launch_maybe_pdl(qkv_norm_rope_kernel<16, 1, 3, 4>, dim3(n_tokens, split), dim3(kThreads), 0, s, true, a, t);
+    } else if (a.rotary % 16 == 0) {
+        e = launch_maybe_pdl(qkv_norm_rope_kernel<8, 4, 2, 3>, dim3((n_tokens + 3) / 4), dim3(kThreads), 0, s, true, a, t);
     } else {
-        e = launch_maybe_pdl(qkv_norm_rope_kernel<4, 4>, dim3((n_tokens + 3) / 4), dim3(kThreads), 0, s, true, a, t);
+        // 16-byte chunks would hold elements that rotate and elements that do not
+        e = launch_maybe_pdl(qkv_norm_rope_kernel<16, 4, 2, 3>, dim3((n_tokens + 3) / 4), dim3(kThreads), 0, s, true, a, t);
     }
     return e == cudaSuccess ? MAC_OK : MAC_ERR_CUDA;
 }

@@ -5,11 +5,11 @@
 // Append, per block of 16 elements x of a head (all exact in fp32 but the two
 // roundings the format itself makes):
 //   s = e4m3(max|x| / 6), code_i = e2m1(x_i / s)
-// The quotient is formed as x * (1 / s) and then rounded to a multiple of
-// 2^-13 before the conversion.  A tie between two e2m1 values is
-// x = t s with t in {0.25, ..., 5}; x has 8 significant bits and t s at most 7,
-// so a quotient that is no tie is off it by at least 2^-9 of it (2^-11), while
-// x * (1 / s) is within 2^-22 of it: the rounding puts ties back on the tie and
+// The quotient is formed as x * (1 / s), rounded to a multiple of 2^-13 before
+// the conversion.  A tie between two e2m1 values is x = t s with t in {0.25,
+// ..., 5}; x has 8 significant bits and t s at most 7, so a quotient that is no
+// tie is off it by at least 2^-9 of it (2^-11), while x * (1 / s) is within
+// 2^-22 of it: the rounding puts ties back on the tie and
 // moves nothing across one.  A division per element would cost more than the
 // rest of the kernel together.
 #include "../../include/mac.h"
@@ -30,6 +30,7 @@ namespace macgpu {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kQuadTokens = 512;    // from here on a lane takes four tokens: below, one block per lane spreads further
 
 // two e2m1 codes (lo in the low four bits) of two floats, ties to even, at most 6
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
@@ -59,29 +60,40 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
 // eight bytes of codes.  inv: 1 / the store's global scale.
 __device__ __forceinline__ void quantise(const uint4 (&u)[2], float inv, uint32_t &scale, uint2 &codes)
 {
-    const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-    uint32_t top = 0;   // largest magnitude pattern: its order is that of the magnitudes, NaN above infinity
+    uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    // largest magnitude pattern: its order is that of the magnitudes, NaN above infinity
+    uint32_t m[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        top = max(top, w[i] & 0x7fffu);
-        top = max(top, (w[i] >> 16) & 0x7fffu);
-    }
+    for (int i = 0; i < 8; i++) m[i] = w[i] & 0x7fff7fffu;
+    const uint32_t two = __vimax3_s16x2(__vimax3_s16x2(m[0], m[1], m[2]), __vimax3_s16x2(m[3], m[4], m[5]),
+                                        __vmaxs2(m[6], m[7]));
+    const uint32_t top = max(two & 0xffffu, two >> 16);
     scale = 0xff;       // NaN
     codes = make_uint2(0, 0);
     if (top >= 0x7f80u) return;
-    scale = to_e4m3(__uint_as_float(top << 16) * inv / 6.f);
+    const float want = __uint_as_float(top << 16) * inv / 6.f;
+    scale = to_e4m3(want);
     if (scale == 0) return;
-    // 1 / s of an e4m3 value s
     const uint32_t sh = e4m3x2_to_f16x2(scale);
-    const float r = inv / __low2float(*reinterpret_cast<const __half2 *>(&sh));
+    const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh));
+    const float r = inv / s;
+    if (want > 500.f) {
+        // the scale has saturated: what lies beyond 8 s, and ends as 6 s, could leave the range of the rounding below
+        const __nv_bfloat162 lim = __float2bfloat162_rn(8.f * s / inv);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+            w[i] = bf16x2_bits(__hmax2(__hmin2(x, lim), __hneg2(lim)));
+        }
+    }
     uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        // + 1.5 x 2^10 - 1.5 x 2^10: to a multiple of 2^-13 (|x / s| is below 2^9: s is at least 15/16 of max / 6,
-        // or half of it among the smallest scales, unless the scale saturates; then anything beyond 6 ends as 6)
-        const float lo = fminf(fmaxf(__uint_as_float(w[i] << 16) * r, -8.f), 8.f);
-        const float hi = fminf(fmaxf(__uint_as_float(w[i] & 0xffff0000u) * r, -8.f), 8.f);
-        b[i] = to_e2m1x2(__fsub_rn(__fadd_rn(lo, 1536.f), 1536.f), __fsub_rn(__fadd_rn(hi, 1536.f), 1536.f));
+        // x / s to a multiple of 2^-13: an fma onto 1.5 x 2^10, whose last bit that is, and back (|x / s| is at most 12:
+        // s is at least 15/16 of max / 6, or half of it among the smallest scales)
+        const float lo = __fsub_rn(__fmaf_rn(__uint_as_float(w[i] << 16), r, 1536.f), 1536.f);
+        const float hi = __fsub_rn(__fmaf_rn(__uint_as_float(w[i] & 0xffff0000u), r, 1536.f), 1536.f);
+        b[i] = to_e2m1x2(lo, hi);
     }
     codes.x = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
     codes.y = b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24;
@@ -97,41 +109,28 @@ struct MoveArgs {
     int n_tokens;
 };
 
-// One row (token, K or V, head) per eight lanes, one block of 16 per lane.
-__global__ void __launch_bounds__(kThreads) quant_append_kernel(const __grid_constant__ MoveArgs a)
+// Writes one block of one token: eight bytes of codes and the scale byte.
+__device__ __forceinline__ void put_block(uint8_t *page, bool is_v, int tok, int j, uint2 codes, uint32_t scale)
 {
-    pdl_wait();
-    const int j = threadIdx.x & 7;
-    const int Hkv = a.st.kv_heads;
-    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
-    const bool in = row < a.rows;
-    const int h = in ? (int)(row % Hkv) : 0;
-    const int64_t r2 = in ? row / Hkv : 0;
-    const bool is_v = r2 & 1;
-    const int t = (int)(r2 >> 1);
-    const int slot = in ? a.slots[t] : -1;
-    bool ok = slot >= 0;
-    if (ok && slot / kPage >= a.st.num_pages) {
-        ok = false;
-        if (j == 0) atomicOr(a.st.err, kQErrSlot);
-    }
-    if (!ok) return;
-    uint32_t scale;
-    uint2 codes;
-    const __nv_bfloat16 *x = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * kD + j * kQBlock;
-    const uint4 u[2] = {reinterpret_cast<const uint4 *>(x)[0], reinterpret_cast<const uint4 *>(x)[1]};
-    quantise(u, is_v ? a.st.v_inv : a.st.k_inv, scale, codes);
-    uint8_t *page = a.st.pages + ((size_t)(slot / kPage) * Hkv + h) * kQPageBytes;
-    const int tok = slot % kPage;
     if (!is_v) {
         *reinterpret_cast<uint2 *>(page + tok * (kD / 2) + j * 8) = codes;
-        page[kQKScale + tok * kQBlocks + j] = (uint8_t)scale;
+        page[q_kscale_at(tok, j)] = (uint8_t)scale;
     } else {
-        const int c = tok >> 2, tt = tok & 3;
-        uint8_t *p = page + kQV + (j * 4 + c) * 16 + tt * 4;
-        *reinterpret_cast<uint32_t *>(p) = codes.x;
-        *reinterpret_cast<uint32_t *>(p + 512) = codes.y;
-        page[kQVScale + c * 32 + j * 4 + q_scale_byte(tt)] = (uint8_t)scale;
+        *reinterpret_cast<uint32_t *>(page + q_v_at(tok, j, 0)) = codes.x;
+        *reinterpret_cast<uint32_t *>(page + q_v_at(tok, j, 1)) = codes.y;
+        page[q_vscale_at(tok, j)] = (uint8_t)scale;
+    }
+}
+
+__device__ __forceinline__ void get_block(const uint8_t *page, bool is_v, int tok, int j, uint2 &codes, uint32_t &scale)
+{
+    if (!is_v) {
+        codes = *reinterpret_cast<const uint2 *>(page + tok * (kD / 2) + j * 8);
+        scale = page[q_kscale_at(tok, j)];
+    } else {
+        codes = make_uint2(*reinterpret_cast<const uint32_t *>(page + q_v_at(tok, j, 0)),
+                           *reinterpret_cast<const uint32_t *>(page + q_v_at(tok, j, 1)));
+        scale = page[q_vscale_at(tok, j)];
     }
 }
 
@@ -150,49 +149,152 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h, float s)
     return bf16x2_bits(__floats2bfloat162_rn(f.x * s, f.y * s));
 }
 
-__global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_constant__ MoveArgs a)
+// A block's sixteen values as bf16.
+__device__ __forceinline__ void write_block(__nv_bfloat16 *out, uint2 codes, uint32_t scale, float global)
 {
-    pdl_wait();
-    const int j = threadIdx.x & 7;
-    const int Hkv = a.st.kv_heads;
-    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
-    const bool in = row < a.rows;
-    const int h = in ? (int)(row % Hkv) : 0;
-    const int64_t r2 = in ? row / Hkv : 0;
-    const bool is_v = r2 & 1;
-    const int t = (int)(r2 >> 1);
-    const int slot = in ? a.slots[t] : -1;
-    bool ok = slot >= 0;
-    if (ok && slot / kPage >= a.st.num_pages) {
-        ok = false;
-        if (j == 0) atomicOr(a.st.err, kQErrSlot);
-    }
-    uint32_t scale = 0;
-    uint2 codes = make_uint2(0, 0);
-    if (ok) {
-        const uint8_t *page = a.st.pages + ((size_t)(slot / kPage) * Hkv + h) * kQPageBytes;
-        const int tok = slot % kPage;
-        if (!is_v) {
-            codes = *reinterpret_cast<const uint2 *>(page + tok * (kD / 2) + j * 8);
-            scale = page[kQKScale + tok * kQBlocks + j];
-        } else {
-            const int c = tok >> 2, tt = tok & 3;
-            const uint8_t *p = page + kQV + (j * 4 + c) * 16 + tt * 4;
-            codes = make_uint2(*reinterpret_cast<const uint32_t *>(p), *reinterpret_cast<const uint32_t *>(p + 512));
-            scale = page[kQVScale + c * 32 + j * 4 + q_scale_byte(tt)];
-        }
-    }
-    if (!in) return;
     const uint32_t sh = e4m3x2_to_f16x2(scale);
-    const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * (is_v ? a.st.v_scale : a.st.k_scale);
+    const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * global;
     uint32_t x[4], y[4];
     e2m1x8_to_f16(codes.x, x);
     e2m1x8_to_f16(codes.y, y);
-    __nv_bfloat16 *out = (is_v ? a.v_out : a.k_out) + ((int64_t)t * Hkv + h) * kD + j * kQBlock;
     reinterpret_cast<uint4 *>(out)[0] = make_uint4(scaled_bf16x2(x[0], s), scaled_bf16x2(x[1], s),
                                                    scaled_bf16x2(x[2], s), scaled_bf16x2(x[3], s));
     reinterpret_cast<uint4 *>(out)[1] = make_uint4(scaled_bf16x2(y[0], s), scaled_bf16x2(y[1], s),
                                                    scaled_bf16x2(y[2], s), scaled_bf16x2(y[3], s));
+}
+
+// The token's slot, or -1 where it has none or one outside the store.
+__device__ __forceinline__ int slot_of(const MoveArgs &a, int t, bool report)
+{
+    const int slot = a.slots[t];
+    if (slot >= 0 && slot / kPage >= a.st.num_pages) {
+        if (report) atomicOr(a.st.err, kQErrSlot);
+        return -1;
+    }
+    return slot < 0 ? -1 : slot;
+}
+
+__device__ __forceinline__ uint8_t *page_at(const MoveArgs &a, int slot, int h)
+{
+    return a.st.pages + ((size_t)(slot / kPage) * a.st.kv_heads + h) * kQPageBytes;
+}
+
+// Few tokens: a row (token, K or V, head) per eight lanes, a block per lane.
+template <bool kGather>
+__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_wait();
+    const int j = threadIdx.x & 7, Hkv = a.st.kv_heads;
+    const int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 3;
+    if (row >= a.rows) return;
+    const int h = (int)(row % Hkv);
+    const int64_t r2 = row / Hkv;
+    const bool is_v = r2 & 1;
+    const int t = (int)(r2 >> 1);
+    const int slot = slot_of(a, t, j == 0);
+    uint32_t scale = 0;
+    uint2 codes = make_uint2(0, 0);
+    if (kGather) {
+        if (slot >= 0) get_block(page_at(a, slot, h), is_v, slot % kPage, j, codes, scale);
+        write_block((is_v ? a.v_out : a.k_out) + ((int64_t)t * Hkv + h) * kD + j * kQBlock, codes, scale,
+                    is_v ? a.st.v_scale : a.st.k_scale);
+    } else if (slot >= 0) {
+        const __nv_bfloat16 *x = (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride) + h * kD + j * kQBlock;
+        const uint4 u[2] = {reinterpret_cast<const uint4 *>(x)[0], reinterpret_cast<const uint4 *>(x)[1]};
+        quantise(u, is_v ? a.st.v_inv : a.st.k_inv, scale, codes);
+        put_block(page_at(a, slot, h), is_v, slot % kPage, j, codes, scale);
+    }
+}
+
+// Many tokens: a warp takes 16 consecutive tokens of one head and K or V, lane
+// (c, j) block j of the tokens 4 c .. 4 c + 3.  Where those four are an aligned
+// quad of a page (as a prefill's are), their scales are one word and their
+// value codes two 16-byte vectors, and a warp's stores cover whole sectors;
+// elsewhere each token goes by itself, as above.
+template <bool kGather>
+__global__ void __launch_bounds__(kThreads) quant_quads_kernel(const __grid_constant__ MoveArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31, j = lane & 7, c = lane >> 3, Hkv = a.st.kv_heads;
+    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;   // [16 tokens][K or V][head]
+    const int h = (int)(warp % Hkv);
+    const int64_t r2 = warp / Hkv;
+    const bool is_v = r2 & 1;
+    const int t0 = (int)(r2 >> 1) * kPage + 4 * c;
+    if (t0 >= a.n_tokens) return;
+    int slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) slot[i] = t0 + i < a.n_tokens ? slot_of(a, t0 + i, j == 0) : -1;
+    const bool quad = slot[0] >= 0 && (slot[0] & 3) == 0 && slot[1] == slot[0] + 1 && slot[2] == slot[0] + 2 &&
+                      slot[3] == slot[0] + 3;
+    const float global = is_v ? a.st.v_scale : a.st.k_scale, inv = is_v ? a.st.v_inv : a.st.k_inv;
+    uint2 codes[4];
+    uint32_t scale[4];
+    if (kGather) {
+        __nv_bfloat16 *out = (is_v ? a.v_out : a.k_out) + ((int64_t)t0 * Hkv + h) * kD + j * kQBlock;
+        if (quad) {
+            const uint8_t *page = page_at(a, slot[0], h);
+            const int tok = slot[0] % kPage;
+            const uint32_t sw = *reinterpret_cast<const uint32_t *>(page + (is_v ? q_vscale_at(tok, j) : q_kscale_at(tok, j)));
+            if (is_v) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(page + q_v_at(tok, j, 0));
+                const uint4 y = *reinterpret_cast<const uint4 *>(page + q_v_at(tok, j, 1));
+                codes[0] = make_uint2(x.x, y.x);
+                codes[1] = make_uint2(x.y, y.y);
+                codes[2] = make_uint2(x.z, y.z);
+                codes[3] = make_uint2(x.w, y.w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++) codes[i] = *reinterpret_cast<const uint2 *>(page + (tok + i) * (kD / 2) + j * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) scale[i] = sw >> 8 * (is_v ? q_scale_byte(i) : i) & 0xff;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                codes[i] = make_uint2(0, 0);
+                scale[i] = 0;
+                if (slot[i] >= 0) get_block(page_at(a, slot[i], h), is_v, slot[i] % kPage, j, codes[i], scale[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (t0 + i < a.n_tokens) write_block(out + (int64_t)i * Hkv * kD, codes[i], scale[i], global);
+    } else {
+        const __nv_bfloat16 *src = is_v ? a.v : a.k;
+        const int64_t stride = is_v ? a.v_stride : a.k_stride;
+        uint4 u[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(src + (t0 + i) * stride + h * kD + j * kQBlock);
+            if (slot[i] >= 0) {
+                u[i][0] = x[0];
+                u[i][1] = x[1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (slot[i] >= 0) quantise(u[i], inv, scale[i], codes[i]);
+        if (quad) {
+            uint8_t *page = page_at(a, slot[0], h);
+            const int tok = slot[0] % kPage;
+            if (is_v) {
+                *reinterpret_cast<uint4 *>(page + q_v_at(tok, j, 0)) = make_uint4(codes[0].x, codes[1].x, codes[2].x, codes[3].x);
+                *reinterpret_cast<uint4 *>(page + q_v_at(tok, j, 1)) = make_uint4(codes[0].y, codes[1].y, codes[2].y, codes[3].y);
+                *reinterpret_cast<uint32_t *>(page + q_vscale_at(tok, j)) =
+                    scale[0] | scale[2] << 8 | scale[1] << 16 | scale[3] << 24;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++) *reinterpret_cast<uint2 *>(page + (tok + i) * (kD / 2) + j * 8) = codes[i];
+                *reinterpret_cast<uint32_t *>(page + q_kscale_at(tok, j)) =
+                    scale[0] | scale[1] << 8 | scale[2] << 16 | scale[3] << 24;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (slot[i] >= 0) put_block(page_at(a, slot[i], h), is_v, slot[i] % kPage, j, codes[i], scale[i]);
+        }
+    }
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -276,10 +378,14 @@ mac_status check_handle(mac_quant_ctx *h)
 mac_status launch_move(mac_quant_ctx *h, bool gather, MoveArgs a, void *stream)
 {
     a.st = h->st;
-    a.rows = 2 * (int64_t)a.n_tokens * h->cfg.kv_heads;
-    const int64_t blocks = (a.rows * 8 + kThreads - 1) / kThreads;
-    const cudaError_t e = launch_maybe_pdl(gather ? quant_gather_kernel : quant_append_kernel, dim3((unsigned)blocks),
-                                           dim3(kThreads), 0, (cudaStream_t)stream, true, a);
+    const int Hkv = h->cfg.kv_heads;
+    a.rows = 2 * (int64_t)a.n_tokens * Hkv;
+    const bool quads = a.n_tokens >= kQuadTokens;
+    const int64_t threads = quads ? 2 * ((int64_t)(a.n_tokens + kPage - 1) / kPage) * Hkv * 32 : a.rows * 8;
+    const auto kernel = quads ? (gather ? quant_quads_kernel<true> : quant_quads_kernel<false>)
+                              : (gather ? quant_rows_kernel<true> : quant_rows_kernel<false>);
+    const cudaError_t e = launch_maybe_pdl(kernel, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                                           (cudaStream_t)stream, true, a);
     return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, gather ? "gather launch" : "append launch");
 }
 

@@ -18,11 +18,13 @@
 // no bank conflict, and each thread's words are matrix fragments once
 // converted (g = lane / 4, c = lane % 4):
 //   K codes   [token 16][64 B]: byte i of a token = elements 2 i, 2 i + 1
-//   K scales  [token 16][block 8]
+//   K scales  [c 4][block 8][tt 4]: token 4 c + tt
 //   V codes   [w 2][block 8][c 4][tt 4][i 4]: token 4 c + tt, elements 8 w + 2 i
 //             and 8 w + 2 i + 1 of the block
 //   V scales  [c 4][block 8][4]: tokens 4 c, 4 c + 2, 4 c + 1, 4 c + 3 (two
 //             masks then leave the f16 pairs of tokens 0, 1 and 2, 3)
+// The four scales, and the sixteen bytes of value codes, of an aligned quad of
+// tokens stand together, so a writer of whole quads stores words and vectors.
 // In a byte the lower element stands in the low four bits.
 #pragma once
 #include "mac_internal.cuh"
@@ -42,6 +44,17 @@ enum : uint32_t { kQErrPage = 1u, kQErrSlot = 2u, kQErrLen = 4u, kQErrTimeout = 
 
 // the byte of token t % 4 among a block's four V scales
 __host__ __device__ inline int q_scale_byte(int tt) { return (tt >> 1) | (tt & 1) << 1; }
+
+__host__ __device__ inline int q_kscale_at(int tok, int block) { return kQKScale + (tok >> 2) * 32 + block * 4 + (tok & 3); }
+__host__ __device__ inline int q_vscale_at(int tok, int block)
+{
+    return kQVScale + (tok >> 2) * 32 + block * 4 + q_scale_byte(tok & 3);
+}
+// word w of a token's two words of value codes in a block
+__host__ __device__ inline int q_v_at(int tok, int block, int w)
+{
+    return kQV + w * 512 + (block * 4 + (tok >> 2)) * 16 + (tok & 3) * 4;
+}
 
 constexpr int kQMaxBatch = 1024;        // requests per attention call (one prefix in shared memory)
 constexpr int kQMaxRows = 32;           // query rows per KV head and request: group x query tokens

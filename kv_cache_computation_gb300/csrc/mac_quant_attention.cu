@@ -154,7 +154,6 @@ struct Smem {
     long long scan[32];
     // parked pieces of the block, in order: their group (-1: none)
     int piece_group[kMaxPieces];
-    float2 nothing;                     // the summary of a piece that is not there
     unsigned long long bar[64];
 };
 
@@ -183,23 +182,17 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
     if (write_lse && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
-// Adds n partial rows to (o, m, l), a warp per call: lanes hold four elements
-// of o each.  at(i) gives partial i's summary (max, sum) and its 128 floats;
-// the summaries are read first, one lane each, so the rows' loads depend on
-// nothing and run together.
-// With kOthers the rows come from other blocks: they are read past the L1.
-template <bool kOthers, int kUnroll, typename F>
-__device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, float &m, float &l)
+// Adds n partial rows of other blocks to (o, m, l), a warp per call: row i's
+// summary (max, sum) is part_ml[row(i)], its 128 floats part_o[row(i)]; a lane
+// holds four elements of o.  The summaries are read first, one lane each, so
+// the rows' loads depend on nothing and run together.  Read past the L1.
+template <typename F>
+__device__ __forceinline__ void merge_rows(const QuantAttnArgs &a, int n, F row, int lane, float4 &o, float &m, float &l)
 {
     for (int i0 = 0; i0 < n; i0 += 32) {
         const int k = min(32, n - i0);
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        const float4 *src = nullptr;
-        if (lane < k) {
-            const float2 *summary;
-            at(i0 + lane, summary, src);
-            ml = kOthers ? __ldcg(summary) : *summary;
-        }
+        if (lane < k) ml = __ldcg(a.part_ml + row(i0 + lane));
         const bool none = ml.y == 0.f;      // saw no token
         const float top = fmaxf(m, warp_max(none ? -CUDART_INF_F : ml.x));
         // a NaN sum survives: its weight is a number or NaN, and the product NaN
@@ -207,16 +200,16 @@ __device__ __forceinline__ void merge_rows(int n, F at, int lane, float4 &o, flo
         l = l * wo + warp_sum(none ? 0.f : ml.y * w);
         o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
         m = top;
-#pragma unroll kUnroll
+#pragma unroll 8
         for (int i = 0; i < k; i++) {
-            const float4 *p = reinterpret_cast<const float4 *>(__shfl_sync(0xffffffffu, (unsigned long long)src, i));
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row(i0 + i) * kD) + lane);
             const float wi = __shfl_sync(0xffffffffu, w, i);
-            const int skip = __shfl_sync(0xffffffffu, (int)none, i);
-            const float4 x = skip ? make_float4(0.f, 0.f, 0.f, 0.f) : kOthers ? __ldcg(p + lane) : p[lane];
-            o.x += x.x * wi;
-            o.y += x.y * wi;
-            o.z += x.z * wi;
-            o.w += x.w * wi;
+            const bool skip = __shfl_sync(0xffffffffu, (int)none, i);
+            // an empty partial's floats are its own zeros
+            o.x += skip ? 0.f : x.x * wi;
+            o.y += skip ? 0.f : x.y * wi;
+            o.z += skip ? 0.f : x.z * wi;
+            o.w += skip ? 0.f : x.w * wi;
         }
     }
 }
@@ -328,7 +321,6 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (tid < 2 * TEAMS) sm.piece_group[tid] = -1;
-    if (tid == 0) sm.nothing = make_float2(-CUDART_INF_F, 0.f);
     __syncthreads();
 
     // the block's and the warp's range of units
@@ -411,6 +403,24 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
 #pragma unroll
         for (int s = 0; s < STAGES; s++) issue(s);
 
+        // while the first pages arrive: the group that starts in this block and runs on behind it, for the second kernel
+        // (the last warp of a block always has a unit)
+        if (team == TEAMS - 1 && lane == 0) {
+            const int ob = request_of(sm, a.batch, Hkv, cta_hi - 1);
+            const long long on = sm.pre[ob + 1] - sm.pre[ob], off = cta_hi - 1 - sm.pre[ob] * Hkv;
+            const int og = off >> 32 ? (int)(off / on) : (int)((uint32_t)off / (uint32_t)on);
+            const long long start = sm.pre[ob] * Hkv + og * on, end = start + on;
+            int owner = -1, last = 0;
+            if (start >= cta_lo && end > cta_hi) {
+                owner = ob * Hkv + og;
+                // the block that holds the group's last unit: a float guess, put right by the exact ranges
+                last = min(grid - 1, (int)((float)(end - 1) / (float)U * (float)grid));
+                while (first_unit(last * TEAMS) >= end) last--;
+                while (first_unit((last + 1) * TEAMS) < end) last++;
+            }
+            a.meta[cta] = make_int4(owner, last, 0, 0);
+        }
+
         int stage = 0;
         uint32_t phase = 0;
         const int tk = 4 * (g8 >> 1) + (g8 & 1);    // token of matrix row g; row g + 8 is token tk + 2
@@ -483,8 +493,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         // the scale's f16 (times 2^-8) in both halves
-                        xa[pp][h] = lds1(page + kQKScale + tk * 8 + 2 * c4 + h) * 0x00800080u;
-                        xb[pp][h] = lds1(page + kQKScale + (tk + 2) * 8 + 2 * c4 + h) * 0x00800080u;
+                        const uint32_t at = page + kQKScale + (g8 >> 1) * 32 + (2 * c4 + h) * 4 + (g8 & 1);
+                        xa[pp][h] = lds1(at) * 0x00800080u;
+                        xb[pp][h] = lds1(at + 2) * 0x00800080u;
                     }
                 }
 #pragma unroll
@@ -677,50 +688,55 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     __threadfence_block();
     __syncthreads();
 
-    // merge the parked pieces group by group
-    int owner = -1, owner_last = 0;
-    for (int i = 0; i < 2 * TEAMS;) {
-        const int grp = sm.piece_group[i];
-        if (grp < 0) {
-            i++;
-            continue;
-        }
-        int j = i + 1;
-        while (j < 2 * TEAMS && (sm.piece_group[j] == grp || sm.piece_group[j] < 0)) j++;
+    // Merge the parked pieces group by group, a warp per row.  Lane i looks at
+    // piece i; a run of pieces of one group starts where the group differs
+    // from the piece before it.
+    const int mine = lane < 2 * TEAMS ? sm.piece_group[lane] : -1;
+    const uint32_t parked = __ballot_sync(0xffffffffu, mine >= 0);
+    const uint32_t below = parked & ((1u << lane) - 1u);
+    const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+    uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+    while (starts) {
+        const int first = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const uint32_t run = parked & ~((1u << first) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
+        const int grp = __shfl_sync(0xffffffffu, mine, first);
         const int b = grp / Hkv, g = grp - b * Hkv;
         const long long n_units = sm.pre[b + 1] - sm.pre[b];
-        const long long start = sm.pre[b] * Hkv + g * n_units, end = start + n_units;
-        const bool whole = start >= cta_lo && end <= cta_hi;
-        const int slot = start < cta_lo ? 0 : 1;
-        if (!whole && slot == 1) {
-            owner = grp;
-            // the block that holds the group's last unit: a float guess, put right by the exact ranges
-            int c = min(grid - 1, (int)((float)(end - 1) / (float)U * (float)grid));
-            while (first_unit(c * TEAMS) >= end) c--;
-            while (first_unit((c + 1) * TEAMS) < end) c++;
-            owner_last = c;
-        }
+        const long long start = sm.pre[b] * Hkv + g * n_units;
+        const bool whole = start >= cta_lo && start + n_units <= cta_hi;
         for (int r = team; r < a.rows; r += TEAMS) {
+            const int t = lane >> 1;
+            const int64_t row = park + (int64_t)t * PADROWS + r;
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (run >> lane & 1) ml = lane & 1 ? *parked_ml(t, r) : a.part_ml[row];
+            const bool none = ml.y == 0.f;      // saw no token
+            const float m = warp_max(none ? -CUDART_INF_F : ml.x);
+            // a NaN sum survives: its weight is a number or NaN, and the product NaN
+            const float w = none ? 0.f : exp2f(ml.x - m);
+            const float l = warp_sum(none ? 0.f : ml.y * w);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float m = -CUDART_INF_F, l = 0.f;
-            merge_rows<false, 2>(j - i, [&](int k, const float2 *&ml, const float4 *&src) {
-                const int t = (i + k) >> 1;
-                const int64_t row = park + (int64_t)t * PADROWS + r;
-                const bool last = (i + k) & 1;
-                ml = sm.piece_group[i + k] < 0 ? &sm.nothing : last ? parked_ml(t, r) : a.part_ml + row;
-                src = reinterpret_cast<const float4 *>(last ? parked_o(t, r) : a.part_o + row * kD);
-            }, lane, o, m, l);
+            uint32_t rest_of = __ballot_sync(0xffffffffu, !none);
+            while (rest_of) {
+                const int i = __ffs(rest_of) - 1;
+                rest_of &= rest_of - 1;
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float *src = i & 1 ? parked_o(i >> 1, r) : a.part_o + (park + (int64_t)(i >> 1) * PADROWS + r) * kD;
+                const float4 x = reinterpret_cast<const float4 *>(src)[lane];
+                o.x += x.x * wi;
+                o.y += x.y * wi;
+                o.z += x.z * wi;
+                o.w += x.w * wi;
+            }
             if (whole) {
                 finish4(a, b, g, r, lane * 4, o, m, l, lane == 0);
             } else {
-                const int64_t row = crossing + slot * PADROWS + r;
-                reinterpret_cast<float4 *>(a.part_o + row * kD)[lane] = o;
-                if (lane == 0) a.part_ml[row] = make_float2(m, l);
+                const int64_t at = crossing + (start < cta_lo ? 0 : PADROWS) + r;
+                reinterpret_cast<float4 *>(a.part_o + at * kD)[lane] = o;
+                if (lane == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
-        i = j;
     }
-    if (tid == 0) a.meta[cta] = make_int4(owner, owner_last, 0, 0);
 }
 
 // Block (i, r): row r of the group that starts in block i of the attention
@@ -739,24 +755,29 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
     const int n = meta.y - (int)blockIdx.x + 1;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -CUDART_INF_F, l = 0.f;
-    // warp w takes partials w, w + 4, ...; then lane w of warp 0 the four warps' results
-    merge_rows<true, 8>((n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
-        const int k = i * kCombineWarps + warp;
-        const int64_t row = ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r;
-        ml = a.part_ml + row;
-        src = reinterpret_cast<const float4 *>(a.part_o + row * kD);
-    }, lane, o, m, l);
-    so[warp][lane] = o;
-    if (lane == 0) sml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp) return;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-    m = -CUDART_INF_F;
-    l = 0.f;
-    merge_rows<false, 1>(kCombineWarps, [&](int i, const float2 *&ml, const float4 *&src) {
-        ml = &sml[i];
-        src = so[i];
-    }, lane, o, m, l);
+    const auto row = [&](int k) { return ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r; };
+    if (n <= 32) {
+        if (warp) return;
+        merge_rows(a, n, row, lane, o, m, l);
+    } else {
+        // warp w takes partials w, w + 4, ...; then warp 0 adds the others' results
+        merge_rows(a, (n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i) { return row(i * kCombineWarps + warp); },
+                   lane, o, m, l);
+        so[warp][lane] = o;
+        if (lane == 0) sml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp) return;
+#pragma unroll 1
+        for (int w = 1; w < kCombineWarps; w++) {
+            const float2 ml = sml[w];
+            const float4 x = so[w][lane];
+            if (ml.y == 0.f) continue;
+            const float top = fmaxf(m, ml.x), wo = l == 0.f ? 0.f : exp2f(m - top), wi = exp2f(ml.x - top);
+            o = make_float4(o.x * wo + x.x * wi, o.y * wo + x.y * wi, o.z * wo + x.z * wi, o.w * wo + x.w * wi);
+            l = l * wo + ml.y * wi;
+            m = top;
+        }
+    }
     const int b = meta.x / a.st.kv_heads;
     finish4(a, b, meta.x - b * a.st.kv_heads, r, lane * 4, o, m, l, lane == 0);
 }

@@ -219,12 +219,13 @@ def test_store_round_trip_is_the_format(T, Hkv, pages, ks, vs):
         assert (gk == 0).all() and (gv == 0).all()
 
 
-@pytest.mark.parametrize("first,T", [(0, 64), (0, 40), (3, 61), (16, 16), (5, 7)])
-def test_store_whole_pages(first, T):
+@pytest.mark.parametrize("first,T,pages", [(0, 64, 9), (0, 40, 9), (3, 61, 9), (16, 16, 9), (5, 7, 9), (0, 640, 41),
+                                           (4, 513, 41), (7, 600, 41), (0, 641, 41)])
+def test_store_whole_pages(first, T, pages):
     """Runs of consecutive tokens through pages in any order, starting and ending inside a page, beside other tokens of
     the same pages that stay as they are."""
     from kv_cache_computation_gb300 import QuantKV
-    pages, Hkv = 9, 2
+    Hkv = 2
     cache = QuantKV(Hkv, Hkv, num_pages=pages)
     order = np.random.default_rng(4).permutation(pages)
     every = torch.from_numpy((order[:, None] * 16 + np.arange(16)).reshape(-1).astype(np.int32))

@@ -150,7 +150,7 @@ def test_store_layout_covers_a_page_once():
             i = e % 16 // 2
             byte = 1152 + (i // 4) * 512 + (j * 4 + c) * 16 + tt * 4 + i % 4
             nib.setdefault(2 * byte + e % 2, []).append(("v", tok, e))
-            scale.setdefault(1024 + tok * 8 + j, set()).add(("k", tok, j))
+            scale.setdefault(1024 + c * 32 + j * 4 + tt, set()).add(("k", tok, j))
             scale.setdefault(2176 + c * 32 + j * 4 + (0, 2, 1, 3)[tt], set()).add(("v", tok, j))
     assert all(len(x) == 1 for x in nib.values()) and all(len(x) == 1 for x in scale.values())
     assert sorted(nib) == list(range(0, 2 * 1024)) + list(range(2 * 1152, 2 * 2176))
@@ -158,6 +158,9 @@ def test_store_layout_covers_a_page_once():
     for lane in range(32):
         g, c = lane // 4, lane % 4
         tk = 4 * (g >> 1) + (g & 1)
+        for h in range(2):                                       # K scale bytes of the lane's two blocks
+            at = 1024 + (g >> 1) * 32 + (2 * c + h) * 4 + (g & 1)
+            assert scale[at] == {("k", tk, 2 * c + h)} and scale[at + 2] == {("k", tk + 2, 2 * c + h)}
         for row, tok in ((g, tk), (g + 8, tk + 2)):
             # matrix rows {2c, 2c+1, 2c+8, 2c+9} are tokens 4c .. 4c+3
             assert tok == 4 * (row % 8 // 2) + row % 2 + (2 if row >= 8 else 0)
