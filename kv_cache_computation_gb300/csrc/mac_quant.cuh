@@ -82,7 +82,7 @@ struct QuantAttnArgs {
     float v_out_scale;                  // v_scale x 2^8
     float *part_o;                      // [kQPartRows][128]
     float2 *part_ml;                    // [kQPartRows]
-    int4 *meta;                         // [grid]: group that starts in the block and runs on, its last block
+    int4 *meta;                         // groups that cross blocks: {group or -1, last block, first block, 0}
 };
 
 cudaError_t quant_attention_config(int sm_count);

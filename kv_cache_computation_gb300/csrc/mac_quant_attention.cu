@@ -45,7 +45,10 @@ namespace macgpu {
 
 namespace {
 
-constexpr int kPP = 2;                                  // pages per unit
+#ifndef QPP
+#define QPP 2
+#endif
+constexpr int kPP = QPP;                                  // pages per unit
 constexpr int kUnitTok = kPP * kPage;
 constexpr int kUnitBytes = kPP * kQPageBytes;
 constexpr float kMargin = 6.f;                          // log2: how far a score may pass the softmax reference
@@ -142,16 +145,23 @@ __device__ __forceinline__ uint32_t lds1(uint32_t addr)
 // still has to be written).
 __device__ __forceinline__ int units_of(int len) { return len > kUnitTok ? (len - 1) / kUnitTok + 1 : 1; }
 
-// A warp's shared memory: its ring and, where Q does not stay in registers, Q.
-__host__ __device__ constexpr int team_bytes(int q_tiles, int stages)
+// A warp's shared memory: its ring and, where Q does not stay in registers, Q;
+// at the end the piece it parks.
+__host__ __device__ constexpr int team_bytes(int nt, int stages, bool qreg)
 {
-    return stages * kUnitBytes + q_tiles * 2048;
+    const int run = stages * kUnitBytes + (qreg ? 0 : nt * 2048), parked = (nt * 8 * kParkRow * 4 + 127) / 128 * 128;
+    return run > parked ? run : parked;
 }
+
+// Where the second kernel finds its groups: with no more groups than blocks in
+// meta[group], else in meta[the block in which the group starts].
+__host__ __device__ inline bool meta_by_group(const QuantAttnArgs &a, int grid) { return (int64_t)a.batch * a.st.kv_heads <= grid; }
 
 struct Smem {
     long long pre[kQMaxBatch + 1];      // units of the requests before b (per KV head)
     int len[kQMaxBatch];
     long long scan[32];
+    long long lo, hi;                   // the block's units
     // parked pieces of the block, in order: their group (-1: none)
     int piece_group[kMaxPieces];
     unsigned long long bar[64];
@@ -180,38 +190,6 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
     *reinterpret_cast<uint2 *>(a.out + row * kD + d0) = make_uint2(
         bf16x2_bits(__floats2bfloat162_rn(o.x * inv, o.y * inv)), bf16x2_bits(__floats2bfloat162_rn(o.z * inv, o.w * inv)));
     if (write_lse && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
-}
-
-// Adds n partial rows of other blocks to (o, m, l), a warp per call: row i's
-// summary (max, sum) is part_ml[row(i)], its 128 floats part_o[row(i)]; a lane
-// holds four elements of o.  The summaries are read first, one lane each, so
-// the rows' loads depend on nothing and run together.  Read past the L1.
-template <typename F>
-__device__ __forceinline__ void merge_rows(const QuantAttnArgs &a, int n, F row, int lane, float4 &o, float &m, float &l)
-{
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int k = min(32, n - i0);
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        if (lane < k) ml = __ldcg(a.part_ml + row(i0 + lane));
-        const bool none = ml.y == 0.f;      // saw no token
-        const float top = fmaxf(m, warp_max(none ? -CUDART_INF_F : ml.x));
-        // a NaN sum survives: its weight is a number or NaN, and the product NaN
-        const float w = none ? 0.f : exp2f(ml.x - top), wo = l == 0.f ? 0.f : exp2f(m - top);
-        l = l * wo + warp_sum(none ? 0.f : ml.y * w);
-        o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
-        m = top;
-#pragma unroll 8
-        for (int i = 0; i < k; i++) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row(i0 + i) * kD) + lane);
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const bool skip = __shfl_sync(0xffffffffu, (int)none, i);
-            // an empty partial's floats are its own zeros
-            o.x += skip ? 0.f : x.x * wi;
-            o.y += skip ? 0.f : x.y * wi;
-            o.z += skip ? 0.f : x.z * wi;
-            o.w += skip ? 0.f : x.w * wi;
-        }
-    }
 }
 
 // Row r of a group's queries as f16, the lane's 32 elements from 32 c on in
@@ -266,9 +244,8 @@ template <int NT, int TEAMS, int STAGES, int MINB, bool QREG>
 __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const __grid_constant__ QuantAttnArgs a)
 {
     constexpr int PADROWS = NT * 8;
-    constexpr int TEAM_BYTES = team_bytes(QREG ? 0 : NT, STAGES);
+    constexpr int TEAM_BYTES = team_bytes(NT, STAGES, QREG);
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
-    static_assert(PADROWS * kParkRow * 4 <= TEAM_BYTES, "a parked piece fits the warp's shared memory");
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ Smem sm;
     const int tid = threadIdx.x, lane = tid & 31, team = tid >> 5;
@@ -329,8 +306,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     const long long most = U >= TEAMS ? U / TEAMS : 1;
     const int grid = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
     const int cta = blockIdx.x;
+    const bool by_group = meta_by_group(a, gridDim.x);
     if (cta >= grid) {
-        if (tid == 0) a.meta[cta] = make_int4(-1, 0, 0, 0);
+        if (tid == 0 && !by_group) a.meta[cta] = make_int4(-1, 0, 0, 0);
         return;
     }
     const int teams = grid * TEAMS, me = cta * TEAMS + team;
@@ -340,10 +318,14 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     auto first_unit = [&](int i) { return per * i + (long long)(rest * (uint32_t)i / (uint32_t)teams); };
     const long long lo = first_unit(me), hi = first_unit(me + 1);
     const long long cta_lo = first_unit(cta * TEAMS), cta_hi = first_unit((cta + 1) * TEAMS);
+    if (tid == 0) {
+        sm.lo = cta_lo;     // for the merge behind the long loop
+        sm.hi = cta_hi;
+    }
     // partial rows: the block's two crossing groups, then its warps' first pieces.  A warp's last piece is parked in
     // its own shared memory, which it has read to the end by then.
-    const int64_t crossing = (int64_t)cta * 2 * PADROWS;
-    const int64_t park = ((int64_t)gridDim.x * 2 + (int64_t)cta * TEAMS) * PADROWS;
+    auto crossing_row = [&](int which, int r) { return ((int64_t)blockIdx.x * 2 + which) * PADROWS + r; };
+    auto first_row = [&](int t, int r) { return ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * TEAMS + t) * PADROWS + r; };
     auto parked_o = [&](int t, int r) { return reinterpret_cast<float *>(dyn + (size_t)t * TEAM_BYTES) + r * kParkRow; };
     auto parked_ml = [&](int t, int r) { return reinterpret_cast<float2 *>(parked_o(t, r) + kD); };
 
@@ -374,7 +356,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         auto issue = [&](int s) {
             if (ld_left == 0) return;
             const uint32_t bar = bar0 + 8 * s;
-            const int pages = ld_tok > kPage ? kPP : ld_tok > 0 ? 1 : 0;
+            const int pages = kPP == 2 && ld_tok > kPage ? 2 : ld_tok > 0 ? 1 : 0;
             if (lane == 0)
                 asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n"
                              :: "r"(bar), "r"((uint32_t)pages * kQPageBytes)
@@ -398,7 +380,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             }
             fetch();
         };
-        static_assert(kPP == 2, "a unit has one or two pages");
+        static_assert(kPP <= 2, "a unit has one or two pages");
         fetch();
 #pragma unroll
         for (int s = 0; s < STAGES; s++) issue(s);
@@ -418,7 +400,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 while (first_unit(last * TEAMS) >= end) last--;
                 while (first_unit((last + 1) * TEAMS) < end) last++;
             }
-            a.meta[cta] = make_int4(owner, last, 0, 0);
+            if (owner >= 0 || !by_group) a.meta[by_group ? owner : cta] = make_int4(owner, last, cta, 0);
         }
 
         int stage = 0;
@@ -560,7 +542,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        x[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+                        x[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
+#pragma unroll
+                        for (int pp = 1; pp < kPP; pp++) x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
                         moves |= x[nt][h] > top_raw[nt][h];
                     }
                 if (__any_sync(0xffffffffu, moves)) {
@@ -645,7 +629,10 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 }
             const bool ends = u0 + n == n_units, whole = u0 == 0 && ends;
             const int which = ends ? 0 : 1;     // 1: the group runs on into the next warp's range
-            if (!whole && lane == 0) sm.piece_group[2 * team + which] = b * Hkv + g;
+            if (lane == 0) {
+                if (!whole) sm.piece_group[2 * team + which] = b * Hkv + g;
+                else if (meta_by_group(a, gridDim.x)) a.meta[b * Hkv + g] = make_int4(-1, 0, 0, 0);
+            }
             if (which) __syncwarp();            // the parked piece takes the place of what the warp has read
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
@@ -668,7 +655,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         if (a.lse && g8 == 0)
                             a.lse[row] = l == 0.f ? -CUDART_INF_F : (ref[nt][h] - kPShift + log2f(l)) * kLn2;
                     } else {
-                        const int64_t row = park + (int64_t)team * PADROWS + r;
+                        const int64_t row = first_row(team, r);
                         float *dst = which ? parked_o(team, r) : a.part_o + row * kD;
 #pragma unroll
                         for (int j = 0; j < 8; j += 2)
@@ -704,12 +691,11 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         const int b = grp / Hkv, g = grp - b * Hkv;
         const long long n_units = sm.pre[b + 1] - sm.pre[b];
         const long long start = sm.pre[b] * Hkv + g * n_units;
-        const bool whole = start >= cta_lo && start + n_units <= cta_hi;
+        const bool whole = start >= sm.lo && start + n_units <= sm.hi;
+        if (whole && tid == 0 && meta_by_group(a, gridDim.x)) a.meta[grp] = make_int4(-1, 0, 0, 0);
         for (int r = team; r < a.rows; r += TEAMS) {
-            const int t = lane >> 1;
-            const int64_t row = park + (int64_t)t * PADROWS + r;
             float2 ml = make_float2(-CUDART_INF_F, 0.f);
-            if (run >> lane & 1) ml = lane & 1 ? *parked_ml(t, r) : a.part_ml[row];
+            if (run >> lane & 1) ml = lane & 1 ? *parked_ml(lane >> 1, r) : a.part_ml[first_row(lane >> 1, r)];
             const bool none = ml.y == 0.f;      // saw no token
             const float m = warp_max(none ? -CUDART_INF_F : ml.x);
             // a NaN sum survives: its weight is a number or NaN, and the product NaN
@@ -721,7 +707,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 const int i = __ffs(rest_of) - 1;
                 rest_of &= rest_of - 1;
                 const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float *src = i & 1 ? parked_o(i >> 1, r) : a.part_o + (park + (int64_t)(i >> 1) * PADROWS + r) * kD;
+                const float *src = i & 1 ? parked_o(i >> 1, r) : a.part_o + first_row(i >> 1, r) * kD;
                 const float4 x = reinterpret_cast<const float4 *>(src)[lane];
                 o.x += x.x * wi;
                 o.y += x.y * wi;
@@ -731,7 +717,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             if (whole) {
                 finish4(a, b, g, r, lane * 4, o, m, l, lane == 0);
             } else {
-                const int64_t at = crossing + (start < cta_lo ? 0 : PADROWS) + r;
+                const int64_t at = crossing_row(start < sm.lo ? 0 : 1, r);
                 reinterpret_cast<float4 *>(a.part_o + at * kD)[lane] = o;
                 if (lane == 0) a.part_ml[at] = make_float2(m, l);
             }
@@ -739,47 +725,96 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     }
 }
 
-// Block (i, r): row r of the group that starts in block i of the attention
-// grid and runs on into the blocks up to meta.y.
-constexpr int kCombineWarps = 4;
+// The groups that cross blocks, merged: block (x, y) has the group of meta[x],
+// which spans the attention kernel's blocks meta.z .. meta.y, and the rows
+// y rpb .. of it, 8 / rpb warps to a row, a lane with four elements.  A warp
+// takes eight partials at a time, and its loads are independent of one another.
+// The body runs twice: first without partials while the attention kernel still
+// works, which brings its instructions into the caches (1 to 1.5 us of the 3.6
+// that the merge took without), then with them.
+constexpr int kCombineWarps = 8, kCombineBatch = 8;
 
 __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const __grid_constant__ QuantAttnArgs a,
-                                                                          int padrows)
+                                                                          int padrows, int rpb)
 {
     __shared__ float4 so[kCombineWarps][32];
     __shared__ float2 sml[kCombineWarps];
-    pdl_wait();
-    const int4 meta = a.meta[blockIdx.x];
-    if (meta.x < 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
-    const int n = meta.y - (int)blockIdx.x + 1;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -CUDART_INF_F, l = 0.f;
-    const auto row = [&](int k) { return ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r; };
-    if (n <= 32) {
-        if (warp) return;
-        merge_rows(a, n, row, lane, o, m, l);
-    } else {
-        // warp w takes partials w, w + 4, ...; then warp 0 adds the others' results
-        merge_rows(a, (n - warp + kCombineWarps - 1) / kCombineWarps, [&](int i) { return row(i * kCombineWarps + warp); },
-                   lane, o, m, l);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wpr = kCombineWarps / rpb, sub = warp % wpr, r = blockIdx.y * rpb + warp / wpr;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; pass++) {
+        int n = 0, group = 0, cta0 = 0;
+        if (pass) {
+            pdl_wait();
+            const int4 meta = __ldcg(a.meta + blockIdx.x);
+            if (meta.x < 0) return;
+            group = meta.x;
+            cta0 = meta.z;
+            n = r < a.rows ? meta.y - cta0 + 1 : 0;
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m = -CUDART_INF_F, l = 0.f;
+        int k0 = sub * kCombineBatch;
+        do {
+            // partial k: the group's part of block cta0 + k
+            float2 ml[kCombineBatch];
+            float4 x[kCombineBatch];
+#pragma unroll
+            for (int i = 0; i < kCombineBatch; i++) {
+                const int k = k0 + i;
+                const int64_t row = ((int64_t)(cta0 + k) * 2 + (k == 0 ? 1 : 0)) * padrows + r;
+                ml[i] = make_float2(-CUDART_INF_F, 0.f);
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < n) {
+                    ml[i] = __ldcg(a.part_ml + row);
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + row * kD) + lane);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kCombineBatch; i++)
+                if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);      // a sum of 0 saw no token
+            const float wo = l == 0.f ? 0.f : ex2_approx(m - top);
+            o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
+            l *= wo;
+#pragma unroll
+            for (int i = 0; i < kCombineBatch; i++) {
+                // a NaN sum survives: its weight is a number or NaN, and the product NaN
+                const bool some = ml[i].y != 0.f;
+                const float w = some ? ex2_approx(ml[i].x - top) : 0.f;
+                l += some ? ml[i].y * w : 0.f;
+                o.x += some ? x[i].x * w : 0.f;
+                o.y += some ? x[i].y * w : 0.f;
+                o.z += some ? x[i].z * w : 0.f;
+                o.w += some ? x[i].w * w : 0.f;
+            }
+            m = top;
+            k0 += wpr * kCombineBatch;
+        } while (k0 < n);
         so[warp][lane] = o;
         if (lane == 0) sml[warp] = make_float2(m, l);
         __syncthreads();
-        if (warp) return;
+        if (sub == 0) {
+            float top = -CUDART_INF_F;
 #pragma unroll 1
-        for (int w = 1; w < kCombineWarps; w++) {
-            const float2 ml = sml[w];
-            const float4 x = so[w][lane];
-            if (ml.y == 0.f) continue;
-            const float top = fmaxf(m, ml.x), wo = l == 0.f ? 0.f : exp2f(m - top), wi = exp2f(ml.x - top);
-            o = make_float4(o.x * wo + x.x * wi, o.y * wo + x.y * wi, o.z * wo + x.z * wi, o.w * wo + x.w * wi);
-            l = l * wo + ml.y * wi;
-            m = top;
+            for (int w = 0; w < wpr; w++)
+                if (sml[warp + w].y != 0.f) top = fmaxf(top, sml[warp + w].x);
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.f;
+#pragma unroll 1
+            for (int w = 0; w < wpr; w++) {
+                const float2 ml = sml[warp + w];
+                const float4 x = so[warp + w][lane];
+                if (ml.y == 0.f) continue;
+                const float f = ex2_approx(ml.x - top);
+                l += ml.y * f;
+                o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
+            }
+            const int b = group / a.st.kv_heads;
+            if (n > 0) finish4(a, b, group - b * a.st.kv_heads, r, lane * 4, o, top, l, lane == 0);
         }
+        __syncthreads();
     }
-    const int b = meta.x / a.st.kv_heads;
-    finish4(a, b, meta.x - b * a.st.kv_heads, r, lane * 4, o, m, l, lane == 0);
 }
 
 struct Variant {
@@ -792,7 +827,7 @@ template <int NT, int TEAMS, int STAGES, int MINB, bool QREG>
 Variant variant()
 {
     return {quant_attention_kernel<NT, TEAMS, STAGES, MINB, QREG>, TEAMS, NT * 8, MINB,
-            (size_t)TEAMS * team_bytes(QREG ? 0 : NT, STAGES)};
+            (size_t)TEAMS * team_bytes(NT, STAGES, QREG)};
 }
 
 // As many warps as the registers of an output tile of 8 NT rows leave room for.
@@ -832,7 +867,12 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, int sm_count, cudaStr
     const int grid = grid_of(v, sm_count);
     cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.teams * 32), v.smem, s, true, a);
     if (e != cudaSuccess) return e;
-    return launch_maybe_pdl(quant_combine_kernel, dim3(grid, a.rows), dim3(kCombineWarps * 32), 0, s, true, a, v.padrows);
+    // as many warps to a row as keep the blocks, most of which find nothing to merge, near one wave
+    const int items = meta_by_group(a, grid) ? a.batch * a.st.kv_heads : grid;
+    int rpb = 1;
+    while (rpb < kCombineWarps && rpb < a.rows && (int64_t)items * ((a.rows + rpb - 1) / rpb) > 4 * sm_count) rpb *= 2;
+    return launch_maybe_pdl(quant_combine_kernel, dim3(items, (a.rows + rpb - 1) / rpb), dim3(kCombineWarps * 32), 0, s, true,
+                            a, v.padrows, rpb);
 }
 
 }  // namespace macgpu
