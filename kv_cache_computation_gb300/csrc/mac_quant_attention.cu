@@ -23,8 +23,8 @@
 //    thread's K words are 32 consecutive elements of a token (two scales), and
 //    its V words one 16-element block of four consecutive tokens (four scales),
 //    whose codes are paired by token with two logic operations per eight codes.
-// Roundings: Q is bf16 and becomes f16 with a power of two per row (exact
-// unless an element is 2^-28 of the row's largest); stored values are exact in
+// Roundings: Q is bf16 and becomes f16 with a power of two per group (exact but
+// for elements below 2^-28 of the group's largest, which keep 2^-39 of it); stored values are exact in
 // f16; the weights P, at most 2^15, are rounded to f16 (2^-11 of each) and
 // summed unrounded in fp32; sums, the maximum and the output stay in fp32.
 // P's factor 2^9 keeps weights down to 2^-33 of the largest.
@@ -45,10 +45,7 @@ namespace macgpu {
 
 namespace {
 
-#ifndef QPP
-#define QPP 2
-#endif
-constexpr int kPP = QPP;                                  // pages per unit
+constexpr int kPP = 2;                                  // pages per unit
 constexpr int kUnitTok = kPP * kPage;
 constexpr int kUnitBytes = kPP * kQPageBytes;
 constexpr float kMargin = 6.f;                          // log2: how far a score may pass the softmax reference
@@ -81,7 +78,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -192,49 +189,39 @@ __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, in
     if (write_lse && a.lse) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
-// Row r of a group's queries as f16, the lane's 32 elements from 32 c on in
-// four words of eight, times the power of two that brings the row's largest
-// element into [2^14, 2^15) (zeros past the rows).  Returns what takes a raw
-// score of the row to log2 units.
-template <typename F>
-__device__ __forceinline__ float load_q(const QuantAttnArgs &a, int b, int g, int r, int c, F put)
+// The lane's 32 elements from 32 c on of row r of a group's queries (zeros past
+// the rows).
+__device__ __forceinline__ void load_q(const QuantAttnArgs &a, int b, int g, int r, int c, uint32_t (&w)[16])
 {
-    uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 16; i++) w[i] = 0;
     if (r < a.rows) {
         const int qt = r / a.G;
         const uint4 *src = reinterpret_cast<const uint4 *>(
             a.q + (((int64_t)b * a.n_query + qt) * a.heads + g * a.G + (r - qt * a.G)) * kD + 32 * c);
 #pragma unroll
-        for (int i = 0; i < 4; i++) w[i] = src[i];
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            top = max(top, x[k] & 0x7fffu);
-            top = max(top, (x[k] >> 16) & 0x7fffu);
+        for (int i = 0; i < 4; i++) {
+            const uint4 v = src[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
     }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    int shift = 14 - ((int)(top >> 7) - 127);
-    if (top == 0 || top >= 0x7f80u) shift = 0;
-    shift = shift > 126 ? 126 : shift;
-    const float up = __int_as_float((shift + 127) << 23);
+}
+
+// The larger of top and the bit patterns of the finite magnitudes in w.
+__device__ __forceinline__ uint32_t finite_top(const uint32_t (&w)[16], uint32_t top)
+{
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t f[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            f[k] = f16x2(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
-        put(i, f);
+    for (int i = 0; i < 16; i++) {
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        top = max(top, lo < 0x7f80u ? lo : 0u);
+        top = max(top, hi < 0x7f80u ? hi : 0u);
     }
-    return fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
+    return top;
+}
+
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t two, float up)
+{
+    return f16x2(__uint_as_float(two << 16) * up, __uint_as_float(two & 0xffff0000u) * up);
 }
 
 // NT: N tiles (8 rows each), TEAMS warps per block, STAGES units in a warp's
@@ -244,6 +231,7 @@ template <int NT, int TEAMS, int STAGES, int MINB, bool QREG>
 __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const __grid_constant__ QuantAttnArgs a)
 {
     constexpr int PADROWS = NT * 8;
+    constexpr int PG = NT <= 2 ? kPP : 1;       // pages whose scores are made together, as registers allow
     constexpr int TEAM_BYTES = team_bytes(NT, STAGES, QREG);
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
     extern __shared__ __align__(128) unsigned char dyn[];
@@ -356,7 +344,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         auto issue = [&](int s) {
             if (ld_left == 0) return;
             const uint32_t bar = bar0 + 8 * s;
-            const int pages = kPP == 2 && ld_tok > kPage ? 2 : ld_tok > 0 ? 1 : 0;
+            const int pages = ld_tok > kPage ? 2 : ld_tok > 0 ? 1 : 0;
             if (lane == 0)
                 asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n"
                              :: "r"(bar), "r"((uint32_t)pages * kQPageBytes)
@@ -380,7 +368,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             }
             fetch();
         };
-        static_assert(kPP <= 2, "a unit has one or two pages");
+        static_assert(kPP == 2, "a unit has one or two pages");
         fetch();
 #pragma unroll
         for (int s = 0; s < STAGES; s++) issue(s);
@@ -412,37 +400,52 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             const int len = sm.len[b];
             const int full = max(len - (a.n_query - 1), 0);     // tokens every row sees
             uint32_t qf[QREG ? NT : 1][16];
-            float sc[NT][2], ref[NT][2], top_raw[NT][2], sum[NT][2], o[NT][8][4];
+            float ref[NT][2], sum[NT][2], o[NT][8][4];
+            // Q in f16, times the power of two that brings the group's largest finite element into [2^14, 2^15); sc
+            // takes a raw score to log2 units
+            uint32_t top = 0;
+            uint32_t w[QREG ? NT : 1][16];
             if (QREG) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    const float rs = load_q(a, b, g, nt * 8 + g8, c4, [&](int i, const uint32_t (&f)[4]) {
-#pragma unroll
-                        for (int k = 0; k < 4; k++) qf[nt][4 * i + k] = f[k];
-                    });
-#pragma unroll
-                    for (int h = 0; h < 2; h++) sc[nt][h] = __shfl_sync(0xffffffffu, rs, (2 * c4 + h) * 4);
+                    load_q(a, b, g, nt * 8 + g8, c4, w[nt]);
+                    top = finite_top(w[nt], top);
                 }
             } else {
-                const uint32_t q0 = ring + STAGES * kUnitBytes + lane * 16;
-                float rs_all = 0.f;         // lane 8 nt + g: the scale of row 8 nt + g
 #pragma unroll 1
                 for (int nt = 0; nt < NT; nt++) {
-                    const float rs = load_q(a, b, g, nt * 8 + g8, c4,
-                                            [&](int i, const uint32_t (&f)[4]) { sts16(q0 + (nt * 4 + i) * 512, f); });
-                    const float mine = __shfl_sync(0xffffffffu, rs, (lane & 7) * 4);
-                    if ((lane >> 3) == nt) rs_all = mine;
+                    load_q(a, b, g, nt * 8 + g8, c4, w[0]);
+                    top = finite_top(w[0], top);
                 }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int shift = top ? min(14 - ((int)(top >> 7) - 127), 126) : 0;
+            const float up = __int_as_float((shift + 127) << 23);
+            const float sc = fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
+            if (QREG) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                    for (int h = 0; h < 2; h++) sc[nt][h] = __shfl_sync(0xffffffffu, rs_all, nt * 8 + 2 * c4 + h);
+                    for (int i = 0; i < 16; i++) qf[nt][i] = scaled_f16x2(w[nt][i], up);
+            } else {
+                const uint32_t q0 = ring + STAGES * kUnitBytes + lane * 16;
+#pragma unroll 1
+                for (int nt = 0; nt < NT; nt++) {
+                    load_q(a, b, g, nt * 8 + g8, c4, w[0]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        uint32_t f[4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) f[k] = scaled_f16x2(w[0][4 * i + k], up);
+                        sts16(q0 + (nt * 4 + i) * 512, f);
+                    }
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    ref[nt][h] = top_raw[nt][h] = -CUDART_INF_F;
+                    ref[nt][h] = -CUDART_INF_F;
                     sum[nt][h] = 0.f;
                 }
 #pragma unroll
@@ -465,50 +468,53 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) s[pp][nt][k] = 0.f;
-                uint32_t wa[kPP][4], wb[kPP][4], xa[kPP][2], xb[kPP][2];
 #pragma unroll
-                for (int pp = 0; pp < kPP; pp++) {
-                    const uint32_t page = unit + pp * kQPageBytes;
-                    const uint4 ka = lds16(page + tk * 64 + c4 * 16), kb = lds16(page + (tk + 2) * 64 + c4 * 16);
-                    wa[pp][0] = ka.x, wa[pp][1] = ka.y, wa[pp][2] = ka.z, wa[pp][3] = ka.w;
-                    wb[pp][0] = kb.x, wb[pp][1] = kb.y, wb[pp][2] = kb.z, wb[pp][3] = kb.w;
+                for (int p0 = 0; p0 < kPP; p0 += PG) {
+                    uint32_t wa[PG][4], wb[PG][4], xa[PG][2], xb[PG][2];
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        // the scale's f16 (times 2^-8) in both halves
-                        const uint32_t at = page + kQKScale + (g8 >> 1) * 32 + (2 * c4 + h) * 4 + (g8 & 1);
-                        xa[pp][h] = lds1(at) * 0x00800080u;
-                        xb[pp][h] = lds1(at + 2) * 0x00800080u;
-                    }
-                }
+                    for (int pp = 0; pp < PG; pp++) {
+                        const uint32_t page = unit + (p0 + pp) * kQPageBytes;
+                        const uint4 ka = lds16(page + tk * 64 + c4 * 16), kb = lds16(page + (tk + 2) * 64 + c4 * 16);
+                        wa[pp][0] = ka.x, wa[pp][1] = ka.y, wa[pp][2] = ka.z, wa[pp][3] = ka.w;
+                        wb[pp][0] = kb.x, wb[pp][1] = kb.y, wb[pp][2] = kb.z, wb[pp][3] = kb.w;
 #pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t ha[kPP][4], hb[kPP][4];
-#pragma unroll
-                    for (int pp = 0; pp < kPP; pp++) {
-                        unpack8(wa[pp][w], ha[pp]);
-                        unpack8(wb[pp][w], hb[pp]);
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            ha[pp][k] = hmul2(ha[pp][k], xa[pp][w >> 1]);
-                            hb[pp][k] = hmul2(hb[pp][k], xb[pp][w >> 1]);
+                        for (int h = 0; h < 2; h++) {
+                            // the scale's f16 (times 2^-8) in both halves
+                            const uint32_t at = page + kQKScale + (g8 >> 1) * 32 + (2 * c4 + h) * 4 + (g8 & 1);
+                            xa[pp][h] = lds1(at) * 0x00800080u;
+                            xb[pp][h] = lds1(at + 2) * 0x00800080u;
                         }
                     }
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        uint32_t f[4];
-                        if (QREG) {
+                    for (int w = 0; w < 4; w++) {
+                        uint32_t ha[PG][4], hb[PG][4];
 #pragma unroll
-                            for (int k = 0; k < 4; k++) f[k] = qf[nt][4 * w + k];
-                        } else {
-                            const uint4 v = lds16(ring + STAGES * kUnitBytes + ((nt * 4 + w) * 32 + lane) * 16);
-                            f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+                        for (int pp = 0; pp < PG; pp++) {
+                            unpack8(wa[pp][w], ha[pp]);
+                            unpack8(wb[pp][w], hb[pp]);
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                ha[pp][k] = hmul2(ha[pp][k], xa[pp][w >> 1]);
+                                hb[pp][k] = hmul2(hb[pp][k], xb[pp][w >> 1]);
+                            }
                         }
 #pragma unroll
-                        for (int k = 0; k < 2; k++)
+                        for (int nt = 0; nt < NT; nt++) {
+                            uint32_t f[4];
+                            if (QREG) {
 #pragma unroll
-                            for (int pp = 0; pp < kPP; pp++)
-                                mma_f16(s[pp][nt], ha[pp][2 * k], hb[pp][2 * k], ha[pp][2 * k + 1], hb[pp][2 * k + 1],
-                                        f[2 * k], f[2 * k + 1]);
+                                for (int k = 0; k < 4; k++) f[k] = qf[nt][4 * w + k];
+                            } else {
+                                const uint4 v = lds16(ring + STAGES * kUnitBytes + ((nt * 4 + w) * 32 + lane) * 16);
+                                f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 2; k++)
+#pragma unroll
+                                for (int pp = 0; pp < PG; pp++)
+                                    mma_f16(s[p0 + pp][nt], ha[pp][2 * k], hb[pp][2 * k], ha[pp][2 * k + 1],
+                                            hb[pp][2 * k + 1], f[2 * k], f[2 * k + 1]);
+                        }
                     }
                 }
                 if (tail) {
@@ -545,20 +551,19 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         x[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
 #pragma unroll
                         for (int pp = 1; pp < kPP; pp++) x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
-                        moves |= x[nt][h] > top_raw[nt][h];
+                        moves |= x[nt][h] * sc > ref[nt][h] + kMargin;
                     }
                 if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            float y = x[nt][h] * sc[nt][h];
+                            float y = x[nt][h] * sc;
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
                             y = fmaxf(ref[nt][h], y);
                             const float f = ref[nt][h] == -CUDART_INF_F ? 0.f : ex2_approx(ref[nt][h] - y);
                             ref[nt][h] = y;
-                            top_raw[nt][h] = (y + kMargin) / sc[nt][h];
                             sum[nt][h] *= f;
 #pragma unroll
                             for (int j = 0; j < 8; j++) {
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         float p[4];
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            p[k] = ex2_approx(fmaf(s[pp][nt][k], sc[nt][k & 1], base[k & 1]));
+                            p[k] = ex2_approx(fmaf(s[pp][nt][k], sc, base[k & 1]));
                             sum[nt][k & 1] += p[k];
                         }
                         pb[pp][nt][0] = movmatrix_t(f16x2(p[0], p[1]));

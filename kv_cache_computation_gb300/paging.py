@@ -6,7 +6,7 @@ from typing import NamedTuple
 import torch
 
 from . import _native as N
-from .attention import _check, _dev, _on, _out, _stream_ptr, _table
+from .attention import _check, _dev, _on, _stream_ptr, _table
 
 # bits of PageStep.status
 OUT_OF_PAGES, ROW_FULL, OUT_OF_RANGE, TOO_MANY_TOKENS, RING_FULL = 1, 2, 4, 8, 16
@@ -47,12 +47,12 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     ring = _dev(free_pages, "free_pages", torch.int32, (n,), device)
     state = _dev(free_state, "free_state", torch.int32, (2,), device)
     with _on(device, stream):
-        out = (lengths if in_place else _out((B,), device, torch.int32),
-               free_state if in_place else _out((2,), device, torch.int32), _out((B + 1,), device, torch.int32),
-               _out((max_tokens,), device, torch.int32), _out((max_tokens,), device, torch.int32),
-               _out((1,), device, torch.int32))
-        lo, so, starts, pos, slot, status = (t.data_ptr() for t in out)
-        _check("mac_page_step",
-               N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so,
-                                     starts, pos, slot, status, _stream_ptr(stream, device)))
+        new = lengths.new_empty
+        out = (lengths if in_place else new(B), free_state if in_place else new(2), new(B + 1), new(max_tokens),
+               new(max_tokens), new(1))
+        lo, so, starts, pos, slot, status = [t.data_ptr() for t in out]
+        st = N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so, starts, pos, slot,
+                                   status, _stream_ptr(stream, device))
+    if st:
+        _check("mac_page_step", st)
     return PageStep(*out)

@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from . import _native as N
-from .attention import _check, _dev, _on, _out, _stream_ptr
+from .attention import _check, _dev, _on, _stream_ptr
 
 
 def _rows(t, name, heads, head_dim):
@@ -48,12 +48,13 @@ class QkvRotary:
         _check("mac_rope_init", N.lib().mac_rope_init(ctypes.byref(cfg), ctypes.byref(self._rope)))
         self._ref = ctypes.byref(self._rope)
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self._all = heads + 2 * kv_heads
+        self._k_at, self._v_at = 2 * heads * head_dim, 2 * (heads + kv_heads) * head_dim     # bytes into a token's row
 
     def __call__(self, qkv, positions, q_weight=None, k_weight=None, want_pre=True, stream=None):
-        H, Hkv, d = self.heads, self.kv_heads, self.head_dim
-        at, stride = _rows(qkv, "qkv", H + 2 * Hkv, d)
-        return self._run(qkv.shape[0], qkv.device, at, stride, at + 2 * H * d, stride, at + 2 * (H + Hkv) * d, stride,
-                         positions, q_weight, k_weight, want_pre, stream)
+        at, stride = _rows(qkv, "qkv", self._all, self.head_dim)
+        return self._run(qkv, at, stride, at + self._k_at, stride, at + self._v_at, stride, positions, q_weight, k_weight,
+                         want_pre, stream)
 
     def split(self, q, k, v, positions, q_weight=None, k_weight=None, want_pre=True, stream=None):
         """The same from separate projections q [tokens, heads * 128], k and v [tokens, kv_heads * 128]."""
@@ -65,18 +66,21 @@ class QkvRotary:
         qp, qs = _rows(q, "q", self.heads, self.head_dim)
         kp, ks = _rows(k, "k", self.kv_heads, self.head_dim)
         vp, vs = _rows(v, "v", self.kv_heads, self.head_dim)
-        return self._run(T, q.device, qp, qs, kp, ks, vp, vs, positions, q_weight, k_weight, want_pre, stream)
+        return self._run(q, qp, qs, kp, ks, vp, vs, positions, q_weight, k_weight, want_pre, stream)
 
-    def _run(self, T, device, q, qs, k, ks, v, vs, positions, q_weight, k_weight, want_pre, stream):
-        H, Hkv, d = self.heads, self.kv_heads, self.head_dim
+    def _run(self, like, q, qs, k, ks, v, vs, positions, q_weight, k_weight, want_pre, stream):
+        T, device, d = like.shape[0], like.device, self.head_dim
         pos = _dev(positions, "positions", torch.int32, (T,), device)
         wq = None if q_weight is None else _dev(q_weight, "q_weight", torch.bfloat16, (d,), device)
         wk = None if k_weight is None else _dev(k_weight, "k_weight", torch.bfloat16, (d,), device)
+        qshape, kshape = (T, self.heads, d), (T, self.kv_heads, d)
         with _on(device, stream):
-            q_post, k_out, v_out = _out((T, H, d), device), _out((T, Hkv, d), device), _out((T, Hkv, d), device)
-            q_pre = _out((T, H, d), device) if want_pre else None
-            _check("mac_qkv_norm_rope",
-                   N.lib().mac_qkv_norm_rope(self._ref, T, q, qs, k, ks, v, vs, wq, wk, pos,
-                                             None if q_pre is None else q_pre.data_ptr(), q_post.data_ptr(),
-                                             k_out.data_ptr(), v_out.data_ptr(), _stream_ptr(stream, device)))
+            new = like.new_empty
+            q_post, k_out, v_out = new(qshape), new(kshape), new(kshape)
+            q_pre = new(qshape) if want_pre else None
+            status = N.lib().mac_qkv_norm_rope(self._ref, T, q, qs, k, ks, v, vs, wq, wk, pos,
+                                               None if q_pre is None else q_pre.data_ptr(), q_post.data_ptr(),
+                                               k_out.data_ptr(), v_out.data_ptr(), _stream_ptr(stream, device))
+        if status:
+            _check("mac_qkv_norm_rope", status)
         return q_pre, q_post, k_out, v_out
