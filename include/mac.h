@@ -338,8 +338,8 @@ mac_status mac_rope_init(const mac_rope_config *cfg, mac_rope *out);
  * for every query and key head (y = x where w is NULL), then
  *   q_pre = y, q_post = rotated y   (queries),  k_out = rotated y   (keys),
  *   v_out = the values unchanged,
- * computed in fp32 (angles in 64-bit fixed point, exact at any int32
- * position) and rounded to bf16 once.  These are the q_pre, q_post, k_new and
+ * computed in fp32 (angles in 64-bit fixed point, good to 2^-22 rad at any
+ * int32 position) and rounded to bf16 once.  These are the q_pre, q_post, k_new and
  * v_new of mac_decode_step.
  *   dev_q, dev_k, dev_v  bf16, token t's heads at element t * stride (strides
  *                        in elements, multiples of 8, at least the heads'
@@ -424,7 +424,7 @@ mac_status mac_quant_query_sizes(const mac_quant_config *cfg, size_t *store_byte
  * handle, replays of graphs captured from it among them, must be ordered
  * with one another (one stream, or events): they share the scratch.  Handles
  * (the layers of a model) whose calls are ordered may share one scratch
- * buffer. */
+ * buffer; they then share its error word too. */
 mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t store_bytes, void *dev_scratch,
                             size_t scratch_bytes, mac_quant_handle *out);
 

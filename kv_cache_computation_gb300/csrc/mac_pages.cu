@@ -18,6 +18,8 @@
 // old state from all writes of the new, so a caller may update in place.
 // Tokens, new pages and freed pages are then spread over all threads, each
 // finding its request by a binary search in shared memory.
+// Measured in a captured graph: 1 request 4.5 us, 32 requests 4.7, 250 requests
+// 5.3; 65536 packed tokens 8 us (1 request) to 12 us (250).
 #include "../../include/mac.h"
 #include "mac_device.cuh"
 
@@ -29,7 +31,9 @@ namespace {
 
 constexpr int kThreads = 1024;          // one request per thread in the scans
 constexpr int kCluster = 8;             // blocks (a portable cluster size)
-constexpr int kOneBlockTokens = 4096;   // up to this many packed tokens one block does the step
+// Up to this many packed tokens one block does the step.  Both sides, us: 512
+// tokens 5.3 and 5.3, 1024 5.7 / 5.8 (a cluster), 2048 6.4 / 5.7, 16384 16 / 6.4.
+constexpr int kOneBlockTokens = 1024;
 
 struct PageArgs {
     int batch, table_cols, num_pages, max_tokens;

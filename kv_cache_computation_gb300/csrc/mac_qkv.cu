@@ -26,8 +26,8 @@
 // spread over more blocks (gridDim.y splits a token's rows), so that each row of
 // lanes has one to three rows and one token's latency is a single row's.
 // Measured, 32 over 8 heads with norms and pre-rotation queries: 1 token 2.1 us,
-// 37 tokens 2.2, 600 tokens 4.0 (in a captured graph); 32768 tokens 177 us, 6.06
-// TB/s.  8-byte chunks with the sines read from shared memory per row took 195 us;
+// 37 tokens 2.2, 600 tokens 4.0 (in a captured graph); 32768 tokens 176 us, 6.1
+// TB/s, of which 671 MB are writes at 3.8 TB/s (a plain fill reaches 4.03).  8-byte chunks with the sines read from shared memory per row took 195 us;
 // two rows in flight per lane at three blocks per SM beat one (190 us), three
 // (182, two blocks) and six (245).
 #include "../../include/mac.h"
@@ -43,7 +43,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPairs = kD / 2;
-constexpr int kTileTokens = 608;                    // from here on a block takes four tokens
+// A block takes four tokens from kTileRows tokens per row of a token on.  Both
+// sides, us: 48 rows: 608 tokens 4.7 (one token per block) against 5.5, 2048
+// 13.9 / 15.2, 3000 20.3 / 20.4, 8192 53 / 49, 32768 203 / 176; 10 rows: 1024
+// 4.9 / 4.0, 32768 124 / 73.
+constexpr int kTileRows = 60;
+constexpr int kSpreadBlocks = 608;                  // four blocks per SM
 
 struct QkvArgs {
     const __nv_bfloat16 *q, *k, *v;
@@ -295,9 +300,9 @@ extern "C" mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, cons
     for (int i = 0; i < kPairs; i++) t.t[i] = rope->turns[i];
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (n_tokens < kTileTokens) {
+    if (n_tokens < kTileRows * a.rows) {
         // few tokens: one to a block, its rows over as many blocks as keep the grid near four blocks per SM
-        int split = kTileTokens / n_tokens;
+        int split = kSpreadBlocks / n_tokens;
         const int most = (a.rows + 15) / 16;
         split = split < 1 ? 1 : split > most ? most : split;
         e = launch_maybe_pdl(qkv_norm_rope_kernel<16, 1, 3, 4>, dim3(n_tokens, split), dim3(kThreads), 0, s, true, a, t);

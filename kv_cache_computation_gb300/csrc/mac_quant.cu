@@ -9,9 +9,14 @@
 // the conversion.  A tie between two e2m1 values is x = t s with t in {0.25,
 // ..., 5}; x has 8 significant bits and t s at most 7, so a quotient that is no
 // tie is off it by at least 2^-9 of it (2^-11), while x * (1 / s) is within
-// 2^-22 of it: the rounding puts ties back on the tie and
-// moves nothing across one.  A division per element would cost more than the
-// rest of the kernel together.
+// 2^-22 of it: the rounding puts ties back on the tie and moves nothing across
+// one.  A division per element would cost more than the rest of the kernel.
+//
+// What bounds them, 32768 tokens of 8 heads: the append (134 MB in, 38 MB out)
+// 32.6 us, 5.3 TB/s, the loads' latency at half occupancy (four tokens' blocks
+// per lane; three or six blocks per SM instead of four: 36 and 40 us); the gather
+// (38 MB in, 134 MB out) 33 us, 4.07 TB/s of writes, which is what a plain fill
+// reaches (4.03).  8 tokens: 1.7 and 1.5 us in a captured graph, launch and latency.
 #include "../../include/mac.h"
 #include "mac_device.cuh"
 #include "mac_quant.cuh"
@@ -30,7 +35,10 @@ namespace macgpu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kQuadTokens = 512;    // from here on a lane takes four tokens: below, one block per lane spreads further
+// From this many (token, head) pairs on a lane takes four tokens; below, one
+// block per lane spreads further.  Both sides, us, 8 heads: 512 tokens 2.2 (one
+// block) against 2.8, 1024 2.6 / 2.9, 2048 3.8 / 3.6; 32768 43 / 30 (append).
+constexpr int64_t kQuadPairs = 16384;
 
 // two e2m1 codes (lo in the low four bits) of two floats, ties to even, at most 6
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi)
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_const
 // value codes two 16-byte vectors, and a warp's stores cover whole sectors;
 // elsewhere each token goes by itself, as above.
 template <bool kGather>
-__global__ void __launch_bounds__(kThreads) quant_quads_kernel(const __grid_constant__ MoveArgs a)
+__global__ void __launch_bounds__(kThreads, 4) quant_quads_kernel(const __grid_constant__ MoveArgs a)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31, j = lane & 7, c = lane >> 3, Hkv = a.st.kv_heads;
@@ -380,7 +388,7 @@ mac_status launch_move(mac_quant_ctx *h, bool gather, MoveArgs a, void *stream)
     a.st = h->st;
     const int Hkv = h->cfg.kv_heads;
     a.rows = 2 * (int64_t)a.n_tokens * Hkv;
-    const bool quads = a.n_tokens >= kQuadTokens;
+    const bool quads = (int64_t)a.n_tokens * Hkv >= kQuadPairs;
     const int64_t threads = quads ? 2 * ((int64_t)(a.n_tokens + kPage - 1) / kPage) * Hkv * 32 : a.rows * 8;
     const auto kernel = quads ? (gather ? quant_quads_kernel<true> : quant_quads_kernel<false>)
                               : (gather ? quant_rows_kernel<true> : quant_rows_kernel<false>);
@@ -445,8 +453,9 @@ mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t
     good = good && prop.major * 10 + prop.minor == 103;
     if (good) {
         h->sm_count = prop.multiProcessorCount;
-        // an unwritten slot reads back as zeros
-        good = quant_attention_config(h->sm_count) == cudaSuccess && cudaMemset(dev_store, 0, z.store) == cudaSuccess &&
+        // an unwritten slot reads back as zeros; work in flight may still use a shared scratch or a recycled buffer
+        good = quant_attention_config(h->sm_count) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess &&
+               cudaMemset(dev_store, 0, z.store) == cudaSuccess &&
                cudaMemset(dev_scratch, 0, z.scratch) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
     }
     if (!good) {

@@ -24,18 +24,38 @@
 //    its V words one 16-element block of four consecutive tokens (four scales),
 //    whose codes are paired by token with two logic operations per eight codes.
 // Roundings: Q is bf16 and becomes f16 with a power of two per group (exact but
-// for elements below 2^-28 of the group's largest, which keep 2^-39 of it); stored values are exact in
-// f16; the weights P, at most 2^15, are rounded to f16 (2^-11 of each) and
-// summed unrounded in fp32; sums, the maximum and the output stay in fp32.
-// P's factor 2^9 keeps weights down to 2^-33 of the largest.
+// for elements below 2^-28 of the group's largest, which keep 2^-39 of it);
+// stored values are exact in f16; the weights P, at most 2^15, are rounded to
+// f16 (2^-11 of each; P's factor 2^9 keeps weights down to 2^-33 of the largest)
+// and summed unrounded in fp32; scores, sums, the reference and the output stay
+// in fp32.
 //
 // Work split.  The units (two pages) of all (request, KV head) groups form one
-// line, which is cut into equal ranges, one per warp team, whatever the
-// lengths; the cut is derived in every block from the lengths on the device, so
-// a captured call serves any lengths.  A group inside one team's range is
-// finished by it.  The pieces of the others are parked, merged per block, and,
-// where a group crosses blocks, merged again by a second kernel (one block per
-// crossing group and row).  No block waits for another.
+// line, which is cut into equal ranges, one per warp, whatever the lengths; the
+// cut is derived in every block from the lengths on the device, so a captured
+// call serves any lengths, and it is fixed by them, so a call repeats bit for
+// bit.  A group inside one warp's range is finished by it.  The pieces of the
+// others are parked, merged per block, and, where a group crosses blocks, merged
+// again by a second kernel.  No block waits for another.
+//
+// Measured (GB300, 128-element heads, stream in TB/s of the copy peak 6.7):
+//   rows  8 KV heads x 8 x 128K (1208 MB)  205 us  5.9   283 instructions a page
+//         8 KV heads x 1 x 128K (151 MB)    37 us  4.0
+//         8 KV heads x 1 x 4K                12 us (in a captured graph)
+//    16   1 KV head  x 8 x 128K (151 MB)    53 us  2.9
+//    24                                     64 us  2.4
+//    32                                     76 us  2.0   494 instructions a page
+// At 8 rows the ALU (half rate: a conversion takes two cycles) is 55 % busy and
+// the memory 75 % of nominal; what is left is the spread of the SMs (165 to 201
+// us) and, for a single request, the fixed chain: prologue 1.5 us, first page 1,
+// the last units' spread 3 to 5, merge 2, second kernel 4.  Beyond 8 rows a warp's
+// 64 to 128 output registers leave 12 and 8 warps per SM, whose dependent
+// instructions are not hidden (tensor pipe 27 % and 39 % busy).
+// Tried and slower: units of one page at 16 (248 us) or 20 warps (263); 20 warps
+// with spills (246); the next unit's scores in one block with this unit's
+// output (212 against 207); two warps per page with 16 rows each (84 us at 32
+// rows); values by head block across lanes, which needs sixteen scale pairs per
+// lane and page instead of two (240).
 #include "mac_device.cuh"
 #include "mac_quant.cuh"
 

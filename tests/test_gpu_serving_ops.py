@@ -32,7 +32,9 @@ def _check_rope(got, y, what, mag):
 @pytest.mark.parametrize("T,H,Hkv,rotary,inter,norm,pos0", [
     (1, 32, 8, 128, False, True, 0), (1, 1, 1, 128, True, True, 131071), (3, 28, 4, 64, False, True, 7),
     (37, 32, 4, 96, True, True, 1000), (5, 6, 3, 0, False, True, 5), (2, 64, 8, 8, False, False, 2 ** 31 - 3),
-    (607, 4, 2, 128, False, True, 100000), (608, 5, 5, 40, True, True, 3), (1031, 32, 8, 128, False, True, 122880),
+    (479, 4, 2, 128, False, True, 100000), (480, 4, 2, 128, False, True, 100000), (901, 5, 5, 40, True, True, 3),
+    (1031, 32, 8, 128, False, True, 122880), (2881, 32, 8, 128, False, True, 7), (1203, 8, 4, 112, False, True, 9),
+    (1203, 8, 4, 96, True, False, 9),
     (4, 32, 1, 128, False, True, -9)])
 def test_norm_rope(T, H, Hkv, rotary, inter, norm, pos0):
     from kv_cache_computation_gb300 import QkvRotary
@@ -192,7 +194,8 @@ def _slots(n, pages, seed):
 
 
 @pytest.mark.parametrize("T,Hkv,pages,ks,vs", [(1, 1, 1, 1.0, 1.0), (5, 8, 3, 1.0, 4.0), (64, 3, 4, 0.25, 1.0),
-                                               (333, 2, 40, 1.0, 2.0 ** -20), (2048, 8, 128, 1.0, 1.0)])
+                                               (333, 2, 40, 1.0, 2.0 ** -20), (2048, 8, 128, 1.0, 1.0),
+                                               (5463, 3, 342, 1.0, 1.0)])
 def test_store_round_trip_is_the_format(T, Hkv, pages, ks, vs):
     from kv_cache_computation_gb300 import QuantKV
     cache = QuantKV(Hkv, Hkv, num_pages=pages, k_scale=ks, v_scale=vs)
@@ -219,8 +222,8 @@ def test_store_round_trip_is_the_format(T, Hkv, pages, ks, vs):
         assert (gk == 0).all() and (gv == 0).all()
 
 
-@pytest.mark.parametrize("first,T,pages", [(0, 64, 9), (0, 40, 9), (3, 61, 9), (16, 16, 9), (5, 7, 9), (0, 640, 41),
-                                           (4, 513, 41), (7, 600, 41), (0, 641, 41)])
+@pytest.mark.parametrize("first,T,pages", [(0, 64, 9), (0, 40, 9), (3, 61, 9), (16, 16, 9), (5, 7, 9), (0, 8208, 514),
+                                           (4, 8193, 514), (7, 8195, 514), (0, 8209, 514)])
 def test_store_whole_pages(first, T, pages):
     """Runs of consecutive tokens through pages in any order, starting and ending inside a page, beside other tokens of
     the same pages that stay as they are."""
