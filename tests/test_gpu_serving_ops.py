@@ -265,6 +265,29 @@ def test_store_strides_nonfinite_and_bad_slots():
     assert torch.isnan(gv[2, 0, 16:32]).all() and torch.isfinite(gv[2, 1]).all()
 
 
+def test_store_beyond_32_bit_offsets():
+    """A store of 5.5 GB: slots in its last pages are stored, read and attended like any other."""
+    from kv_cache_computation_gb300 import QuantKV
+    pages, Hkv, n = 300_000, 8, 50
+    cache = QuantKV(16, Hkv, num_pages=pages)
+    assert cache.sizes["store"] > 5 * 2 ** 30
+    table = torch.tensor([[pages - 1, 3, pages - 70_000, pages - 2]], dtype=torch.int32)
+    t = torch.arange(n)
+    slots = (table[0, t // 16] * 16 + t % 16).to(torch.int32)
+    k, v, q = _randn((n, Hkv, 128), 1), _randn((n, Hkv, 128), 2), _randn((1, 16, 128), 3)
+    cache.append(k.cuda(), v.cuda(), slots.cuda())
+    gk, gv = cache.gather(slots.cuda())
+    K, V = R.stored(k.double().numpy()), R.stored(v.double().numpy())
+    np.testing.assert_array_equal(gk.double().cpu().numpy(), K)
+    np.testing.assert_array_equal(gv.double().cpu().numpy(), V)
+    out, lse = cache.attention(q.cuda(), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda())
+    cache.sync()
+    o, l, mag, top = R.attention(q.double().numpy(), K, V, 1 / np.sqrt(128))
+    to, tl = R.attention_tolerance(o, mag, top, l, n)
+    assert (np.abs(out.double().cpu().numpy() - o) <= to).all()
+    assert (np.abs(lse.double().cpu().numpy() - l) <= tl).all()
+
+
 # ---- attention over the store -------------------------------------------------------
 
 class Case:
