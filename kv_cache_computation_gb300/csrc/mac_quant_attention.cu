@@ -700,14 +700,15 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     __threadfence_block();
     __syncthreads();
 
-    // Merge the parked pieces group by group, a warp per row.  Lane i looks at
-    // piece i; a run of pieces of one group starts where the group differs
+    // Merge the parked pieces group by group; the rows of all groups go round the
+    // warps.  Lane i looks at piece i; a run of pieces of one group starts where the group differs
     // from the piece before it.
     const int mine = lane < 2 * TEAMS ? sm.piece_group[lane] : -1;
     const uint32_t parked = __ballot_sync(0xffffffffu, mine >= 0);
     const uint32_t below = parked & ((1u << lane) - 1u);
     const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
     uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+    int turn = team;        // the warp's next row of the run
     while (starts) {
         const int first = __ffs(starts) - 1;
         starts &= starts - 1;
@@ -718,7 +719,8 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         const long long start = sm.pre[b] * Hkv + g * n_units;
         const bool whole = start >= sm.lo && start + n_units <= sm.hi;
         if (whole && tid == 0 && meta_by_group(a, gridDim.x)) a.meta[grp] = make_int4(-1, 0, 0, 0);
-        for (int r = team; r < a.rows; r += TEAMS) {
+        int r = turn;
+        for (; r < a.rows; r += TEAMS) {
             float2 ml = make_float2(-CUDART_INF_F, 0.f);
             if (run >> lane & 1) ml = lane & 1 ? *parked_ml(lane >> 1, r) : a.part_ml[first_row(lane >> 1, r)];
             const bool none = ml.y == 0.f;      // saw no token
@@ -747,6 +749,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 if (lane == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
+        turn = r - a.rows;
     }
 }
 
