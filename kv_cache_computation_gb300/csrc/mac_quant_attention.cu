@@ -57,9 +57,7 @@
 // rows); values by head block across lanes, which needs sixteen scale pairs per
 // lane and page instead of two (240).
 #include "mac_device.cuh"
-#include "mac_quant.cuh"
-
-#include <cuda_fp16.h>
+#include "mac_quant_line.cuh"
 
 namespace macgpu {
 
@@ -68,18 +66,9 @@ namespace {
 constexpr int kPP = 2;                                  // pages per unit
 constexpr int kUnitTok = kPP * kPage;
 constexpr int kUnitBytes = kPP * kQPageBytes;
-constexpr float kMargin = 6.f;                          // log2: how far a score may pass the softmax reference
-constexpr float kPShift = 9.f;                          // P is held times 2^kPShift: 2^(6 + 9) is below the f16 maximum
 constexpr uint32_t kSpinLimit = 1u << 22;
 constexpr int kMaxPieces = 32;
 constexpr int kParkRow = kD + 4;                        // floats per parked row: its output and summary, padded
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
-                 :: "r"(dst), "l"(src), "r"(bytes), "r"(mbar)
-                 : "memory");
-}
 
 __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity)
 {
@@ -103,65 +92,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// two floats as f16x2, x in the low half
-__device__ __forceinline__ uint32_t f16x2(float x, float y)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
-    return r;
-}
-
-// eight codes -> four f16x2, one per byte
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&h)[4])
-{
-    asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\ncvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4])
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds4(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void sts4(uint32_t addr, uint32_t v)
-{
-    asm volatile("st.shared.u32 [%0], %1;\n" :: "r"(addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds1(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// Units of request b: two pages each, one for an empty request (its output
-// still has to be written).
-__device__ __forceinline__ int units_of(int len) { return len > kUnitTok ? (len - 1) / kUnitTok + 1 : 1; }
-
 // A warp's shared memory: its ring and, where Q does not stay in registers, Q;
 // at the end the piece it parks.
 __host__ __device__ constexpr int team_bytes(int nt, int stages, bool qreg)
@@ -170,31 +100,13 @@ __host__ __device__ constexpr int team_bytes(int nt, int stages, bool qreg)
     return run > parked ? run : parked;
 }
 
-// Where the second kernel finds its groups: with no more groups than blocks in
-// meta[group], else in meta[the block in which the group starts].
-__host__ __device__ inline bool meta_by_group(const QuantAttnArgs &a, int grid) { return (int64_t)a.batch * a.st.kv_heads <= grid; }
-
 struct Smem {
-    long long pre[kQMaxBatch + 1];      // units of the requests before b (per KV head)
-    int len[kQMaxBatch];
-    long long scan[32];
+    Line line;
     long long lo, hi;                   // the block's units
     // parked pieces of the block, in order: their group (-1: none)
     int piece_group[kMaxPieces];
     unsigned long long bar[64];
 };
-
-// The request that holds a unit of the line: the last b with pre[b] * Hkv <= unit.
-__device__ __forceinline__ int request_of(const Smem &sm, int batch, int Hkv, long long unit)
-{
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sm.pre[mid] * Hkv <= unit) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
 
 // Writes a row's finished output (four elements at d0) and its lse.
 __device__ __forceinline__ void finish4(const QuantAttnArgs &a, int b, int g, int r, int d0, float4 o, float m, float l,
@@ -239,11 +151,6 @@ __device__ __forceinline__ uint32_t finite_top(const uint32_t (&w)[16], uint32_t
     return top;
 }
 
-__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t two, float up)
-{
-    return f16x2(__uint_as_float(two << 16) * up, __uint_as_float(two & 0xffff0000u) * up);
-}
-
 // NT: N tiles (8 rows each), TEAMS warps per block, STAGES units in a warp's
 // ring.  Up to 16 rows a lane keeps its part of Q in registers, beyond that in
 // shared memory (one 16-byte load per tile serves both pages of a unit).
@@ -262,42 +169,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     pdl_wait();
     pdl_launch_dependents();
 
-    // lengths, and the prefix of the requests' units
-    {
-        const long long cap = (long long)a.table_cols * kPage;
-        long long carry = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += TEAMS * 32) {
-            const int b = b0 + tid;
-            int len = 0;
-            if (b < a.batch) {
-                len = a.lens[b];
-                if (len < 0 || len > cap) {
-                    if (blockIdx.x == 0) atomicOr(a.st.err, kQErrLen);
-                    len = len < 0 ? 0 : (int)cap;
-                }
-                sm.len[b] = len;
-            }
-            long long x = b < a.batch ? units_of(len) : 0;
-            const long long own = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (lane == 31) sm.scan[team] = x;
-            __syncthreads();
-            long long before = carry, all = carry;
-#pragma unroll
-            for (int w = 0; w < TEAMS; w++) {
-                if (w < team) before += sm.scan[w];
-                all += sm.scan[w];
-            }
-            if (b < a.batch) sm.pre[b] = before + x - own;
-            carry = all;
-            __syncthreads();
-        }
-        if (tid == 0) sm.pre[a.batch] = carry;
-    }
+    make_line<TEAMS, kUnitTok>(a, sm.line);
     const uint32_t bar0 = smem_u32(&sm.bar[team * STAGES]);
     const uint32_t ring = smem_u32(dyn) + (uint32_t)team * TEAM_BYTES;
     if (tid == 0) {
@@ -309,7 +181,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
     __syncthreads();
 
     // the block's and the warp's range of units
-    const long long U = sm.pre[a.batch] * Hkv;
+    const long long U = sm.line.pre[a.batch] * Hkv;
     // every warp of an active block has work: blocks beyond that stay idle
     const long long most = U >= TEAMS ? U / TEAMS : 1;
     const int grid = most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
@@ -319,13 +191,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         if (tid == 0 && !by_group) a.meta[cta] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const int teams = grid * TEAMS, me = cta * TEAMS + team;
-    // the first unit of warp i of the grid, floor(U i / teams): the remainder's share fits 32 bits, and U almost always
-    const long long per = U >> 32 ? U / teams : (long long)((uint32_t)U / (uint32_t)teams);
-    const uint32_t rest = (uint32_t)(U - per * teams);
-    auto first_unit = [&](int i) { return per * i + (long long)(rest * (uint32_t)i / (uint32_t)teams); };
-    const long long lo = first_unit(me), hi = first_unit(me + 1);
-    const long long cta_lo = first_unit(cta * TEAMS), cta_hi = first_unit((cta + 1) * TEAMS);
+    const Cut cut(U, grid * TEAMS);
+    const long long lo = cut.first(cta * TEAMS + team), hi = cut.first(cta * TEAMS + team + 1);
+    const long long cta_lo = cut.first(cta * TEAMS), cta_hi = cut.first((cta + 1) * TEAMS);
     if (tid == 0) {
         sm.lo = cta_lo;     // for the merge behind the long loop
         sm.hi = cta_hi;
@@ -339,31 +207,26 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
 
     if (lo < hi) {
         int left = (int)(hi - lo);      // units to go
-        int b = request_of(sm, a.batch, Hkv, lo);
-        int n_units = (int)(sm.pre[b + 1] - sm.pre[b]);
-        const long long in = lo - sm.pre[b] * Hkv;      // below Hkv * n_units
-        int g = in >> 32 ? (int)(in / n_units) : (int)((uint32_t)in / (uint32_t)n_units);
-        int u0 = (int)(in - (long long)g * n_units);
+        int b, g, u0, n_units;
+        locate(a, sm.line, lo, b, g, u0, n_units);
 
         // The copies run ahead of the reading over the same units: ld_group units of (ld_b, ld_g) to go, tokens from
         // the next unit on in the request, and the lane's page id of that unit, read one unit ahead.
         const size_t page_stride = (size_t)Hkv * kQPageBytes;
-        int ld_left = left, ld_b = b, ld_g = g, ld_group = n_units - u0, ld_tok = sm.len[b] - u0 * kUnitTok;
+        int ld_left = left, ld_b = b, ld_g = g, ld_group = n_units - u0, ld_tok = sm.line.len[b] - u0 * kUnitTok;
         const int32_t *ld_ids = a.table + (int64_t)b * a.table_stride + u0 * kPP + lane;
         int next_id = 0;
         auto fetch = [&]() {
             next_id = 0;
-            if (lane < kPP && lane * kPage < ld_tok) {
-                next_id = *ld_ids;
-                if ((unsigned)next_id >= (unsigned)a.st.num_pages) {
-                    atomicOr(a.st.err, kQErrPage);
-                    next_id = 0;        // stays inside the store; the request's output is wrong
-                }
-            }
+            if (lane < kPP && lane * kPage < ld_tok) next_id = *ld_ids;     // checked where it is used, when it has arrived
         };
         auto issue = [&](int s) {
             if (ld_left == 0) return;
             const uint32_t bar = bar0 + 8 * s;
+            if ((unsigned)next_id >= (unsigned)a.st.num_pages) {
+                atomicOr(a.st.err, kQErrPage);
+                next_id = 0;            // stays inside the store; the request's output is wrong
+            }
             const int pages = ld_tok > kPage ? 2 : ld_tok > 0 ? 1 : 0;
             if (lane == 0)
                 asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n"
@@ -379,8 +242,8 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                     ld_g = 0;
                     ld_b++;
                 }
-                ld_group = (int)(sm.pre[ld_b + 1] - sm.pre[ld_b]);
-                ld_tok = sm.len[ld_b];
+                ld_group = (int)(sm.line.pre[ld_b + 1] - sm.line.pre[ld_b]);
+                ld_tok = sm.line.len[ld_b];
                 ld_ids = a.table + (int64_t)ld_b * a.table_stride + lane;
             } else {
                 ld_tok -= kUnitTok;
@@ -395,21 +258,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
 
         // while the first pages arrive: the group that starts in this block and runs on behind it, for the second kernel
         // (the last warp of a block always has a unit)
-        if (team == TEAMS - 1 && lane == 0) {
-            const int ob = request_of(sm, a.batch, Hkv, cta_hi - 1);
-            const long long on = sm.pre[ob + 1] - sm.pre[ob], off = cta_hi - 1 - sm.pre[ob] * Hkv;
-            const int og = off >> 32 ? (int)(off / on) : (int)((uint32_t)off / (uint32_t)on);
-            const long long start = sm.pre[ob] * Hkv + og * on, end = start + on;
-            int owner = -1, last = 0;
-            if (start >= cta_lo && end > cta_hi) {
-                owner = ob * Hkv + og;
-                // the block that holds the group's last unit: a float guess, put right by the exact ranges
-                last = min(grid - 1, (int)((float)(end - 1) / (float)U * (float)grid));
-                while (first_unit(last * TEAMS) >= end) last--;
-                while (first_unit((last + 1) * TEAMS) < end) last++;
-            }
-            if (owner >= 0 || !by_group) a.meta[by_group ? owner : cta] = make_int4(owner, last, cta, 0);
-        }
+        if (team == TEAMS - 1 && lane == 0) write_meta(a, sm.line, cut, U, grid, TEAMS, cta_lo, cta_hi);
 
         int stage = 0;
         uint32_t phase = 0;
@@ -417,7 +266,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         while (left > 0) {
             // one piece: units [u0, u0 + n) of group (b, g)
             const int n = min(left, n_units - u0);
-            const int len = sm.len[b];
+            const int len = sm.line.len[b];
             const int full = max(len - (a.n_query - 1), 0);     // tokens every row sees
             uint32_t qf[QREG ? NT : 1][16];
             float ref[NT][2], sum[NT][2], o[NT][8][4];
@@ -693,7 +542,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             u0 = 0;
             if (++g == Hkv) {
                 g = 0;
-                if (++b < a.batch) n_units = (int)(sm.pre[b + 1] - sm.pre[b]);
+                if (++b < a.batch) n_units = (int)(sm.line.pre[b + 1] - sm.line.pre[b]);
             }
         }
     }
@@ -715,8 +564,8 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         const uint32_t run = parked & ~((1u << first) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
         const int grp = __shfl_sync(0xffffffffu, mine, first);
         const int b = grp / Hkv, g = grp - b * Hkv;
-        const long long n_units = sm.pre[b + 1] - sm.pre[b];
-        const long long start = sm.pre[b] * Hkv + g * n_units;
+        const long long n_units = sm.line.pre[b + 1] - sm.line.pre[b];
+        const long long start = sm.line.pre[b] * Hkv + g * n_units;
         const bool whole = start >= sm.lo && start + n_units <= sm.hi;
         if (whole && tid == 0 && meta_by_group(a, gridDim.x)) a.meta[grp] = make_int4(-1, 0, 0, 0);
         int r = turn;
