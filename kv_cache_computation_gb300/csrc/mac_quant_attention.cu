@@ -151,6 +151,88 @@ __device__ __forceinline__ uint32_t finite_top(const uint32_t (&w)[16], uint32_t
     return top;
 }
 
+// Partial rows in the scratch: every block's two crossing groups, then every
+// team's first piece.  A team's last piece is parked in its own shared memory,
+// which it has read to the end by then.
+struct Parking {
+    unsigned char *smem;
+    int team_bytes, teams, padrows;
+    __device__ __forceinline__ int64_t crossing_row(int which, int r) const
+    {
+        return ((int64_t)blockIdx.x * 2 + which) * padrows + r;
+    }
+    __device__ __forceinline__ int64_t first_row(int t, int r) const
+    {
+        return ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * teams + t) * padrows + r;
+    }
+    __device__ __forceinline__ float *last_o(int t, int r) const
+    {
+        return reinterpret_cast<float *>(smem + (size_t)t * team_bytes) + r * kParkRow;
+    }
+    __device__ __forceinline__ float2 *last_ml(int t, int r) const { return reinterpret_cast<float2 *>(last_o(t, r) + kD); }
+};
+
+// Behind the long loop: all warps of the block (WARPS, in TEAMS teams).
+template <int TEAMS, int WARPS>
+__device__ __forceinline__ void merge_pieces(const QuantAttnArgs &a, const Smem &sm, const Parking &park)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hkv = a.st.kv_heads;
+    __threadfence_block();
+    __syncthreads();
+
+    // Merge the parked pieces group by group; the rows of all groups go round the
+    // warps.  Lane i looks at piece i; a run of pieces of one group starts where the group differs
+    // from the piece before it.
+    const int mine = lane < 2 * TEAMS ? sm.piece_group[lane] : -1;
+    const uint32_t parked = __ballot_sync(0xffffffffu, mine >= 0);
+    const uint32_t below = parked & ((1u << lane) - 1u);
+    const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
+    uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
+    int turn = warp;        // the warp's next row of the run
+    while (starts) {
+        const int first = __ffs(starts) - 1;
+        starts &= starts - 1;
+        const uint32_t run = parked & ~((1u << first) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
+        const int grp = __shfl_sync(0xffffffffu, mine, first);
+        const int b = grp / Hkv, g = grp - b * Hkv;
+        const long long n_units = sm.line.pre[b + 1] - sm.line.pre[b];
+        const long long start = sm.line.pre[b] * Hkv + g * n_units;
+        const bool whole = start >= sm.lo && start + n_units <= sm.hi;
+        if (whole && tid == 0 && meta_by_group(a, gridDim.x)) a.meta[grp] = make_int4(-1, 0, 0, 0);
+        int r = turn;
+        for (; r < a.rows; r += WARPS) {
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (run >> lane & 1) ml = lane & 1 ? *park.last_ml(lane >> 1, r) : a.part_ml[park.first_row(lane >> 1, r)];
+            const bool none = ml.y == 0.f;      // saw no token
+            const float m = warp_max(none ? -CUDART_INF_F : ml.x);
+            // a NaN sum survives: its weight is a number or NaN, and the product NaN
+            const float w = none ? 0.f : exp2f(ml.x - m);
+            const float l = warp_sum(none ? 0.f : ml.y * w);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t rest_of = __ballot_sync(0xffffffffu, !none);
+            while (rest_of) {
+                const int i = __ffs(rest_of) - 1;
+                rest_of &= rest_of - 1;
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float *src = i & 1 ? park.last_o(i >> 1, r) : a.part_o + park.first_row(i >> 1, r) * kD;
+                const float4 x = reinterpret_cast<const float4 *>(src)[lane];
+                o.x += x.x * wi;
+                o.y += x.y * wi;
+                o.z += x.z * wi;
+                o.w += x.w * wi;
+            }
+            if (whole) {
+                finish4(a, b, g, r, lane * 4, o, m, l, lane == 0);
+            } else {
+                const int64_t at = park.crossing_row(start < sm.lo ? 0 : 1, r);
+                reinterpret_cast<float4 *>(a.part_o + at * kD)[lane] = o;
+                if (lane == 0) a.part_ml[at] = make_float2(m, l);
+            }
+        }
+        turn = r - a.rows;
+    }
+}
+
 // NT: N tiles (8 rows each), TEAMS warps per block, STAGES units in a warp's
 // ring.  Up to 16 rows a lane keeps its part of Q in registers, beyond that in
 // shared memory (one 16-byte load per tile serves both pages of a unit).
@@ -198,12 +280,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
         sm.lo = cta_lo;     // for the merge behind the long loop
         sm.hi = cta_hi;
     }
-    // partial rows: the block's two crossing groups, then its warps' first pieces.  A warp's last piece is parked in
-    // its own shared memory, which it has read to the end by then.
-    auto crossing_row = [&](int which, int r) { return ((int64_t)blockIdx.x * 2 + which) * PADROWS + r; };
-    auto first_row = [&](int t, int r) { return ((int64_t)gridDim.x * 2 + (int64_t)blockIdx.x * TEAMS + t) * PADROWS + r; };
-    auto parked_o = [&](int t, int r) { return reinterpret_cast<float *>(dyn + (size_t)t * TEAM_BYTES) + r * kParkRow; };
-    auto parked_ml = [&](int t, int r) { return reinterpret_cast<float2 *>(parked_o(t, r) + kD); };
+    const Parking park{dyn, TEAM_BYTES, TEAMS, PADROWS};
 
     if (lo < hi) {
         int left = (int)(hi - lo);      // units to go
@@ -529,13 +606,13 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         if (a.lse && g8 == 0)
                             a.lse[row] = l == 0.f ? -CUDART_INF_F : (ref[nt][h] - kPShift + log2f(l)) * kLn2;
                     } else {
-                        const int64_t row = first_row(team, r);
-                        float *dst = which ? parked_o(team, r) : a.part_o + row * kD;
+                        const int64_t row = park.first_row(team, r);
+                        float *dst = which ? park.last_o(team, r) : a.part_o + row * kD;
 #pragma unroll
                         for (int j = 0; j < 8; j += 2)
                             *reinterpret_cast<float4 *>(dst + 16 * g8 + 2 * j) =
                                 make_float4(o[nt][j][h], o[nt][j][2 + h], o[nt][j + 1][h], o[nt][j + 1][2 + h]);
-                        if (g8 == 0) *(which ? parked_ml(team, r) : a.part_ml + row) = make_float2(ref[nt][h] - kPShift, l);
+                        if (g8 == 0) *(which ? park.last_ml(team, r) : a.part_ml + row) = make_float2(ref[nt][h] - kPShift, l);
                     }
                 }
             // the next group
@@ -546,60 +623,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             }
         }
     }
-    __threadfence_block();
-    __syncthreads();
-
-    // Merge the parked pieces group by group; the rows of all groups go round the
-    // warps.  Lane i looks at piece i; a run of pieces of one group starts where the group differs
-    // from the piece before it.
-    const int mine = lane < 2 * TEAMS ? sm.piece_group[lane] : -1;
-    const uint32_t parked = __ballot_sync(0xffffffffu, mine >= 0);
-    const uint32_t below = parked & ((1u << lane) - 1u);
-    const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : 0);
-    uint32_t starts = __ballot_sync(0xffffffffu, mine >= 0 && (!below || before != mine));
-    int turn = team;        // the warp's next row of the run
-    while (starts) {
-        const int first = __ffs(starts) - 1;
-        starts &= starts - 1;
-        const uint32_t run = parked & ~((1u << first) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
-        const int grp = __shfl_sync(0xffffffffu, mine, first);
-        const int b = grp / Hkv, g = grp - b * Hkv;
-        const long long n_units = sm.line.pre[b + 1] - sm.line.pre[b];
-        const long long start = sm.line.pre[b] * Hkv + g * n_units;
-        const bool whole = start >= sm.lo && start + n_units <= sm.hi;
-        if (whole && tid == 0 && meta_by_group(a, gridDim.x)) a.meta[grp] = make_int4(-1, 0, 0, 0);
-        int r = turn;
-        for (; r < a.rows; r += TEAMS) {
-            float2 ml = make_float2(-CUDART_INF_F, 0.f);
-            if (run >> lane & 1) ml = lane & 1 ? *parked_ml(lane >> 1, r) : a.part_ml[first_row(lane >> 1, r)];
-            const bool none = ml.y == 0.f;      // saw no token
-            const float m = warp_max(none ? -CUDART_INF_F : ml.x);
-            // a NaN sum survives: its weight is a number or NaN, and the product NaN
-            const float w = none ? 0.f : exp2f(ml.x - m);
-            const float l = warp_sum(none ? 0.f : ml.y * w);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            uint32_t rest_of = __ballot_sync(0xffffffffu, !none);
-            while (rest_of) {
-                const int i = __ffs(rest_of) - 1;
-                rest_of &= rest_of - 1;
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float *src = i & 1 ? parked_o(i >> 1, r) : a.part_o + first_row(i >> 1, r) * kD;
-                const float4 x = reinterpret_cast<const float4 *>(src)[lane];
-                o.x += x.x * wi;
-                o.y += x.y * wi;
-                o.z += x.z * wi;
-                o.w += x.w * wi;
-            }
-            if (whole) {
-                finish4(a, b, g, r, lane * 4, o, m, l, lane == 0);
-            } else {
-                const int64_t at = crossing_row(start < sm.lo ? 0 : 1, r);
-                reinterpret_cast<float4 *>(a.part_o + at * kD)[lane] = o;
-                if (lane == 0) a.part_ml[at] = make_float2(m, l);
-            }
-        }
-        turn = r - a.rows;
-    }
+    merge_pieces<TEAMS, TEAMS>(a, sm, park);
 }
 
 // The groups that cross blocks, merged: block (x, y) has the group of meta[x],
@@ -711,7 +735,7 @@ Variant variant()
 Variant variant_for(int rows)
 {
     if (rows <= 8) return variant<1, 8, 2, 2, true>();
-    if (rows <= 16) return variant<2, 12, 3, 1, true>();
+    if (rows <= 16) return variant<2, 12, 2, 1, true>();
     if (rows <= 24) return variant<3, 8, 3, 1, false>();
     return variant<4, 8, 3, 1, false>();
 }
