@@ -466,15 +466,44 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                     }
                 }
                 if (tail) {
-                    // tokens nobody sees: their value scales may be NaN and are made zero in the ring
+                    // Value scales that may be NaN, whose product with a weight of 0 would be NaN: those of tokens nobody
+                    // sees, and the NaN scales of tokens that some of several queries see, are made zero in the ring.
                     // (lane: word (page, c, block) of the unit's scales, bytes of tokens 0, 2, 1, 3)
+                    int bad = 0x7fffffff;       // the first token of the second kind with such a scale in the lane's block
 #pragma unroll 1
                     for (int k = lane; k < kPP * 32; k += 32) {
-                        const int seen = len - (tok0 + (k >> 5) * kPage + 4 * ((k >> 3) & 3));
+                        const int first = tok0 + (k >> 5) * kPage + 4 * ((k >> 3) & 3), seen = len - first;
                         const uint32_t keep = (seen > 0 ? 0xffu : 0u) | (seen > 2 ? 0xff00u : 0u) |
                                               (seen > 1 ? 0xff0000u : 0u) | (seen > 3 ? 0xff000000u : 0u);
                         const uint32_t at = unit + (k >> 5) * kQPageBytes + kQVScale + (k & 31) * 4;
-                        sts4(at, lds4(at) & keep);
+                        uint32_t sv = lds4(at) & keep;
+                        if (a.n_query > 1) {
+#pragma unroll
+                            for (int t = 3; t >= 0; t--) {
+                                const uint32_t byte = 0xffu << 8 * q_scale_byte(t);
+                                if (first + t >= full && (sv & byte) == byte) {
+                                    sv &= ~byte;
+                                    bad = min(bad, first + t);
+                                }
+                            }
+                        }
+                        sts4(at, sv);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // a later copy writes the same bytes
+                    if (__any_sync(0xffffffffu, bad != 0x7fffffff)) {
+                        // the queries that do see such a token get their NaN here (the lane's outputs are of block g)
+                        bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 8));
+                        bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 16));
+                        bad = __shfl_sync(0xffffffffu, bad, g8);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const int r = nt * 8 + 2 * c4 + h;
+                                if (r >= a.rows || len - (a.n_query - 1) + r / a.G <= bad) continue;
+#pragma unroll
+                                for (int j = 0; j < 8; j++) o[nt][j][h] = o[nt][j][2 + h] = CUDART_NAN_F;
+                            }
                     }
                     __syncwarp();
 #pragma unroll

@@ -410,6 +410,37 @@ def test_attention_nonfinite_tokens_stay_in_their_request():
     c.check(out, lse, requests=[0, 2])
 
 
+@pytest.mark.parametrize("H,Hkv,nq,n,bad", [
+    (2, 1, 4, 40, [(39, 0, 3)]), (8, 2, 3, 34, [(33, 1, 0), (32, 0, 7)]), (4, 1, 4, 18, [(17, 0, 5), (15, 0, 5)]),
+    (4, 4, 2, 33, [(32, 2, 1), (31, 3, 2)]), (7, 1, 3, 700, [(699, 0, 6), (698, 0, 2)]), (2, 1, 16, 20, [(19, 0, 4), (6, 0, 0)]),
+    (4, 2, 2, 2, [(1, 1, 3)])])
+def test_attention_nonfinite_values_of_later_drafts(H, Hkv, nq, n, bad):
+    """A drafted token whose values hold an infinity: the queries before it do not see it and stay finite, those from it
+    on get NaN in the 16 elements that share its scale, and only there."""
+    c = Case([n, 5 + nq], H, Hkv, nq, seed=71)
+    for tok, h, block in bad:
+        k, v = _randn((1, Hkv, 128), 7), _randn((1, Hkv, 128), 8 + tok)
+        v[0, h, 16 * block + 5] = float("inf")
+        slot = torch.tensor([int(c.table[0, tok // 16]) * 16 + tok % 16], dtype=torch.int32).cuda()
+        c.cache.append(k.cuda(), v.cuda(), slot)
+        c.k[0][tok], c.v[0][tok] = R.stored(k.double().numpy())[0], R.stored(v.double().numpy())[0]
+    out, lse = c.run()
+    c.check(out, lse, requests=[1])
+    # the reference with the bad blocks made zero, and where they are seen
+    v = c.v[0]
+    o, l, mag, top = R.attention(c.q[0].double().numpy(), c.k[0], np.nan_to_num(v), c.scale)
+    to, tl = R.attention_tolerance(o, mag, top, l, n)
+    seen = np.zeros(o.shape, bool)
+    for i in range(nq):
+        rows = np.isnan(v[:n - (nq - 1) + i]).any(0)                # [KV head, element]
+        seen[i] = np.repeat(rows, H // Hkv, 0)
+    assert seen.any() and not seen.all()
+    go = out[0].double().cpu().numpy()
+    np.testing.assert_array_equal(np.isnan(go), seen)
+    assert (np.abs(go - o) <= to)[~seen].all()
+    assert (np.abs(lse[0].double().cpu().numpy() - l) <= tl).all()
+
+
 def test_attention_padded_batch_strided_table_outputs_and_three_dim_q():
     """A padded batch (idle slots of length 0), a table that is a slice of a wider one, given outputs and no lse; the
     rows behind the batch keep what they held."""
