@@ -456,7 +456,8 @@ mac_status mac_quant_gather(mac_quant_handle h, int n_tokens, const int32_t *dev
  *   dev_out    bf16 [batch][n_query][heads][128]; dev_lse fp32
  *              [batch][n_query][heads] natural-log LSE, or NULL
  * What slots past a request's length hold, NaN included, has no effect, nor
- * has what the tokens hold that a query does not see.
+ * has what the tokens hold that a query does not see.  A query row with a NaN
+ * or an infinity gives NaN (out and lse) where it sees a token.
  * Results do not depend on other requests' values, but the split of the work,
  * and with it the order of sums, depends on all lengths of the call.  A page
  * outside the store or a length outside the table is not read; the request's

@@ -186,9 +186,12 @@ __device__ __forceinline__ uint32_t lds1(uint32_t addr)
     return v;
 }
 
+// Two bf16 times up as f16x2.  The added x * 0 makes an infinity NaN: scores of
+// minus infinity alone would read as a row that sees nothing.
 __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t two, float up)
 {
-    return f16x2(__uint_as_float(two << 16) * up, __uint_as_float(two & 0xffff0000u) * up);
+    const float x = __uint_as_float(two << 16), y = __uint_as_float(two & 0xffff0000u);
+    return f16x2(__fmaf_rn(x, up, __fmul_rn(x, 0.f)), __fmaf_rn(y, up, __fmul_rn(y, 0.f)));
 }
 
 }  // namespace

@@ -441,6 +441,30 @@ def test_attention_nonfinite_values_of_later_drafts(H, Hkv, nq, n, bad):
     assert (np.abs(lse[0].double().cpu().numpy() - l) <= tl).all()
 
 
+@pytest.mark.parametrize("H,n", [(4, 7), (4, 3000), (12, 100), (20, 100), (32, 100)])
+def test_attention_nonfinite_queries_give_nan_in_their_row(H, n):
+    """An infinity in a query leaves no softmax: NaN, also where every score is minus infinity; the group's other rows
+    are untouched."""
+    c = Case([n], H, 1, 1, seed=81)
+    k = _randn((n, 1, 128), 9).abs().clamp(min=0.5)                 # no element rounds to 0
+    slots = (torch.from_numpy(c.table[0, np.arange(n) // 16].astype(np.int32)) * 16 + torch.arange(n) % 16).to(torch.int32)
+    c.cache.append(k.cuda(), _randn((n, 1, 128), 200 + 81).cuda(), slots.cuda())
+    c.k[0] = R.stored(k.double().numpy())
+    assert (c.k[0] > 0).all()
+    bad = [0, 1, H - 1]
+    for row, x in zip(bad, ("-inf", "inf", "nan")):
+        c.q[0, 0, row, 77] = float(x)
+    c.dev["q"] = c.q.cuda()
+    out, lse = c.run()
+    assert torch.isnan(out[0, 0, bad]).all() and torch.isnan(lse[0, 0, bad]).all()
+    good = [r for r in range(H) if r not in bad]
+    q = c.q[0].double().numpy()[:, good]
+    o, l, mag, top = R.attention(q, c.k[0], c.v[0], c.scale)
+    to, tl = R.attention_tolerance(o, mag, top, l, n)
+    assert (np.abs(out[0].double().cpu().numpy()[:, good] - o) <= to).all()
+    assert (np.abs(lse[0].double().cpu().numpy()[:, good] - l) <= tl).all()
+
+
 def test_attention_padded_batch_strided_table_outputs_and_three_dim_q():
     """A padded batch (idle slots of length 0), a table that is a slice of a wider one, given outputs and no lse; the
     rows behind the batch keep what they held."""
