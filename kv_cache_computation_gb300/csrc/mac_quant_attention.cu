@@ -94,6 +94,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The bytes of the first n of a word of four V scales (tokens 0, 2, 1, 3).
+__device__ __forceinline__ uint32_t scales_of_first(int n)
+{
+    return (n > 0 ? 0xffu : 0u) | (n > 2 ? 0xff00u : 0u) | (n > 1 ? 0xff0000u : 0u) | (n > 3 ? 0xff000000u : 0u);
+}
+
 // A warp's shared memory: its ring and, where Q does not stay in registers, Q;
 // at the end the piece it parks.
 __host__ __device__ constexpr int team_bytes(int nt, int stages, bool qreg)
@@ -108,6 +114,8 @@ struct Smem {
     // parked pieces of the block, in order: their group (-1: none)
     int piece_group[kMaxPieces];
     unsigned long long bar[64];
+    // several queries: the first token with a NaN scale that only some of them see, per warp and element block
+    int bad[kMaxPieces / 2][kQBlocks];
 };
 
 // Writes a row's finished output (four elements at d0) and its lse.
@@ -402,6 +410,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                     for (int k = 0; k < 4; k++) o[nt][j][k] = 0.f;
             }
 
+            __syncwarp();
+            if (lane < kQBlocks) sm.bad[team][lane] = 0x7fffffff;
+            __syncwarp();
             for (int i = 0; i < n; i++) {
                 if (!mbar_wait(bar0 + 8 * stage, phase)) atomicOr(a.st.err, kQErrTimeout);
                 const uint32_t unit = ring + (uint32_t)stage * kUnitBytes;
@@ -469,42 +480,18 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                     // Value scales that may be NaN, whose product with a weight of 0 would be NaN: those of tokens nobody
                     // sees, and the NaN scales of tokens that some of several queries see, are made zero in the ring.
                     // (lane: word (page, c, block) of the unit's scales, bytes of tokens 0, 2, 1, 3)
-                    int bad = 0x7fffffff;       // the first token of the second kind with such a scale in the lane's block
 #pragma unroll 1
                     for (int k = lane; k < kPP * 32; k += 32) {
-                        const int first = tok0 + (k >> 5) * kPage + 4 * ((k >> 3) & 3), seen = len - first;
-                        const uint32_t keep = (seen > 0 ? 0xffu : 0u) | (seen > 2 ? 0xff00u : 0u) |
-                                              (seen > 1 ? 0xff0000u : 0u) | (seen > 3 ? 0xff000000u : 0u);
+                        const int first = tok0 + (k >> 5) * kPage + 4 * ((k >> 3) & 3);
                         const uint32_t at = unit + (k >> 5) * kQPageBytes + kQVScale + (k & 31) * 4;
-                        uint32_t sv = lds4(at) & keep;
-                        if (a.n_query > 1) {
-#pragma unroll
-                            for (int t = 3; t >= 0; t--) {
-                                const uint32_t byte = 0xffu << 8 * q_scale_byte(t);
-                                if (first + t >= full && (sv & byte) == byte) {
-                                    sv &= ~byte;
-                                    bad = min(bad, first + t);
-                                }
-                            }
-                        }
-                        sts4(at, sv);
+                        uint32_t sv = lds4(at) & scales_of_first(len - first);
+                        const uint32_t nan = __vcmpeq4(sv, 0xffffffffu) & ~scales_of_first(full - first);
+                        if (nan)
+                            atomicMin(&sm.bad[team][k & 7],
+                                      first + (nan & 0xffu ? 0 : nan & 0xff0000u ? 1 : nan & 0xff00u ? 2 : 3));
+                        sts4(at, sv & ~nan);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // a later copy writes the same bytes
-                    if (__any_sync(0xffffffffu, bad != 0x7fffffff)) {
-                        // the queries that do see such a token get their NaN here (the lane's outputs are of block g)
-                        bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 8));
-                        bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 16));
-                        bad = __shfl_sync(0xffffffffu, bad, g8);
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                const int r = nt * 8 + 2 * c4 + h;
-                                if (r >= a.rows || len - (a.n_query - 1) + r / a.G <= bad) continue;
-#pragma unroll
-                                for (int j = 0; j < 8; j++) o[nt][j][h] = o[nt][j][2 + h] = CUDART_NAN_F;
-                            }
-                    }
                     __syncwarp();
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
@@ -600,6 +587,20 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 }
             }
             left -= n;
+
+            const int bad = sm.bad[team][g8];
+            if (__any_sync(0xffffffffu, bad != 0x7fffffff)) {
+                // the queries that see a token whose scale was made zero get its NaN here (the lane's outputs are of block g)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int r = nt * 8 + 2 * c4 + h;
+                        if (r >= a.rows || len - (a.n_query - 1) + r / a.G <= bad) continue;
+#pragma unroll
+                        for (int j = 0; j < 8; j++) o[nt][j][h] = o[nt][j][2 + h] = CUDART_NAN_F;
+                    }
+            }
 
             // the piece's sums over its tokens
 #pragma unroll
