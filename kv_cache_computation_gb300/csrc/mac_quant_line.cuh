@@ -1,5 +1,5 @@
-// What the two attention kernels over the 4-bit store share: the line of work
-// units and its cut into equal ranges, and the unpacking of codes.
+// Parts of the attention over the 4-bit store: the line of work units and its
+// cut into equal ranges, and the unpacking of codes.
 //
 // A unit is a fixed number of tokens of one (request, KV head) group; a request
 // without tokens has one unit, so that its output gets written.  The units of
