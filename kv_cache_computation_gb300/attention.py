@@ -216,8 +216,9 @@ class MacAttention:
             raise ValueError("rotary was made for other heads")
         if qkv.device != self.device:
             raise ValueError(f"qkv is on {qkv.device}, the handle lives on {self.device}")
-        q_pre, q_post, k, v = rotary(qkv, positions, q_weight, k_weight, stream=stream)
-        return self.decode_step(q_pre, q_post, k, v, out=out, lse=lse, want_lse=want_lse, stream=stream)
+        with _on(self.device, stream):
+            q_pre, q_post, k, v = rotary(qkv, positions, q_weight, k_weight)
+            return self.decode_step(q_pre, q_post, k, v, out=out, lse=lse, want_lse=want_lse)
 
     def decode_step_host(self, q_pre, q_post, k_new, v_new, out, lse=None, stream=None):
         """decode_step with pinned host tensors: the step's kernels read the

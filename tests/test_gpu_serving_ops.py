@@ -674,3 +674,27 @@ def test_mac_decode_step_from_a_projection():
     assert macs[0].stats()["hits"] == macs[1].stats()["hits"] > 0
     with pytest.raises(ValueError):
         macs[0].decode_step_qkv(QkvRotary(4, 2), qkv, pos, *w)
+
+
+def test_mac_decode_step_from_a_projection_on_another_stream():
+    """With a stream given, the outputs are made of that stream's memory, so work still queued on the current stream, on
+    memory that it has given back, cannot reach them."""
+    from kv_cache_computation_gb300 import MacAttention, QkvRotary
+    B, H, Hkv = 2, 8, 2
+    rot = QkvRotary(H, Hkv)
+    qkv, pos = _randn((B, (H + 2 * Hkv) * 128), 3).cuda(), torch.zeros(B, dtype=torch.int32).cuda()
+    pages = torch.arange(8, dtype=torch.int32).view(B, 4).cuda()
+    got, s = [], torch.cuda.Stream()
+    for stream in (None, s):
+        m = MacAttention(H, Hkv, ring_len=4, band_r=16, max_batch=B, max_ctx=64, num_pages=8)
+        for b in range(B):
+            m.set_page_table(b, pages[b])
+        m.sync()
+        torch.cuda.synchronize()
+        got.append(m.decode_step_qkv(rot, qkv, pos, stream=stream))
+        torch.cuda.synchronize()
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+        owner = [seg["stream"] for seg in torch.cuda.memory_snapshot()
+                 if seg["address"] <= y.data_ptr() < seg["address"] + seg["total_size"]]
+        assert owner == [s.cuda_stream]
