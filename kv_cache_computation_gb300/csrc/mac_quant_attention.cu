@@ -39,23 +39,24 @@
 // again by a second kernel.  No block waits for another.
 //
 // Measured (GB300, in a captured graph; stream against the copy peak of 6.7 TB/s):
-//   rows  8 KV heads x 8 x 128K (1208 MB) 203 us, 6.0 TB/s   285 instructions a page
+//   rows  8 KV heads x 8 x 128K (1208 MB) 204 us, 5.9 TB/s   284 instructions a page
 //         8 KV heads x 1 x 128K (151 MB)   37 us, 4.1
 //         8 KV heads x 1 x 4K              11 us
-//    16   1 KV head  x 8 x 128K (151 MB)   50 us, 3.0        379
+//    16   1 KV head  x 8 x 128K (151 MB)   50 us, 3.0        384
 //    24                                    61 us, 2.5
-//    32                                    73 us, 2.1        472
-// At 8 rows the stream runs at 6.3 TB/s while it lasts (the ALU, where a
-// conversion takes two cycles, 54 % busy, the half-rate f16 multiplies 43 %); a
+//    32                                    74 us, 2.0        473
+// At 8 rows the stream runs at 6.2 TB/s while it lasts (the ALU, where a
+// conversion takes two cycles, 54 % busy, the half-rate f16 multiplies 42 %); a
 // single request pays the fixed chain besides: prologue 1.5 us, first page 1,
 // merge 2, second kernel 4.  Beyond 8 rows a warp's 64 to 128 output registers
 // leave 12 and 8 warps per SM, whose dependent instructions are not hidden
 // (2.2 to 1.6 instructions a cycle, tensor pipe 29 % and 39 % busy).
-// Tried and slower, us: at 8 rows (203) units of one page with 16 or 20 warps
+// Tried and slower, us: at 8 rows (204) units of one page with 16 or 20 warps
 // 248 and 263, 20 warps with spills 246, the next unit's scores in one block
 // with this unit's output 212, value scales for every element block in every lane
-// 240; at 16 / 32 rows (50 / 73) two warps per page with 16 rows each (84 at 32),
-// pairs of warps that split scores by page and output by element 57 / 83, keys
+// 240; at 16 / 32 rows (50 / 74) two warps per page with 16 rows each (84 at 32),
+// pairs of warps that split scores by page and output by element 57 / 83, a unit's
+// pages one after the other 52 / 80 and, with more warps, 58 / 170, keys
 // and accumulators in tensor memory on tcgen05 71 / 98 (four barrier round trips
 // per 128 tokens take longer than their stream).
 #include "mac_device.cuh"
