@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_kernel(const 
                     put<W>(a.q_pre + at + da, x);
                     put<W>(a.q_pre + at + db, y);
                 }
-                if (a.interleaved) {
+                if (!turn) {
+                    // these elements stay: a product with the sine's 0 would bring a neighbour's infinity or NaN in
+                } else if (a.interleaved) {
 #pragma unroll
                     for (int j = 0; j < W / 2; j++) {
                         const float2 c0 = rot[j], c1 = rot[j + W / 2];

@@ -1,0 +1,55 @@
+"""Edges of the operators around the decode step on the GPU: non-finite values
+beside what they must not reach, slots without new tokens, rejected drafts,
+refused releases, queries of very different magnitude, shared scratch."""
+import numpy as np
+import pytest
+import torch
+
+import serving_reference as R
+from test_gpu_serving_ops import BF16, Case, _check_rope, _randn
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+# ---- norm and rotation -------------------------------------------------------
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T,rotary,inter", [(3, 0, False), (3, 64, False), (3, 64, True), (3, 8, True), (130, 104, False),
+                                            (310, 96, False), (310, 96, True), (310, 40, True), (310, 0, False)])
+def test_rope_leaves_unrotated_elements_alone(T, rotary, inter, norm):
+    """An infinity or NaN behind the rotated elements stays where it is: every other element of that part is what the
+    definition gives, and without a norm nothing of the row's rotated part changes either."""
+    from kv_cache_computation_gb300 import QkvRotary
+    H, Hkv = 3, 1
+    x = _randn((T, (H + 2 * Hkv) * 128), 1).view(T, H + 2 * Hkv, 128)
+    # token t, head h: one element behind the rotated ones
+    for t in range(T):
+        for h in range(H + Hkv):
+            at = rotary + (7 * t + 31 * h) % (128 - rotary)
+            x[t, h, at] = (float("inf"), float("-inf"), float("nan"), 2.0)[(t + h) % 4]
+    pos = torch.arange(T, dtype=torch.int32) + 5
+    w = (_randn(128, 2).abs() + 0.5).to(BF16) if norm else None
+    dw = None if w is None else w.cuda()
+    rot = QkvRotary(H, Hkv, rotary_dim=rotary, base=10000.0, interleaved=inter)
+    q_pre, q_post, k, _ = rot(x.reshape(T, -1).cuda(), pos.cuda(), dw, dw)
+    for got, src in ((q_post, x[:, :H]), (k, x[:, H:H + Hkv]), (q_pre, x[:, :H])):
+        y, r = R.norm_rope(src, w, pos, rotary, 10000.0, inter, 1e-6)
+        want = y if got is q_pre else r
+        g = got.double().cpu()
+        for test in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(test(g), test(want)), test
+        fine = torch.isfinite(want)
+        mag = torch.where(torch.isfinite(y), y.abs(), 0.0)
+        half = rotary // 2
+        if half and got is not q_pre:
+            a, b = ((slice(0, rotary, 2), slice(1, rotary, 2)) if inter else (slice(0, half), slice(half, rotary)))
+            mag[..., a] = mag[..., b] = mag[..., a] + mag[..., b]
+        _check_rope(torch.where(fine, g, 0.0), torch.where(fine, want, 0.0), "finite elements", mag)
+        if not norm:
+            same = torch.isnan(src[..., rotary:]) | (got.cpu()[..., rotary:] == src[..., rotary:])
+            assert same.all()
