@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             const int len = sm.line.len[b];
             const int full = max(len - (a.n_query - 1), 0);     // tokens every row sees
             uint32_t qf[QREG ? NT : 1][16];
-            float ref[NT][2], sum[NT][2], o[NT][8][4];
+            // low: the row's reference less kPShift, weights are 2^(score - low)
+            float low[NT][2], sum[NT][2], o[NT][8][4];
             // Q in f16, times the power of two that brings the group's largest finite element into [2^14, 2^15); sc
             // takes a raw score to log2 units
             uint32_t top = 0;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    ref[nt][h] = -CUDART_INF_F;
+                    low[nt][h] = kLowest;
                     sum[nt][h] = 0.f;
                 }
 #pragma unroll
@@ -506,29 +507,37 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                                     if (tok0 + pp * kPage + tk + 2 * k >= lim) s[pp][nt][2 * k + h] = -CUDART_INF_F;
                         }
                 }
-                // softmax: the reference moves only when a score passes it by more than the margin
+                // softmax: the reference moves only when a score passes it by more than the margin.  Scores are rounded
+                // before the reference is taken off, as the reference was: a fused product would be off by its rounding,
+                // which passes any margin for scores beyond 2^27.
                 float x[NT][2];
                 bool moves = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
+#pragma unroll
+                        for (int pp = 0; pp < kPP; pp++) {
+                            s[pp][nt][h] = __fmul_rn(s[pp][nt][h], sc);
+                            s[pp][nt][2 + h] = __fmul_rn(s[pp][nt][2 + h], sc);
+                        }
                         x[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
 #pragma unroll
                         for (int pp = 1; pp < kPP; pp++) x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
-                        moves |= x[nt][h] * sc > ref[nt][h] + kMargin;
+                        moves |= x[nt][h] - low[nt][h] > kMargin + kPShift;
                     }
                 if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            float y = x[nt][h] * sc;
+                            float y = x[nt][h];
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                            y = fmaxf(ref[nt][h], y);
-                            const float f = ref[nt][h] == -CUDART_INF_F ? 0.f : ex2_approx(ref[nt][h] - y);
-                            ref[nt][h] = y;
+                            // scores of 2^23 and more are whole numbers too coarse to take the shift from
+                            y = fmaxf(low[nt][h], fabsf(y) < 0x1p23f ? y - kPShift : y);
+                            const float f = ex2_approx(low[nt][h] - y);
+                            low[nt][h] = y;
                             sum[nt][h] *= f;
 #pragma unroll
                             for (int j = 0; j < 8; j++) {
@@ -540,15 +549,12 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 uint32_t pb[kPP][NT][2];    // P^T fragments: tokens 4 c .. 4 c + 3, row g
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    float base[2];
-#pragma unroll
-                    for (int h = 0; h < 2; h++) base[h] = kPShift - (ref[nt][h] == -CUDART_INF_F ? 0.f : ref[nt][h]);
 #pragma unroll
                     for (int pp = 0; pp < kPP; pp++) {
                         float p[4];
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            p[k] = ex2_approx(fmaf(s[pp][nt][k], sc, base[k & 1]));
+                            p[k] = ex2_approx(s[pp][nt][k] - low[nt][k & 1]);
                             sum[nt][k & 1] += p[k];
                         }
                         pb[pp][nt][0] = movmatrix_t(f16x2(p[0], p[1]));
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
                         dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
                         if (a.lse && g8 == 0)
-                            a.lse[row] = l == 0.f ? -CUDART_INF_F : (ref[nt][h] - kPShift + log2f(l)) * kLn2;
+                            a.lse[row] = l == 0.f ? -CUDART_INF_F : (low[nt][h] + log2f(l)) * kLn2;
                     } else {
                         const int64_t row = park.first_row(team, r);
                         float *dst = which ? park.last_o(team, r) : a.part_o + row * kD;
@@ -645,7 +651,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                         for (int j = 0; j < 8; j += 2)
                             *reinterpret_cast<float4 *>(dst + 16 * g8 + 2 * j) =
                                 make_float4(o[nt][j][h], o[nt][j][2 + h], o[nt][j + 1][h], o[nt][j + 1][2 + h]);
-                        if (g8 == 0) *(which ? park.last_ml(team, r) : a.part_ml + row) = make_float2(ref[nt][h] - kPShift, l);
+                        if (g8 == 0) *(which ? park.last_ml(team, r) : a.part_ml + row) = make_float2(low[nt][h], l);
                     }
                 }
             // the next group

@@ -15,6 +15,7 @@ namespace {
 
 constexpr float kMargin = 6.f;      // log2: how far a score may pass the softmax reference
 constexpr float kPShift = 9.f;      // P is held times 2^kPShift: 2^(6 + 9) is below the f16 maximum
+constexpr float kLowest = -3e38f;   // the reference before the first token: finite, so that masked scores give weight 0
 
 struct Line {
     long long pre[kQMaxBatch + 1];  // units of the requests before b (per KV head)

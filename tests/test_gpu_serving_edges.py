@@ -53,3 +53,29 @@ def test_rope_leaves_unrotated_elements_alone(T, rotary, inter, norm):
         if not norm:
             same = torch.isnan(src[..., rotary:]) | (got.cpu()[..., rotary:] == src[..., rotary:])
             assert same.all()
+
+
+# ---- attention over the store ------------------------------------------------
+
+@pytest.mark.parametrize("qscale", [2.0 ** 20, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 28, 1e15, 1e30])
+@pytest.mark.parametrize("H,n", [(4, 5000), (12, 200), (20, 200), (32, 200)])
+def test_attention_scores_beyond_the_significand(H, n, qscale):
+    """Scores of 2^20 to 2^100 leave all weight to the row's largest: the output is that token's value (rounded to
+    bf16, its weight 1 to 2^-11 by f16) and the lse its score (18 * 2^-23 of sum |q k| as derived for the smaller
+    ones).  The second largest has no weight where it is further below than both scores' errors, 64 log2 units
+    more included."""
+    c = Case([n], H, 1, 1, seed=17, qscale=qscale)
+    out, lse = c.run()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    q, k, v = c.q[0, 0].double().numpy(), c.k[0][:, 0], c.v[0][:, 0]
+    s = (k @ q.T) * c.scale
+    err = 18 * 2.0 ** -23 * (np.abs(k) @ np.abs(q.T)).max(0) * c.scale
+    order = np.argsort(s, axis=0)
+    best, second = order[-1], order[-2]
+    at = np.arange(H)
+    clear = s[best, at] - s[second, at] > 2 * err + 64
+    assert clear.sum() >= H // 2
+    go, gl = out[0, 0].double().cpu().numpy(), lse[0, 0].double().cpu().numpy()
+    want = v[best]
+    assert (np.abs(go - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 1e-12)[clear].all()
+    assert (np.abs(gl - s[best, at]) <= err + 2.0 ** -21 * np.abs(gl))[clear].all()
