@@ -458,7 +458,8 @@ mac_status mac_quant_gather(mac_quant_handle h, int n_tokens, const int32_t *dev
  * What slots past a request's length hold, NaN included, has no effect, nor
  * has what the tokens hold that a query does not see.  A query row with a NaN
  * or an infinity gives NaN (out and lse) where it sees a token.
- * Results do not depend on other requests' values, but the split of the work,
+ * Results do not depend on other requests' values, nor a row's on other heads'
+ * or query tokens' queries, whatever their size; but the split of the work,
  * and with it the order of sums, depends on all lengths of the call.  A page
  * outside the store or a length outside the table is not read; the request's
  * output is then wrong and mac_quant_sync reports it.  Async on stream. */

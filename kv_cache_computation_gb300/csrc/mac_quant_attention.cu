@@ -23,8 +23,8 @@
 //    thread's K words are 32 consecutive elements of a token (two scales), and
 //    its V words one 16-element block of four consecutive tokens (four scales),
 //    whose codes are paired by token with two logic operations per eight codes.
-// Roundings: Q is bf16 and becomes f16 with a power of two per group (exact but
-// for elements below 2^-28 of the group's largest, which keep 2^-39 of it);
+// Roundings: Q is bf16 and becomes f16 with a power of two per row (exact but
+// for elements below 2^-28 of the row's largest, which keep 2^-39 of it);
 // stored values are exact in f16; the weights P, at most 2^15, are rounded to
 // f16 (2^-11 of each; P's factor 2^9 keeps weights down to 2^-33 of the largest)
 // and summed unrounded in fp32; scores, sums, the reference and the output stay
@@ -117,6 +117,7 @@ struct Smem {
     unsigned long long bar[64];
     // several queries: the first token with a NaN scale that only some of them see, per warp and element block
     int bad[kMaxPieces / 2][kQBlocks];
+    float row_sc[kMaxPieces / 2][kQMaxRows];    // log2 units of a row's raw scores, per warp
 };
 
 // Writes a row's finished output (four elements at d0) and its lse.
@@ -150,9 +151,10 @@ __device__ __forceinline__ void load_q(const QuantAttnArgs &a, int b, int g, int
     }
 }
 
-// The larger of top and the bit patterns of the finite magnitudes in w.
-__device__ __forceinline__ uint32_t finite_top(const uint32_t (&w)[16], uint32_t top)
+// The largest bit pattern of the finite magnitudes in w.
+__device__ __forceinline__ uint32_t finite_top(const uint32_t (&w)[16])
 {
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 16; i++) {
         const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
@@ -359,46 +361,41 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             uint32_t qf[QREG ? NT : 1][16];
             // low: the row's reference less kPShift, weights are 2^(score - low)
             float low[NT][2], sum[NT][2], o[NT][8][4];
-            // Q in f16, times the power of two that brings the group's largest finite element into [2^14, 2^15); sc
-            // takes a raw score to log2 units
-            uint32_t top = 0;
-            uint32_t w[QREG ? NT : 1][16];
+            // Q in f16, each row times the power of two that brings its largest finite element into [2^14, 2^15), so that
+            // no row depends on another's size; row_sc takes a row's raw scores to log2 units
+            uint32_t w[16];
+            auto load_row = [&](int nt) {
+                load_q(a, b, g, nt * 8 + g8, c4, w);
+                uint32_t top = finite_top(w);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int shift = top ? min(14 - ((int)(top >> 7) - 127), 126) : 0;
+                if (c4 == 0)
+                    sm.row_sc[team][nt * 8 + g8] = fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
+                return __int_as_float((shift + 127) << 23);
+            };
             if (QREG) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    load_q(a, b, g, nt * 8 + g8, c4, w[nt]);
-                    top = finite_top(w[nt], top);
-                }
-            } else {
-#pragma unroll 1
-                for (int nt = 0; nt < NT; nt++) {
-                    load_q(a, b, g, nt * 8 + g8, c4, w[0]);
-                    top = finite_top(w[0], top);
-                }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int shift = top ? min(14 - ((int)(top >> 7) - 127), 126) : 0;
-            const float up = __int_as_float((shift + 127) << 23);
-            const float sc = fmaxf(a.scale_log2 * __int_as_float((127 - shift) << 23), 1e-37f);
-            if (QREG) {
+                    const float up = load_row(nt);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) qf[nt][i] = scaled_f16x2(w[nt][i], up);
+                    for (int i = 0; i < 16; i++) qf[nt][i] = scaled_f16x2(w[i], up);
+                }
             } else {
                 const uint32_t q0 = ring + STAGES * kUnitBytes + lane * 16;
 #pragma unroll 1
                 for (int nt = 0; nt < NT; nt++) {
-                    load_q(a, b, g, nt * 8 + g8, c4, w[0]);
+                    const float up = load_row(nt);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         uint32_t f[4];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) f[k] = scaled_f16x2(w[0][4 * i + k], up);
+                        for (int k = 0; k < 4; k++) f[k] = scaled_f16x2(w[4 * i + k], up);
                         sts16(q0 + (nt * 4 + i) * 512, f);
                     }
                 }
             }
+            const uint32_t sc0 = smem_u32(&sm.row_sc[team][2 * c4]);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
@@ -513,19 +510,22 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                 float x[NT][2];
                 bool moves = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
+                for (int nt = 0; nt < NT; nt++) {
+                    float sc[2];
+                    lds8(sc0 + nt * 32, sc);
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
 #pragma unroll
                         for (int pp = 0; pp < kPP; pp++) {
-                            s[pp][nt][h] = __fmul_rn(s[pp][nt][h], sc);
-                            s[pp][nt][2 + h] = __fmul_rn(s[pp][nt][2 + h], sc);
+                            s[pp][nt][h] = __fmul_rn(s[pp][nt][h], sc[h]);
+                            s[pp][nt][2 + h] = __fmul_rn(s[pp][nt][2 + h], sc[h]);
                         }
                         x[nt][h] = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
 #pragma unroll
                         for (int pp = 1; pp < kPP; pp++) x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]));
                         moves |= x[nt][h] - low[nt][h] > kMargin + kPShift;
                     }
+                }
                 if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
@@ -534,8 +534,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
                             float y = x[nt][h];
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                            // scores of 2^23 and more are whole numbers too coarse to take the shift from
-                            y = fmaxf(low[nt][h], fabsf(y) < 0x1p23f ? y - kPShift : y);
+                            // a row moves by its own scores alone; those of 2^23 and more are whole numbers too coarse to
+                            // take the shift from
+                            y = y - low[nt][h] > kMargin + kPShift ? (fabsf(y) < 0x1p23f ? y - kPShift : y) : low[nt][h];
                             const float f = ex2_approx(low[nt][h] - y);
                             low[nt][h] = y;
                             sum[nt][h] *= f;

@@ -175,6 +175,11 @@ __device__ __forceinline__ uint32_t lds4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void lds8(uint32_t addr, float (&v)[2])
+{
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];\n" : "=f"(v[0]), "=f"(v[1]) : "r"(addr) : "memory");
+}
+
 __device__ __forceinline__ void sts4(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared.u32 [%0], %1;\n" :: "r"(addr), "r"(v) : "memory");

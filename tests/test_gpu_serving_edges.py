@@ -79,3 +79,24 @@ def test_attention_scores_beyond_the_significand(H, n, qscale):
     want = v[best]
     assert (np.abs(go - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 1e-12)[clear].all()
     assert (np.abs(gl - s[best, at]) <= err + 2.0 ** -21 * np.abs(gl))[clear].all()
+
+
+@pytest.mark.parametrize("H,nq,n", [(4, 1, 300), (4, 1, 9000), (12, 1, 300), (20, 1, 300), (32, 1, 300), (32, 1, 9000),
+                                    (2, 3, 77), (6, 4, 300)])
+def test_attention_rows_of_very_different_magnitude(H, nq, n):
+    """Heads and drafted tokens of one group from 1e-30 to 1e30: a row's result does not depend on the others' size, and
+    a later draft's query does not change an earlier one's result by a bit."""
+    c = Case([n], H, 1, nq, seed=100 + H + nq)
+    q = c.q.float()
+    for i in range(nq):
+        for h in range(H):
+            # at most 1e30 against the store's values of about 1; every other row keeps its ordinary size
+            q[0, i, h] *= (1.0, 1e15, 1.0, 1e-30, 1.0, 1e30)[(i + h) % 6]
+    c.q = q.to(BF16)
+    c.dev["q"] = c.q.cuda()
+    out, lse = c.run()
+    c.check(out, lse)
+    if nq > 1:
+        c.dev["q"][0, nq - 1] *= 2.0 ** 60
+        out2, lse2 = c.run()
+        assert torch.equal(out2[0, :nq - 1], out[0, :nq - 1]) and torch.equal(lse2[0, :nq - 1], lse[0, :nq - 1])
