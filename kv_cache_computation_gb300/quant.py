@@ -138,6 +138,14 @@ class QuantKV:
         if rotary.heads != self.heads or rotary.kv_heads != self.kv_heads:
             raise ValueError("rotary was made for other heads")
         n = qkv.shape[0]
+        # what the attention would refuse, before anything is stored
+        if not 1 <= n // B <= self.max_query or B > self.max_batch:
+            raise ValueError(f"{n // B} query tokens for each of {B} requests; the handle was made for up to "
+                             f"{self.max_query} of {self.max_batch}")
+        _, row, cols = _table(page_table, B, self.device)
+        if cols < 1 or row < cols:
+            raise ValueError("page_table must have a column, and rows that do not overlap")
+        _dev(lengths, "lengths", torch.int32, (B,), self.device)
         _, q, k, v = rotary(qkv, positions[:n], q_weight, k_weight, want_pre=False, stream=stream)
         self.append(k, v, slots[:n], stream=stream)
         return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lengths, stream=stream)

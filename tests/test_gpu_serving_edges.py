@@ -100,3 +100,39 @@ def test_attention_rows_of_very_different_magnitude(H, nq, n):
         c.dev["q"][0, nq - 1] *= 2.0 ** 60
         out2, lse2 = c.run()
         assert torch.equal(out2[0, :nq - 1], out[0, :nq - 1]) and torch.equal(lse2[0, :nq - 1], lse[0, :nq - 1])
+
+
+# ---- a step from its projection --------------------------------------------------
+
+@pytest.mark.parametrize("what", ["queries", "requests", "no_token", "columns", "overlap", "lengths_type", "lengths_shape",
+                                  "table_type"])
+def test_a_refused_step_stores_nothing(what):
+    """Every argument that the step's attention refuses is refused before its append."""
+    from kv_cache_computation_gb300 import MacError, QkvRotary, QuantKV
+    H, Hkv, B, nq = 4, 2, 2, 1
+    cache = QuantKV(H, Hkv, num_pages=4, max_batch=B, max_query=2)
+    rot = QkvRotary(H, Hkv)
+    table, lens = _i32([[0, 1], [2, 3]]), _i32([1, 1])
+    if what == "queries":
+        nq = 3
+    elif what == "requests":
+        B, table, lens = 3, _i32([[0, 1], [2, 3], [1, 0]]), _i32([1, 1, 1])
+    elif what == "no_token":
+        nq = 0
+    elif what == "columns":
+        table = table[:, :0]
+    elif what == "overlap":
+        table = table[:1].expand(2, 2)
+    elif what == "lengths_type":
+        lens = lens.long()
+    elif what == "lengths_shape":
+        lens = lens[:, None]
+    elif what == "table_type":
+        table = table.long()
+    qkv = _randn((B * nq, (H + 2 * Hkv) * 128), 3).cuda()
+    slots = torch.arange(B * nq, dtype=torch.int32).cuda() * 16
+    with pytest.raises((TypeError, ValueError, MacError)):
+        cache.decode_step_qkv(rot, qkv, torch.zeros_like(slots), slots, table, lens)
+    k, v = cache.gather(torch.arange(64, dtype=torch.int32).cuda())
+    assert (k == 0).all() and (v == 0).all()
+    cache.sync()
