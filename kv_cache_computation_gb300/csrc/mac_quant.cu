@@ -368,6 +368,13 @@ mac_status fail_cuda(mac_quant_ctx *h, cudaError_t e, const char *where)
     return MAC_ERR_CUDA;
 }
 
+// A refused argument: no text of an earlier error stands for it.
+mac_status refuse(mac_quant_ctx *h)
+{
+    h->errbuf[0] = 0;
+    return MAC_ERR_INVALID_ARG;
+}
+
 // The handle is usable and its device is the current one.
 mac_status check_handle(mac_quant_ctx *h)
 {
@@ -485,13 +492,13 @@ mac_status mac_quant_append(mac_quant_handle h, int n_tokens, const void *dev_k,
 {
     const mac_status st = check_handle(h);
     if (st != MAC_OK) return st;
-    if (n_tokens < 0) return MAC_ERR_INVALID_ARG;
+    if (n_tokens < 0) return refuse(h);
     if (n_tokens == 0) return MAC_OK;
     const int64_t row = (int64_t)h->cfg.kv_heads * kD;
     if (!dev_k || !dev_v || !dev_slots || !aligned16(dev_k) || !aligned16(dev_v) || ((uintptr_t)dev_slots & 3))
-        return MAC_ERR_INVALID_ARG;
-    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return MAC_ERR_INVALID_ARG;
-    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return MAC_ERR_INVALID_ARG;
+        return refuse(h);
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return refuse(h);
+    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return refuse(h);
     MoveArgs a{};
     a.k = (const __nv_bfloat16 *)dev_k;
     a.v = (const __nv_bfloat16 *)dev_v;
@@ -507,11 +514,11 @@ mac_status mac_quant_gather(mac_quant_handle h, int n_tokens, const int32_t *dev
 {
     const mac_status st = check_handle(h);
     if (st != MAC_OK) return st;
-    if (n_tokens < 0) return MAC_ERR_INVALID_ARG;
+    if (n_tokens < 0) return refuse(h);
     if (n_tokens == 0) return MAC_OK;
     if (!dev_k || !dev_v || !dev_slots || !aligned16(dev_k) || !aligned16(dev_v) || ((uintptr_t)dev_slots & 3))
-        return MAC_ERR_INVALID_ARG;
-    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return MAC_ERR_INVALID_ARG;
+        return refuse(h);
+    if ((int64_t)n_tokens * h->cfg.kv_heads > (1 << 30)) return refuse(h);
     MoveArgs a{};
     a.k_out = (__nv_bfloat16 *)dev_k;
     a.v_out = (__nv_bfloat16 *)dev_v;
@@ -526,12 +533,12 @@ mac_status mac_quant_attention(mac_quant_handle h, int batch, int n_query, const
 {
     const mac_status st = check_handle(h);
     if (st != MAC_OK) return st;
-    if (batch < 0 || batch > h->cfg.max_batch || n_query < 1 || n_query > h->cfg.max_query) return MAC_ERR_INVALID_ARG;
+    if (batch < 0 || batch > h->cfg.max_batch || n_query < 1 || n_query > h->cfg.max_query) return refuse(h);
     if (batch == 0) return MAC_OK;
     if (!dev_q || !dev_table || !dev_lens || !dev_out || !aligned16(dev_q) || !aligned16(dev_out) ||
         (((uintptr_t)dev_table | (uintptr_t)dev_lens | (uintptr_t)dev_lse) & 3))
-        return MAC_ERR_INVALID_ARG;
-    if (table_cols < 1 || table_cols > (1 << 26) || table_stride < table_cols) return MAC_ERR_INVALID_ARG;
+        return refuse(h);
+    if (table_cols < 1 || table_cols > (1 << 26) || table_stride < table_cols) return refuse(h);
     QuantAttnArgs a = h->attn;
     a.n_query = n_query;
     a.rows = a.G * n_query;

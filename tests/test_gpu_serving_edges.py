@@ -136,3 +136,20 @@ def test_a_refused_step_stores_nothing(what):
     k, v = cache.gather(torch.arange(64, dtype=torch.int32).cuda())
     assert (k == 0).all() and (v == 0).all()
     cache.sync()
+
+
+# ---- errors and shared scratch -----------------------------------------------------
+
+def test_a_refusal_carries_no_earlier_text():
+    from kv_cache_computation_gb300 import MacError, QuantKV
+    a = QuantKV(4, 2, num_pages=2)
+    z, bad = torch.zeros((1, 2, 128), dtype=BF16).cuda(), _i32([99])
+    wide = torch.zeros((2, 2 * 128 + 4), dtype=BF16).cuda()
+    for call in (lambda: a.attention(torch.zeros((2, 4, 128), dtype=BF16).cuda(), _i32([[0], [0]]), _i32([0, 0])),
+                 lambda: a.append(wide[:, :256], wide[:, :256], _i32([0, 1]))):
+        a.append(z, z, bad)
+        with pytest.raises(MacError, match="slot"):
+            a.sync()
+        with pytest.raises(MacError) as e:
+            call()
+        assert "slot" not in str(e.value)
