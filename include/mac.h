@@ -419,12 +419,13 @@ mac_status mac_quant_query_sizes(const mac_quant_config *cfg, size_t *store_byte
 
 /* A handle over caller-allocated device buffers (256-byte aligned, at least
  * the sizes above; MAC_ERR_OOM if not) on the current device.  Zeroes both
- * (an unwritten slot reads as zeros).  Synchronous.  Every call below needs
+ * (an unwritten slot reads as zeros), but for a scratch that a live handle uses.  Synchronous.  Every call below needs
  * that device to be current (MAC_ERR_INVALID_ARG otherwise).  Calls on one
  * handle, replays of graphs captured from it among them, must be ordered
  * with one another (one stream, or events): they share the scratch.  Handles
  * (the layers of a model) whose calls are ordered may share one scratch
- * buffer; they then share its error word too. */
+ * buffer, each at its start; they then share its error word too: what the
+ * calls of any met is reported once, by the first to be asked. */
 mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t store_bytes, void *dev_scratch,
                             size_t scratch_bytes, mac_quant_handle *out);
 

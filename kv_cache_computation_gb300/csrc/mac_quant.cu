@@ -26,6 +26,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
+#include <mutex>
 #include <new>
 
 using namespace macgpu;
@@ -353,6 +354,8 @@ struct mac_quant_ctx {
     QuantStore st;
     QuantAttnArgs attn;     // what does not change from call to call
     int device = 0, sm_count = 0;
+    const void *scratch = nullptr;
+    mac_quant_ctx *next = nullptr;      // live handles, under g_live_mutex
     mac_status sticky = MAC_OK;
     char errbuf[256] = {0};
 };
@@ -360,6 +363,11 @@ struct mac_quant_ctx {
 namespace macgpu {
 
 namespace {
+
+// The live handles: one made on another's scratch must not clear the error
+// word that they share, which may hold what nobody has read yet.
+std::mutex g_live_mutex;
+mac_quant_ctx *g_live = nullptr;
 
 mac_status fail_cuda(mac_quant_ctx *h, cudaError_t e, const char *where)
 {
@@ -460,10 +468,18 @@ mac_status mac_quant_create(const mac_quant_config *cfg, void *dev_store, size_t
     good = good && prop.major * 10 + prop.minor == 103;
     if (good) {
         h->sm_count = prop.multiProcessorCount;
+        h->scratch = dev_scratch;
+        std::lock_guard<std::mutex> lock(g_live_mutex);
+        bool shared = false;
+        for (const mac_quant_ctx *o = g_live; o; o = o->next) shared |= o->scratch == dev_scratch && o->device == h->device;
         // an unwritten slot reads back as zeros; work in flight may still use a shared scratch or a recycled buffer
         good = quant_attention_config(h->sm_count) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess &&
                cudaMemset(dev_store, 0, z.store) == cudaSuccess &&
-               cudaMemset(dev_scratch, 0, z.scratch) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+               (shared || cudaMemset(dev_scratch, 0, z.scratch) == cudaSuccess) && cudaDeviceSynchronize() == cudaSuccess;
+        if (good) {
+            h->next = g_live;
+            g_live = h;
+        }
     }
     if (!good) {
         delete h;
@@ -480,6 +496,14 @@ mac_status mac_quant_destroy(mac_quant_handle h)
     if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(h->device) == cudaSuccess) {
         cudaDeviceSynchronize();
         if (dev != h->device) cudaSetDevice(dev);
+    }
+    {
+        std::lock_guard<std::mutex> lock(g_live_mutex);
+        for (mac_quant_ctx **p = &g_live; *p; p = &(*p)->next)
+            if (*p == h) {
+                *p = h->next;
+                break;
+            }
     }
     delete h;
     return MAC_OK;

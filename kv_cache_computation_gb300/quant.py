@@ -33,7 +33,8 @@ class QuantKV:
     pages of a page table.  max_query new tokens per request and call at most
     (heads / kv_heads * max_query <= 32).  Calls on one object must be ordered
     with one another (they share its scratch); layers whose calls are ordered
-    may share scratch: pass another QuantKV as `share`.
+    may share scratch: pass another QuantKV as `share` (sync of either then
+    reports what the calls of both met).
     """
 
     def __init__(self, heads, kv_heads, num_pages, head_dim=128, page_size=16, max_batch=1, max_query=1, sm_scale=0.0,

@@ -153,3 +153,30 @@ def test_a_refusal_carries_no_earlier_text():
         with pytest.raises(MacError) as e:
             call()
         assert "slot" not in str(e.value)
+
+
+def test_a_shared_scratch_keeps_unread_reports():
+    """A layer made on another's scratch does not clear what that one has yet to report; a scratch whose handles are gone
+    starts without reports."""
+    from kv_cache_computation_gb300 import MacError, QuantKV
+    a = QuantKV(4, 2, num_pages=2)
+    z = torch.zeros((1, 2, 128), dtype=BF16).cuda()
+    a.append(z, z, _i32([99]))
+    b = QuantKV(8, 2, num_pages=3, max_query=2, share=a)
+    with pytest.raises(MacError, match="slot"):
+        a.sync()
+    b.sync()
+    b.append(z, z, _i32([99]))
+    with pytest.raises(MacError, match="slot"):             # one word: whoever asks first
+        a.sync()
+    b.sync()
+    b.append(z, z, _i32([99]))
+    a.close()
+    with pytest.raises(MacError, match="slot"):             # the owner's end does not end the sharing
+        b.sync()
+    b.append(z, z, _i32([99]))
+    torch.cuda.synchronize()
+    scratch = b._scratch
+    b.close()
+    c = QuantKV(4, 2, num_pages=2, share=type("Q", (), dict(device=scratch.device, _scratch=scratch))())
+    c.sync()
