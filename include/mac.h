@@ -385,13 +385,25 @@ mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, const void *dev
  *                4  a length or the state out of range, or a page id outside
  *                   the pool met in the table or ring (its tokens get slot -1)
  *                8  a request's tokens would end past max_tokens: denied
- *                16 more pages freed than the ring has room for: none is freed
+ *                16 more pages freed than the ring has room for: none is freed.
+ *                   A state out of range leaves no room, either
  * A denied request keeps its length and gets no page; its packed tokens have
  * slot -1.  max_tokens 1..2^30.  Async on stream. */
 mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
                          int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
                          int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out,
                          int32_t *dev_starts, int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, void *stream);
+
+/* mac_page_step with one more output.
+ *   dev_unreleased  int32 [batch], or NULL: the tokens of a finished request
+ *                whose pages were not freed (bit 16), which are still those of
+ *                its table row; 0 for every other request.  The length of a
+ *                finished request becomes 0 all the same, so in a step in
+ *                place nothing else says which pages it holds */
+mac_status mac_page_step_ex(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
+                            int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
+                            int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out, int32_t *dev_starts,
+                            int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, int32_t *dev_unreleased, void *stream);
 
 /* A paged KV store of 4 bits per value, one layer per handle.  16 consecutive
  * elements x of a head share a scale s = e4m3(max|x| / 6) and are held as

@@ -12,14 +12,20 @@ from .attention import _check, _dev, _on, _stream_ptr, _table
 OUT_OF_PAGES, ROW_FULL, OUT_OF_RANGE, TOO_MANY_TOKENS, RING_FULL = 1, 2, 4, 8, 16
 
 
-class PageStep(NamedTuple):
-    """What page_step returns; all int32 tensors on the GPU."""
+class _PageStep(NamedTuple):
     lengths: torch.Tensor      # [batch] tokens each request holds after the step
     free_state: torch.Tensor   # [2] head and count of the free ring after the step
     starts: torch.Tensor       # [batch + 1] request b's new tokens are the packed tokens starts[b]:starts[b+1]
     positions: torch.Tensor    # [max_tokens] 0-based position of each packed token (0 past the last)
     slots: torch.Tensor        # [max_tokens] page * 16 + offset, or -1: not stored
     status: torch.Tensor       # [1] 0, or the bits above
+
+
+class PageStep(_PageStep):
+    """What page_step returns: six int32 tensors on the GPU (lengths, free_state, starts, positions, slots, status), and
+    `unreleased`: of a step in place, [batch] the tokens of each finished request whose pages could not be freed
+    (status RING_FULL), 0 for all others; else None, since the lengths passed still say it."""
+    unreleased = None
 
 
 def new_page_pool(num_pages, device=None):
@@ -37,7 +43,9 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     ones (negative: the request is finished, its pages are freed).  page_table
     int32 [batch, columns] and free_pages int32 [num_pages] are updated in
     place; lengths and free_state come back as new tensors, or, with in_place,
-    in the tensors passed (for a captured step that runs on).
+    in the tensors passed (for a captured step that runs on).  Where a finished
+    request's pages cannot be freed (status RING_FULL) they stay those of its
+    table row: unreleased keeps its length, which becomes 0.
     """
     device = lengths.device
     B = lengths.shape[0]
@@ -50,9 +58,13 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
         new = lengths.new_empty
         out = (lengths if in_place else new(B), free_state if in_place else new(2), new(B + 1), new(max_tokens),
                new(max_tokens), new(1))
+        unreleased = new(B) if in_place else None
         lo, so, starts, pos, slot, status = [t.data_ptr() for t in out]
-        st = N.lib().mac_page_step(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so, starts, pos, slot,
-                                   status, _stream_ptr(stream, device))
+        st = N.lib().mac_page_step_ex(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so, starts, pos, slot,
+                                      status, unreleased.data_ptr() if in_place else None, _stream_ptr(stream, device))
     if st:
-        _check("mac_page_step", st)
-    return PageStep(*out)
+        _check("mac_page_step_ex", st)
+    step = PageStep(*out)
+    if in_place:
+        step.unreleased = unreleased
+    return step

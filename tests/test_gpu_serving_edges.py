@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import page_reference as PR
 import serving_reference as R
 from test_gpu_serving_ops import BF16, Case, _check_rope, _randn
 
@@ -180,3 +181,39 @@ def test_a_shared_scratch_keeps_unread_reports():
     b.close()
     c = QuantKV(4, 2, num_pages=2, share=type("Q", (), dict(device=scratch.device, _scratch=scratch))())
     c.sync()
+
+
+# ---- page bookkeeping ----------------------------------------------------------------
+
+NAMES = ("lengths", "free_state", "starts", "positions", "slots", "table", "ring", "status", "unreleased")
+
+
+def _step(lens, new, table, ring, state, T, in_place, **kw):
+    """page_step as numpy arrays, in the order of the reference's."""
+    from kv_cache_computation_gb300 import page_step
+    ln, tab, rg, st = _i32(lens), _i32(table), _i32(ring), _i32(state)
+    s = page_step(ln, _i32(new), tab, rg, st, max_tokens=T, in_place=in_place, **kw)
+    assert len(s) == 6 and (s.unreleased is not None) == in_place
+    out = [s.lengths, s.free_state, s.starts, s.positions, s.slots, tab, rg, s.status]
+    return [x.cpu().numpy().astype(np.int64) for x in out + ([s.unreleased] if in_place else [])]
+
+
+def _agree(got, want):
+    for a, b, name in zip(got, want, NAMES):
+        np.testing.assert_array_equal(a, b, err_msg=name)
+
+
+@pytest.mark.parametrize("T", [10, 1500])
+@pytest.mark.parametrize("state,bits", [([5, 8], 16), ([0, 7], 16), ([8, 3], 20), ([-1, 3], 20), ([0, 9], 20), ([2, 4], 16), ([2, 3], 0)])
+def test_refused_release_in_place_keeps_what_it_holds(state, bits, T):
+    """Finished requests of five pages, for which a ring of eight that holds more than three has no room: their lengths come
+    back beside the zeros."""
+    lens, new = [20, 5, 0, 33], [-1, 1, -3, -2]
+    table = [[1, 2, 0], [3, 0, 0], [0, 0, 0], [4, 5, 6]]
+    for in_place in (False, True):
+        want = PR.step(lens, new, table, np.arange(8), state, T)
+        got = _step(lens, new, table, np.arange(8), state, T, in_place)
+        _agree(got, want)
+        assert int(got[7][0]) & ~1 == bits
+        if in_place:
+            assert list(got[8]) == ([20, 0, 0, 33] if bits else [0] * 4)
