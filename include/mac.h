@@ -383,7 +383,9 @@ mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, const void *dev
  *                   a page is denied
  *                2  a request would outgrow its table row: denied
  *                4  a length or the state out of range, or a page id outside
- *                   the pool met in the table or ring (its tokens get slot -1)
+ *                   the pool met in the table or ring (its tokens get slot
+ *                   -1; of a finished request that holds one, no page is
+ *                   freed, so that it cannot get into the ring)
  *                8  a request's tokens would end past max_tokens: denied
  *                16 more pages freed than the ring has room for: none is freed.
  *                   A state out of range leaves no room, either
@@ -396,7 +398,7 @@ mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t
 
 /* mac_page_step with one more output.
  *   dev_unreleased  int32 [batch], or NULL: the tokens of a finished request
- *                whose pages were not freed (bit 16), which are still those of
+ *                whose pages were not freed (bits 4, 16), which are still those of
  *                its table row; 0 for every other request.  The length of a
  *                finished request becomes 0 all the same, so in a step in
  *                place nothing else says which pages it holds */

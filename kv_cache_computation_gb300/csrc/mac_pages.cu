@@ -86,15 +86,29 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
 
 __device__ __forceinline__ int wrap(long long i, int n) { return (int)(i >= n ? i - n : i); }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+
+// *p = x in the shared memory of the cluster's block k.
+__device__ __forceinline__ void store_in_block(int *p, unsigned k, int x)
+{
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"(smem_u32(p)), "r"(k));
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n" :: "r"(addr), "r"(x) : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_constant__ PageArgs a)
 {
     __shared__ long long buf[32];
     __shared__ int s_begin[kThreads], s_first[kThreads], s_rel[kThreads], s_len[kThreads];
     __shared__ unsigned char s_ok[kThreads];
-    __shared__ int s_status, s_popped;
-    pdl_wait();
+    __shared__ int s_stuck[kThreads];       // the request's pages stay: an id among them lies outside the pool
+    __shared__ int s_status, s_popped, s_any_stuck;
     const int tid = threadIdx.x, b = tid;
-    if (tid == 0) s_status = s_popped = 0;
+    if (tid == 0) s_status = s_popped = s_any_stuck = 0;
+    s_stuck[tid] = 0;
+    cluster_arrive();                       // every block may mark requests in every other from the wait on
+    pdl_wait();
     const int N = a.num_pages;
     int head = a.state_in[0], count = a.state_in[1];
     const bool bad_state = head < 0 || head >= N || count < 0 || count > N;
@@ -131,16 +145,59 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
     __syncthreads();
     const int popped = s_popped;
     const bool give_back = !bad_state && (long long)count + total_rel <= N;
+    const int rank = blockIdx.x, stride = gridDim.x * kThreads, gid = rank * kThreads + tid;
+    int found = 0;   // status bits met in the table and ring
+    cluster_wait();
+    // freed pages j0, j0 + 32, ...: their requests and ids (0 past the last), the loads in flight together.  A warp takes
+    // kFlight x 32 pages in a row, so a lane's are seldom of two requests and one search serves them.
+    constexpr int kFlight = 4;
+    const long long first_freed = (long long)(gid - (tid & 31)) * kFlight + (tid & 31);
+    auto freed = [&](long long j0, int (&r)[kFlight], int (&id)[kFlight]) {
+        int at = 0, next = 0;       // the request and where the one behind it starts
+#pragma unroll
+        for (int i = 0; i < kFlight; i++) {
+            const long long j = j0 + 32 * i;
+            id[i] = 0;
+            if (j >= total_rel) continue;
+            if ((int)j >= next) {
+                at = last_at_most(s_rel, a.batch, (int)j);
+                next = at + 1 < a.batch ? s_rel[at + 1] : 0x7fffffff;
+            }
+            r[i] = at;
+            id[i] = a.table[at * a.table_stride + (j - s_rel[at])];
+        }
+    };
+    // an id outside the pool must not reach the ring: its request frees nothing
+    if (give_back) {
+        for (long long j0 = first_freed; j0 < total_rel; j0 += (long long)kFlight * stride) {
+            int r[kFlight], id[kFlight];
+            freed(j0, r, id);
+#pragma unroll
+            for (int i = 0; i < kFlight; i++) {
+                if ((unsigned)id[i] < (unsigned)N) continue;
+                found |= 4;
+                for (unsigned k = 0; k < gridDim.x; k++) {
+                    store_in_block(&s_stuck[r[i]], k, 1);
+                    store_in_block(&s_any_stuck, k, 1);
+                }
+            }
+        }
+    }
 
     // every block has read the old lengths and state by now
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-
-    const int rank = blockIdx.x, stride = gridDim.x * kThreads, gid = rank * kThreads + tid;
-    int found = 0;   // status bits met while writing
+    cluster_arrive();
+    cluster_wait();
+    const bool stuck = s_stuck[tid];
+    if (s_any_stuck) {      // the same in all blocks
+        const int mine = gone && !stuck ? before : 0;
+        const long long to = block_scan(mine, buf, &total_rel);
+        s_rel[tid] = (int)(to - mine);
+        __syncthreads();
+    }
     if (rank == 0) {
         if (live) {
             a.len_out[b] = gone ? 0 : ok ? (int)(len + n) : len;
-            if (a.unreleased) a.unreleased[b] = gone && !give_back ? len : 0;
+            if (a.unreleased) a.unreleased[b] = gone && (!give_back || stuck) ? len : 0;
             a.starts[b] = begin;
         }
         if (tid == 0) {
@@ -152,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
                 a.state_out[0] = wrap((long long)head + popped, N);
                 a.state_out[1] = count - popped + (give_back ? (int)total_rel : 0);
             }
-            found = s_status | (bad_state ? 4 : 0) | (total_rel && !give_back ? 16 : 0);
+            found |= s_status | (bad_state ? 4 : 0) | (total_rel && !give_back ? 16 : 0);
         }
     }
     // block table: the new pages' entries
@@ -164,11 +221,14 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
     }
     // finished requests' pages behind the ring's last free one
     if (give_back) {
-        for (int j = gid; j < (int)total_rel; j += stride) {
-            const int r = last_at_most(s_rel, a.batch, j);
-            const int id = a.table[r * a.table_stride + (j - s_rel[r])];
-            if ((unsigned)id >= (unsigned)N) found |= 4;
-            a.ring[wrap(wrap((long long)head + count, N) + (long long)j, N)] = id;
+        for (long long j0 = first_freed; j0 < total_rel; j0 += (long long)kFlight * stride) {
+            int r[kFlight], id[kFlight];
+            freed(j0, r, id);
+#pragma unroll
+            for (int i = 0; i < kFlight; i++) {
+                const long long j = j0 + 32 * i;
+                if (j < total_rel) a.ring[wrap(wrap((long long)head + count, N) + j, N)] = id[i];
+            }
         }
     }
     // positions and slots of the packed tokens
@@ -196,7 +256,8 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"(smem_u32(&s_status)), "r"(0));
         asm volatile("atom.shared::cluster.or.b32 %0, [%0], %1;\n" : "+r"(addr) : "r"(found) : "memory");
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
     if (rank == 0 && tid == 0) *a.status = *(volatile int *)&s_status;
 }
 

@@ -24,7 +24,7 @@ class _PageStep(NamedTuple):
 class PageStep(_PageStep):
     """What page_step returns: six int32 tensors on the GPU (lengths, free_state, starts, positions, slots, status), and
     `unreleased`: of a step in place, [batch] the tokens of each finished request whose pages could not be freed
-    (status RING_FULL), 0 for all others; else None, since the lengths passed still say it."""
+    (status RING_FULL, or OUT_OF_RANGE: one is not of the pool), 0 for all others; else None, since the lengths passed still say it."""
     unreleased = None
 
 
@@ -44,8 +44,9 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     int32 [batch, columns] and free_pages int32 [num_pages] are updated in
     place; lengths and free_state come back as new tensors, or, with in_place,
     in the tensors passed (for a captured step that runs on).  Where a finished
-    request's pages cannot be freed (status RING_FULL) they stay those of its
-    table row: unreleased keeps its length, which becomes 0.
+    request's pages cannot be freed (status RING_FULL, or OUT_OF_RANGE: one is
+    not of the pool) they stay those of its table row: unreleased keeps its
+    length, which becomes 0.
     """
     device = lengths.device
     B = lengths.shape[0]

@@ -217,3 +217,45 @@ def test_refused_release_in_place_keeps_what_it_holds(state, bits, T):
         assert int(got[7][0]) & ~1 == bits
         if in_place:
             assert list(got[8]) == ([20, 0, 0, 33] if bits else [0] * 4)
+
+
+@pytest.mark.parametrize("T", [12, 3000])
+@pytest.mark.parametrize("where", [[(3, 0)], [(3, 2), (0, 1)], [(3, 1), (5, 0), (5, 3)], [(5, 3)]])
+def test_ids_outside_the_pool_stay_out_of_the_ring(where, T):
+    """A finished request that holds an id outside the pool frees nothing; the others' pages follow one another in the
+    ring, and what the ring counts as free is of the pool."""
+    lens = [40, 3, 30, 40, 16, 64]
+    table = np.array([[0, 1, 2, -1], [3, -1, -1, -1], [4, 5, -1, -1], [6, 7, 8, -1], [9, -1, -1, -1], [10, 11, 12, 13]])
+    ring = np.full(16, -9)
+    ring[[15, 0]] = 14, 15
+    new = [-1, 1, -2, -1, 1, -1]
+    for k, (b, c) in enumerate(where):
+        table[b, c] = (16, -1, 2 ** 31 - 1)[k]
+    for in_place in (False, True):
+        want = PR.step(lens, new, table, ring, [15, 2], T)
+        got = _step(lens, new, table, ring, [15, 2], T, in_place)
+        _agree(got, want)
+        assert int(got[7][0]) == 4
+        free = [int(got[6][(got[1][0] + i) % 16]) for i in range(got[1][1])]
+        assert all(0 <= p < 16 for p in free) and len(set(free)) == len(free)
+        if in_place:
+            assert [b for b in range(6) if got[8][b]] == sorted({b for b, _ in where})
+
+
+def test_long_releases():
+    """Requests of many thousand pages finish beside decoding ones, in one block and in a cluster, one with a bad id."""
+    r = np.random.default_rng(8)
+    N, P = 40000, 8200
+    lens = np.array([131072, 5, 100000, 64, 131072])
+    perm, table, at = r.permutation(N), np.full((5, P), -1, np.int64), 0
+    for b in range(5):
+        table[b, :-(-lens[b] // 16)] = perm[at:at - (-lens[b] // 16)]
+        at += -(-lens[b] // 16)
+    ring = np.full(N, -1)
+    ring[(N - 3 + np.arange(N - at)) % N] = perm[at:]
+    for bad in (False, True):
+        if bad:
+            table[2, 6000] = N
+        for T in (5, 2000):
+            _agree(_step(lens, [-1, 1, -1, 1, -1], table, ring, [N - 3, N - at], T, True),
+                   PR.step(lens, [-1, 1, -1, 1, -1], table, ring, [N - 3, N - at], T))
