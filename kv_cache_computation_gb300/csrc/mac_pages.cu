@@ -12,7 +12,7 @@
 //
 // All of it is integers, a few hundred KB at most, so the launch and the chain
 // of dependent steps bound it: load, three block scans, one write phase.  One
-// block, or for many packed tokens one cluster of blocks, does the whole step
+// block, or for many tokens or pages one cluster of blocks, does the whole step
 // in a single launch: every block makes the scans of the (at most 1024)
 // requests for itself, one request per thread, and the cluster barrier behind
 // the scans separates all reads of the old state from all writes of the new, so
@@ -32,9 +32,12 @@ namespace {
 
 constexpr int kThreads = 1024;          // one request per thread in the scans
 constexpr int kCluster = 8;             // blocks (a portable cluster size)
-// Up to this many packed tokens one block does the step.  Both sides, us: 512
-// tokens 5.3 and 5.3, 1024 5.7 / 5.8 (a cluster), 2048 6.4 / 5.7, 16384 16 / 6.4.
+// Up to this many packed tokens, and pages that could be released, one block
+// does the step.  Both sides, us: 512 tokens 5.3 and 5.3, 1024 5.7 / 5.8 (a
+// cluster), 2048 6.4 / 5.7, 16384 16 / 6.4; 512 released pages 7.0 and 7.0, 2048
+// 7.2 / 7.2, 8192 10.4 / 8.1, 131072 75 / 14.
 constexpr int kOneBlockTokens = 1024;
+constexpr int kOneBlockPages = 4096;
 
 struct PageArgs {
     int batch, table_cols, num_pages, max_tokens;
@@ -296,7 +299,8 @@ mac_status mac_page_step_ex(int batch, int max_tokens, int num_pages, const int3
     PageArgs a{batch, table_cols, num_pages, max_tokens, table_stride, dev_len_in, dev_new, dev_state_in, dev_len_out,
                dev_state_out, dev_table, dev_ring, dev_starts, dev_pos, dev_slot, dev_status,
                dev_unreleased};
-    const int blocks = max_tokens <= kOneBlockTokens ? 1 : kCluster;
+    const bool small = max_tokens <= kOneBlockTokens && (int64_t)batch * table_cols <= kOneBlockPages;
+    const int blocks = small ? 1 : kCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kThreads);

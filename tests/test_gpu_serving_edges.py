@@ -243,7 +243,7 @@ def test_ids_outside_the_pool_stay_out_of_the_ring(where, T):
 
 
 def test_long_releases():
-    """Requests of many thousand pages finish beside decoding ones, in one block and in a cluster, one with a bad id."""
+    """Requests of many thousand pages finish beside decoding ones, one with a bad id."""
     r = np.random.default_rng(8)
     N, P = 40000, 8200
     lens = np.array([131072, 5, 100000, 64, 131072])
@@ -256,6 +256,26 @@ def test_long_releases():
     for bad in (False, True):
         if bad:
             table[2, 6000] = N
-        for T in (5, 2000):
+        for T in (5, 2000):              # the table is wide enough for a cluster in both
             _agree(_step(lens, [-1, 1, -1, 1, -1], table, ring, [N - 3, N - at], T, True),
                    PR.step(lens, [-1, 1, -1, 1, -1], table, ring, [N - 3, N - at], T))
+
+
+@pytest.mark.parametrize("B,P", [(1, 4096), (1, 4097), (64, 64), (63, 66), (1024, 4), (1024, 5)])
+def test_page_step_on_both_sides_of_the_cluster(B, P):
+    """A decode step in which a third of the requests finish, with as many table entries as one block takes and with
+    more."""
+    r = np.random.default_rng(B + P)
+    lens = r.integers(0, 16 * P + 1, B)
+    N = int(((lens + 15) // 16).sum()) + B
+    perm, table, at = r.permutation(N), np.full((B, P), -1, np.int64), 0
+    for b in range(B):
+        used = -(-int(lens[b]) // 16)
+        table[b, :used] = perm[at:at + used]
+        at += used
+    ring = np.full(N, -1)
+    head = int(r.integers(0, N))
+    ring[(head + np.arange(N - at)) % N] = perm[at:]
+    new = np.where(r.random(B) < 0.34, -1, 1)
+    new[0] = -1
+    _agree(_step(lens, new, table, ring, [head, N - at], B, True), PR.step(lens, new, table, ring, [head, N - at], B))
