@@ -387,16 +387,26 @@ mac_status mac_qkv_norm_rope(const mac_rope *rope, int n_tokens, const void *dev
  *                   -1; of a finished request that holds one, no page is
  *                   freed, so that it cannot get into the ring)
  *                8  a request's tokens would end past max_tokens: denied
- *                16 more pages freed than the ring has room for: none is freed.
+ *                16 more pages released than the ring has room for: none is.
  *                   A state out of range leaves no room, either
  * A denied request keeps its length and gets no page; its packed tokens have
- * slot -1.  max_tokens 1..2^30.  Async on stream. */
+ * slot -1.  A length says which entries of its row a request holds, so a caller
+ * must not set one back by itself (rejected drafts: mac_page_step_ex), or the
+ * pages past it are lost.  max_tokens 1..2^30.  Async on stream. */
 mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
                          int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
                          int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out,
                          int32_t *dev_starts, int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, void *stream);
 
-/* mac_page_step with one more output.
+/* mac_page_step with rejected drafts, and one more output.
+ *   dev_rejected int32 [batch], or NULL: tokens taken back from the end of each
+ *                request before its new ones, 0 .. its length (else status 4,
+ *                and the request stays as it is); a finished request's does
+ *                not count.  The pages that it then does not need go to the
+ *                ring, those that it does need stay where they are.  A denied
+ *                request keeps its length less what was taken back.  Where
+ *                its pages cannot be given back (bits 4, 16) it is denied and
+ *                keeps its whole length
  *   dev_unreleased  int32 [batch], or NULL: the tokens of a finished request
  *                whose pages were not freed (bits 4, 16), which are still those of
  *                its table row; 0 for every other request.  The length of a
@@ -405,7 +415,8 @@ mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t
 mac_status mac_page_step_ex(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
                             int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
                             int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out, int32_t *dev_starts,
-                            int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, int32_t *dev_unreleased, void *stream);
+                            int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, const int32_t *dev_rejected,
+                            int32_t *dev_unreleased, void *stream);
 
 /* A paged KV store of 4 bits per value, one layer per handle.  16 consecutive
  * elements x of a head share a scale s = e4m3(max|x| / 6) and are held as

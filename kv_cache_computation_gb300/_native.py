@@ -83,7 +83,7 @@ SIGNATURES = {
     "mac_rope_init": (_i, [ctypes.POINTER(MacRopeConfig), _prope]),
     "mac_qkv_norm_rope": (_i, [_prope, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mac_page_step": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
-    "mac_page_step_ex": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mac_page_step_ex": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mac_quant_query_sizes": (_i, [_pqcfg, _psz, _psz]),
     "mac_quant_create": (_i, [_pqcfg, _vp, _sz, _vp, _sz, ctypes.POINTER(_vp)]),
     "mac_quant_destroy": (_i, [_vp]),

@@ -2,13 +2,17 @@
 // lengths: pages for the new tokens, the finished requests' pages back to the
 // free list, the new lengths, and the packed tokens' positions and slots.
 //
-// Per request b with len tokens and n new ones (n < 0: finished), in order:
-//   before = ceil(len / 16), after = ceil((len + n) / 16), need = after - before
+// Per request b with len tokens, of which `back` are taken back (rejected
+// drafts), and n new ones (n < 0: finished), in order:
+//   held   = ceil(len / 16), kept = len - back, after = ceil((kept + n) / 16)
+//   need   = max(after - held, 0)                    (0 where the request is denied)
+//   rel    = held of a finished request, else held less what it keeps
 //   begin  = sum of n over earlier requests          (packed tokens)
 //   first  = sum of need over earlier requests       (pages taken from the ring)
 // Free page ids stand in a ring of num_pages entries; `head` is the next one
 // out and `count` how many there are.  Page j of the step's pages is
-// ring[head + j]; finished requests' pages go to ring[head + count ...].
+// ring[head + j]; released pages, the last `rel` of a request's row, go to
+// ring[head + count ...].
 //
 // All of it is integers, a few hundred KB at most, so the launch and the chain
 // of dependent steps bound it: load, three block scans, one write phase.  One
@@ -42,37 +46,34 @@ constexpr int kOneBlockPages = 4096;
 struct PageArgs {
     int batch, table_cols, num_pages, max_tokens;
     int64_t table_stride;
-    const int32_t *len_in, *new_tokens, *state_in;
+    const int32_t *len_in, *new_tokens, *rejected, *state_in;
     int32_t *len_out, *state_out, *table, *ring, *starts, *pos, *slot, *status, *unreleased;
 };
 
-__device__ __forceinline__ long long warp_scan(long long v, int lane)
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v, int lane)
 {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        const T y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
     return v;
 }
 
 // Inclusive block scan; *total gets the sum.  Ends with a barrier.
-__device__ long long block_scan(long long v, long long *buf, long long *total)
+template <typename T>
+__device__ T block_scan(T v, T *buf, T *total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long x = warp_scan(v, lane);
+    const T x = warp_scan(v, lane);
     if (lane == 31) buf[w] = x;
     __syncthreads();
-    long long before = 0, all = 0;
-    {
-        const long long t = warp_scan(buf[lane], lane);
-        all = __shfl_sync(0xffffffffu, t, 31);
-        const long long p = __shfl_sync(0xffffffffu, t, (w + 31) & 31);
-        before = w ? p : 0;
-    }
+    const T t = warp_scan(buf[lane], lane);
+    *total = __shfl_sync(0xffffffffu, t, 31);
+    const T before = __shfl_sync(0xffffffffu, t, (w + 31) & 31);
     __syncthreads();
-    *total = all;
-    return x + before;
+    return x + (w ? before : 0);
 }
 
 // The last index with v[i] <= x among n non-decreasing values, v[0] <= x.
@@ -103,7 +104,9 @@ __device__ __forceinline__ void store_in_block(int *p, unsigned k, int x)
 __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_constant__ PageArgs a)
 {
     __shared__ long long buf[32];
+    __shared__ int ibuf[32];
     __shared__ int s_begin[kThreads], s_first[kThreads], s_rel[kThreads], s_len[kThreads];
+    __shared__ int s_held[kThreads], s_from[kThreads];
     __shared__ unsigned char s_ok[kThreads];
     __shared__ int s_stuck[kThreads];       // the request's pages stay: an id among them lies outside the pool
     __shared__ int s_status, s_popped, s_any_stuck;
@@ -118,32 +121,40 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
     if (bad_state) head = count = 0;
     const bool live = b < a.batch;
     const int len = live ? a.len_in[b] : 0, asked = live ? a.new_tokens[b] : 0;
-    const bool bad = len < 0 || (long long)len > (long long)a.table_cols * kPage;
+    const int back = live && asked >= 0 && a.rejected ? a.rejected[b] : 0;
+    const bool bad = len < 0 || (long long)len > (long long)a.table_cols * kPage || back < 0 || back > len;
     const long long n = asked > 0 ? asked : 0;
-    const int before = bad ? 0 : (len + kPage - 1) / kPage;
-    const long long after = bad ? 0 : (len + n + kPage - 1) / kPage;
+    const int kept = bad ? 0 : len - back, held = bad ? 0 : (len + kPage - 1) / kPage;
+    const long long after = bad ? 0 : (kept + n + kPage - 1) / kPage;
     __syncthreads();
 
-    long long total, total_rel, ignored;
+    // tokens are counted in 64 bits; pages, at most batch x table_cols of them, fit 32
+    long long total;
+    int total_rel, ignored;
     const long long end = block_scan(n, buf, &total);
     const bool gone = live && asked < 0 && !bad;
-    const long long rel_end = block_scan(gone ? before : 0, buf, &total_rel);
     const bool wide = after > a.table_cols, late = end > a.max_tokens;
     const bool can = live && asked >= 0 && !bad && !wide && !late;
-    const int need = can ? (int)(after - before) : 0;
-    const long long cum = block_scan(need, buf, &ignored);
+    const int need = can && after > held ? (int)(after - held) : 0;
+    const int cum = block_scan(need, ibuf, &ignored);
     const bool dry = can && need > 0 && cum > count;
-    const bool ok = can && !dry;
+    bool ok = can && !dry;
+    // pages the request gives back: the last of its row
+    const long long keeps = gone ? 0 : ok ? after : (kept + kPage - 1) / kPage;
+    const int rel = live && keeps < held ? held - (int)keeps : 0;
+    const int rel_end = block_scan(rel, ibuf, &total_rel);
     int bits = (dry ? 1 : 0) | (live && bad ? 4 : 0);
     if (live && asked >= 0 && !bad) bits |= wide ? 2 : late ? 8 : 0;
     if (bits) atomicOr(&s_status, bits);
-    if (ok && need > 0) atomicMax(&s_popped, (int)cum);
+    if (ok && need > 0) atomicMax(&s_popped, cum);
     const long long cap = a.max_tokens;
     const int begin = (int)(end - n < cap ? end - n : cap);
     s_begin[tid] = begin;
-    s_first[tid] = (int)(cum - need < 0x7fffffff ? cum - need : 0x7fffffff);
-    s_rel[tid] = (int)(rel_end - (gone ? before : 0));
-    s_len[tid] = bad ? 0 : len;
+    s_first[tid] = cum - need;
+    s_rel[tid] = rel_end - rel;
+    s_from[tid] = held - rel;
+    s_held[tid] = held;
+    s_len[tid] = kept;
     s_ok[tid] = ok;
     __syncthreads();
     const int popped = s_popped;
@@ -167,10 +178,10 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
                 next = at + 1 < a.batch ? s_rel[at + 1] : 0x7fffffff;
             }
             r[i] = at;
-            id[i] = a.table[at * a.table_stride + (j - s_rel[at])];
+            id[i] = a.table[at * a.table_stride + s_from[at] + (j - s_rel[at])];
         }
     };
-    // an id outside the pool must not reach the ring: its request frees nothing
+    // an id outside the pool must not reach the ring: its request gives nothing back
     if (give_back) {
         for (long long j0 = first_freed; j0 < total_rel; j0 += (long long)kFlight * stride) {
             int r[kFlight], id[kFlight];
@@ -190,17 +201,23 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
     // every block has read the old lengths and state by now
     cluster_arrive();
     cluster_wait();
-    const bool stuck = s_stuck[tid];
-    if (s_any_stuck) {      // the same in all blocks
-        const int mine = gone && !stuck ? before : 0;
-        const long long to = block_scan(mine, buf, &total_rel);
-        s_rel[tid] = (int)(to - mine);
+    // a request whose pages cannot be given back keeps them all, and its length (it takes none from the ring, either)
+    const bool stuck = rel > 0 && (!give_back || s_stuck[tid]);
+    if (s_any_stuck || (total_rel && !give_back)) {      // the same in all blocks
+        const int mine = stuck ? 0 : rel;
+        s_rel[tid] = block_scan(mine, ibuf, &total_rel) - mine;
+        if (stuck) {
+            ok = false;
+            s_ok[tid] = 0;
+            s_len[tid] = len;
+        }
+        if (!give_back) found |= 16;
         __syncthreads();
     }
     if (rank == 0) {
         if (live) {
-            a.len_out[b] = gone ? 0 : ok ? (int)(len + n) : len;
-            if (a.unreleased) a.unreleased[b] = gone && (!give_back || stuck) ? len : 0;
+            a.len_out[b] = gone ? 0 : bad || stuck ? len : ok ? (int)(kept + n) : kept;
+            if (a.unreleased) a.unreleased[b] = gone && stuck ? len : 0;
             a.starts[b] = begin;
         }
         if (tid == 0) {
@@ -210,19 +227,19 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
                 a.state_out[1] = a.state_in[1];
             } else {
                 a.state_out[0] = wrap((long long)head + popped, N);
-                a.state_out[1] = count - popped + (give_back ? (int)total_rel : 0);
+                a.state_out[1] = count - popped + (give_back ? total_rel : 0);
             }
-            found |= s_status | (bad_state ? 4 : 0) | (total_rel && !give_back ? 16 : 0);
+            found |= s_status | (bad_state ? 4 : 0);
         }
     }
     // block table: the new pages' entries
     for (int j = gid; j < popped; j += stride) {
-        const int r = last_at_most(s_first, a.batch, j), l = s_len[r];
+        const int r = last_at_most(s_first, a.batch, j);
         const int id = a.ring[wrap((long long)head + j, N)];
         if ((unsigned)id >= (unsigned)N) found |= 4;
-        a.table[r * a.table_stride + (l + kPage - 1) / kPage + (j - s_first[r])] = id;
+        a.table[r * a.table_stride + s_held[r] + (j - s_first[r])] = id;
     }
-    // finished requests' pages behind the ring's last free one
+    // released pages behind the ring's last free one
     if (give_back) {
         for (long long j0 = first_freed; j0 < total_rel; j0 += (long long)kFlight * stride) {
             int r[kFlight], id[kFlight];
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(const __grid_consta
             const int r = last_at_most(s_begin, a.batch, t), l = s_len[r];
             pos = l + (t - s_begin[r]);
             if (s_ok[r]) {
-                const int c = pos / kPage, had = (l + kPage - 1) / kPage;
+                const int c = pos / kPage, had = s_held[r];
                 const int id = c < had ? a.table[r * a.table_stride + c]
                                        : a.ring[wrap((long long)head + s_first[r] + (c - had), N)];
                 if ((unsigned)id < (unsigned)N) slot = id * kPage + pos % kPage;
@@ -279,13 +296,14 @@ mac_status mac_page_step(int batch, int max_tokens, int num_pages, const int32_t
 {
     return mac_page_step_ex(batch, max_tokens, num_pages, dev_len_in, dev_new, dev_len_out, dev_table, table_stride,
                             table_cols, dev_ring, dev_state_in, dev_state_out, dev_starts, dev_pos, dev_slot, dev_status,
-                            nullptr, stream);
+                            nullptr, nullptr, stream);
 }
 
 mac_status mac_page_step_ex(int batch, int max_tokens, int num_pages, const int32_t *dev_len_in, const int32_t *dev_new,
                             int32_t *dev_len_out, int32_t *dev_table, int64_t table_stride, int table_cols,
                             int32_t *dev_ring, const int32_t *dev_state_in, int32_t *dev_state_out, int32_t *dev_starts,
-                            int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, int32_t *dev_unreleased, void *stream)
+                            int32_t *dev_pos, int32_t *dev_slot, int32_t *dev_status, const int32_t *dev_rejected,
+                            int32_t *dev_unreleased, void *stream)
 {
     if (batch < 1 || batch > kThreads || max_tokens < 1 || max_tokens > (1 << 30)) return MAC_ERR_INVALID_ARG;
     if (num_pages < 1 || num_pages > (1 << 27) - 1) return MAC_ERR_INVALID_ARG;   // slots are int32
@@ -295,9 +313,9 @@ mac_status mac_page_step_ex(int batch, int max_tokens, int num_pages, const int3
                        dev_pos, dev_slot, dev_status};
     for (const void *x : p)
         if (!x || !aligned4(x)) return MAC_ERR_INVALID_ARG;
-    if (!aligned4(dev_unreleased)) return MAC_ERR_INVALID_ARG;
-    PageArgs a{batch, table_cols, num_pages, max_tokens, table_stride, dev_len_in, dev_new, dev_state_in, dev_len_out,
-               dev_state_out, dev_table, dev_ring, dev_starts, dev_pos, dev_slot, dev_status,
+    if (!aligned4(dev_rejected) || !aligned4(dev_unreleased)) return MAC_ERR_INVALID_ARG;
+    PageArgs a{batch, table_cols, num_pages, max_tokens, table_stride, dev_len_in, dev_new, dev_rejected, dev_state_in,
+               dev_len_out, dev_state_out, dev_table, dev_ring, dev_starts, dev_pos, dev_slot, dev_status,
                dev_unreleased};
     const bool small = max_tokens <= kOneBlockTokens && (int64_t)batch * table_cols <= kOneBlockPages;
     const int blocks = small ? 1 : kCluster;

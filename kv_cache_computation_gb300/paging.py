@@ -36,7 +36,7 @@ def new_page_pool(num_pages, device=None):
 
 
 def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_tokens, in_place=False,
-              stream=None) -> PageStep:
+              stream=None, rejected=None) -> PageStep:
     """Pages, positions and slots for one step's new tokens, from the lengths on the GPU.
 
     lengths, new_tokens int32 [batch]: tokens each request holds and its new
@@ -47,6 +47,11 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     request's pages cannot be freed (status RING_FULL, or OUT_OF_RANGE: one is
     not of the pool) they stay those of its table row: unreleased keeps its
     length, which becomes 0.
+
+    rejected int32 [batch]: tokens taken back from the end of each request
+    before its new ones (drafts that were not accepted); the pages it then
+    does not need are freed.  Lengths must not be set back in any other way:
+    the pages past them would be lost.
     """
     device = lengths.device
     B = lengths.shape[0]
@@ -55,6 +60,7 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
     n = free_pages.numel()
     ring = _dev(free_pages, "free_pages", torch.int32, (n,), device)
     state = _dev(free_state, "free_state", torch.int32, (2,), device)
+    back = None if rejected is None else _dev(rejected, "rejected", torch.int32, (B,), device)
     with _on(device, stream):
         new = lengths.new_empty
         out = (lengths if in_place else new(B), free_state if in_place else new(2), new(B + 1), new(max_tokens),
@@ -62,7 +68,8 @@ def page_step(lengths, new_tokens, page_table, free_pages, free_state, max_token
         unreleased = new(B) if in_place else None
         lo, so, starts, pos, slot, status = [t.data_ptr() for t in out]
         st = N.lib().mac_page_step_ex(B, max_tokens, n, li, ni, lo, table, row, cols, ring, state, so, starts, pos, slot,
-                                      status, unreleased.data_ptr() if in_place else None, _stream_ptr(stream, device))
+                                      status, back, unreleased.data_ptr() if in_place else None,
+                                      _stream_ptr(stream, device))
     if st:
         _check("mac_page_step_ex", st)
     step = PageStep(*out)

@@ -279,3 +279,75 @@ def test_page_step_on_both_sides_of_the_cluster(B, P):
     new = np.where(r.random(B) < 0.34, -1, 1)
     new[0] = -1
     _agree(_step(lens, new, table, ring, [head, N - at], B, True), PR.step(lens, new, table, ring, [head, N - at], B))
+
+
+@pytest.mark.parametrize("B,P,top,T,seed", [(1, 4, 3, 4, 0), (7, 12, 20, 200, 1), (40, 6, 70, 3000, 2), (300, 20, 25, 8000, 3)])
+def test_rejected_drafts_over_many_steps(B, P, top, T, seed):
+    """Requests that draft, take some of it back, come and go, also where the pool or a row is too small: every step is the
+    definition's, and no page is ever lost or held twice."""
+    from kv_cache_computation_gb300 import new_page_pool, page_step
+    r = np.random.default_rng(seed)
+    N = B * P // 2 + 1
+    ring, state = new_page_pool(N)
+    lens = torch.zeros(B, dtype=torch.int32).cuda()
+    table = torch.zeros((B, P), dtype=torch.int32).cuda()
+    ref = [np.zeros(B, np.int64), [0, N], None, None, None, table.cpu().numpy(), ring.cpu().numpy()]
+    bits, freed = 0, 0
+    for t in range(50):
+        new = np.where(r.random(B) < 0.1, -1, r.integers(0, top + 1, B))
+        rejected = np.minimum(r.integers(0, top + 1, B) * (r.random(B) < 0.6), ref[0])
+        want = PR.step(ref[0], new, ref[5], ref[6], [int(x) for x in ref[1]], T, rejected)
+        s = page_step(lens, _i32(new), table, ring, state, max_tokens=T, rejected=_i32(rejected), in_place=t % 2 == 1)
+        lens, state = s.lengths, s.free_state
+        _agree([x.cpu().numpy() for x in (lens, state, s.starts, s.positions, s.slots, table, ring, s.status)], want[:8])
+        freed += sum(PR.pages(int(want[0][b])) < PR.pages(int(ref[0][b])) for b in range(B) if new[b] >= 0)
+        bits |= int(want[7][0])
+        ref = want
+        held = [int(p) for b in range(B) for p in want[5][b, :PR.pages(int(want[0][b]))]]
+        free = [int(want[6][(int(want[1][0]) + i) % N]) for i in range(int(want[1][1]))]
+        assert sorted(held + free) == list(range(N))
+    assert freed and (B == 1 or bits & 3)
+
+
+def test_rejected_drafts_across_a_page_edge():
+    """15 tokens, 3 drafts of which 2 are rejected, one more token: the page that the drafts opened is not lost."""
+    from kv_cache_computation_gb300 import new_page_pool, page_step
+    ring, state = new_page_pool(8)
+    table = torch.zeros((1, 8), dtype=torch.int32).cuda()
+    s = page_step(_i32([0]), _i32([15]), table, ring, state, max_tokens=32)
+    s = page_step(s.lengths, _i32([3]), table, ring, s.free_state, max_tokens=32)
+    s = page_step(s.lengths, _i32([1]), table, ring, s.free_state, max_tokens=32, rejected=_i32([2]))
+    assert int(s.lengths) == 17 and int(s.positions[0]) == 16 and int(s.slots[0]) == int(table[0, 1]) * 16
+    assert int(s.free_state[1]) == 6
+    s = page_step(s.lengths, _i32([0]), table, ring, s.free_state, max_tokens=32, rejected=_i32([17]))
+    assert int(s.lengths) == 0 and int(s.free_state[1]) == 8 and int(s.status) == 0
+
+
+@pytest.mark.parametrize("what,bit", [("more", 4), ("negative", 4), ("ring", 16), ("state", 16), ("page", 4), ("finished", 0),
+                                      ("dry", 1), ("row", 2), ("tokens", 8)])
+def test_rejected_draft_denials(what, bit):
+    lens, new, rejected = [40, 33, 20, 16], [1, 5, 30, 2], [20, 2, 3, 1]
+    table = [[0, 1, 2, -1], [3, 4, 5, -1], [6, 7, -1, -1], [8, -1, -1, -1]]
+    ring, state, T = np.array([9, 10, 11, 12, 13, 14, 15, -1, -1, -1, -1, -1, -1, -1, -1, -1]), [0, 7], 60
+    if what == "more":
+        rejected[1] = 34
+    elif what == "negative":
+        rejected[0] = -1
+    elif what == "ring":
+        state = [0, 16]
+    elif what == "state":
+        state = [16, 3]
+    elif what == "page":
+        table[0][2] = -4
+    elif what == "finished":
+        new[0], rejected[0] = -1, 999
+    elif what == "dry":
+        state = [0, 1]
+    elif what == "row":
+        new[2] = 48
+    elif what == "tokens":
+        T = 20
+    for in_place in (False, True):
+        want = PR.step(lens, new, table, ring, state, T, rejected)
+        assert int(want[7][0]) & bit == bit and (bit or int(want[7][0]) == 0)
+        _agree(_step(lens, new, table, ring, state, T, in_place, rejected=_i32(rejected)), want)

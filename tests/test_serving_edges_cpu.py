@@ -19,9 +19,11 @@ def native():
 def test_page_step_ex_refusals(native):
     L = native.lib()
     good = dict(batch=2, tokens=2, pages=8, len_in=P, new=P, len_out=P, table=P, stride=4, cols=4, ring=P, state_in=P,
-                state_out=P, starts=P, pos=P, slot=P, status=P, unreleased=None, stream=None)
+                state_out=P, starts=P, pos=P, slot=P, status=P, rejected=None,
+                unreleased=None, stream=None)
     bad = [dict(batch=0), dict(batch=1025), dict(tokens=0), dict(tokens=(1 << 30) + 1), dict(pages=0), dict(pages=1 << 27),
-           dict(cols=0), dict(stride=3), dict(batch=1024, cols=1 << 21, stride=1 << 21), dict(unreleased=ODD)]
+           dict(cols=0), dict(stride=3), dict(batch=1024, cols=1 << 21, stride=1 << 21), dict(unreleased=ODD),
+           dict(rejected=ODD)]
     for name in ("len_in", "new", "len_out", "table", "ring", "state_in", "state_out", "starts", "pos", "slot", "status"):
         bad += [{name: None}, {name: ODD}]
     for kw in bad:
