@@ -493,6 +493,27 @@ mac_status mac_quant_attention(mac_quant_handle h, int batch, int n_query, const
                                int64_t table_stride, int table_cols, const int32_t *dev_lens, void *dev_out,
                                float *dev_lse, void *stream);
 
+/* A decode step's new tokens, packed as mac_page_step leaves them, as n_query
+ * rows for each of `batch` requests: row b * n_query + i is request b's i-th
+ * new token.  The packed arrays hold only tokens that exist, so behind a request
+ * without any (idle, finished) they and the rows of a padded batch differ.
+ *   n_packed     entries of dev_pos and dev_slots
+ *   dev_starts   int32 [batch + 1], mac_page_step's, or NULL: every request has
+ *                n_query packed tokens (n_packed >= batch * n_query)
+ *   dev_table, dev_lens  as the attention takes them, lengths after the step
+ *   dev_pos_out, dev_slots_out  int32 [batch * n_query], for mac_qkv_norm_rope
+ *                and mac_quant_append;  dev_lens_out  int32 [batch], for the attention
+ * A request's rows count if it has exactly n_query packed tokens and their slots
+ * are those that its table gives the last n_query tokens of its length.
+ * Otherwise its rows get position 0 and slot -1 and its length becomes 0 (not
+ * stored; out 0, lse -inf), which mac_quant_sync reports, unless it has no packed
+ * token or none of them has a slot (idle, finished, denied).  Outputs must not
+ * overlap the inputs.  Async on stream. */
+mac_status mac_quant_step_rows(mac_quant_handle h, int batch, int n_query, int n_packed, const int32_t *dev_starts,
+                               const int32_t *dev_pos, const int32_t *dev_slots, const int32_t *dev_table,
+                               int64_t table_stride, int table_cols, const int32_t *dev_lens, int32_t *dev_pos_out,
+                               int32_t *dev_slots_out, int32_t *dev_lens_out, void *stream);
+
 /* Wait for the device and report what its checks met since the last call:
  * MAC_ERR_STATE (text in mac_quant_last_error), which is then cleared. */
 mac_status mac_quant_sync(mac_quant_handle h);

@@ -16,7 +16,7 @@ attention over it):
 
     step = page_step(lengths, new_tokens, page_table, *free, max_tokens=B)
     out, lse = QuantKV(32, 8, num_pages=4096, max_batch=B).decode_step_qkv(
-        QkvRotary(32, 8), qkv, step.positions, step.slots, page_table, step.lengths)
+        QkvRotary(32, 8), qkv, step.positions, step.slots, page_table, step.lengths, starts=step.starts)
 
 The CUDA library must be built first (``kv_cache_computation_gb300.build``);
 there is no CPU fallback.

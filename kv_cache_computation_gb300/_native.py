@@ -90,6 +90,7 @@ SIGNATURES = {
     "mac_quant_append": (_i, [_vp, _i, _vp, _i64, _vp, _i64, _vp, _vp]),
     "mac_quant_gather": (_i, [_vp, _i, _vp, _vp, _vp, _vp]),
     "mac_quant_attention": (_i, [_vp, _i, _i, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp]),
+    "mac_quant_step_rows": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp]),
     "mac_quant_sync": (_i, [_vp]),
     "mac_quant_last_error": (ctypes.c_char_p, [_vp]),
     "mac_status_string": (ctypes.c_char_p, [_i]),

@@ -40,7 +40,7 @@ constexpr int kQVScale = kQV + kPage * kD / 2;
 static_assert(kQPageBytes == 2304 && kQV % 128 == 0 && kQVScale % 128 == 0, "page layout");
 
 // bits of the device error word
-enum : uint32_t { kQErrPage = 1u, kQErrSlot = 2u, kQErrLen = 4u, kQErrTimeout = 8u };
+enum : uint32_t { kQErrPage = 1u, kQErrSlot = 2u, kQErrLen = 4u, kQErrTimeout = 8u, kQErrRow = 16u };
 
 // the byte of token t % 4 among a block's four V scales
 __host__ __device__ inline int q_scale_byte(int tt) { return (tt >> 1) | (tt & 1) << 1; }

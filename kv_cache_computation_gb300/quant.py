@@ -127,11 +127,15 @@ class QuantKV:
         return out, lse
 
     def decode_step_qkv(self, rotary, qkv, positions, slots, page_table, lengths, q_weight=None, k_weight=None,
-                        stream=None):
+                        stream=None, starts=None):
         """One layer's step from its QKV projection: norm and rotation, append, attention.
 
-        qkv [batch * n_query, (heads + 2 kv_heads) * 128]; positions, slots and lengths (the tokens after the
-        step) as page_step gives them for n_query new tokens per request.  Returns (out, lse).
+        qkv [batch * n_query, (heads + 2 kv_heads) * 128]: row b * n_query + i is request b's i-th new token;
+        positions, slots, lengths (the tokens after the step) and starts as page_step gives them.  Without
+        starts every request must have n_query new tokens; with them, a request without any (an idle or
+        finished one of a padded batch), or one that page_step denied, is left out: nothing of its rows is
+        stored, its out is 0 and its lse -inf.  So is a request with another number of new tokens, or whose
+        slots are not those of its own row of page_table, which sync() then reports.  Returns (out, lse).
         """
         B = lengths.shape[0]
         if B == 0 or qkv.shape[0] % B:
@@ -143,13 +147,26 @@ class QuantKV:
         if not 1 <= n // B <= self.max_query or B > self.max_batch:
             raise ValueError(f"{n // B} query tokens for each of {B} requests; the handle was made for up to "
                              f"{self.max_query} of {self.max_batch}")
-        _, row, cols = _table(page_table, B, self.device)
+        table, row, cols = _table(page_table, B, self.device)
         if cols < 1 or row < cols:
             raise ValueError("page_table must have a column, and rows that do not overlap")
-        _dev(lengths, "lengths", torch.int32, (B,), self.device)
-        _, q, k, v = rotary(qkv, positions[:n], q_weight, k_weight, want_pre=False, stream=stream)
-        self.append(k, v, slots[:n], stream=stream)
-        return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lengths, stream=stream)
+        packed = positions.numel()
+        if starts is None and packed < n:
+            raise ValueError(f"positions must hold the {n} new tokens, got {packed}")
+        lp = _dev(lengths, "lengths", torch.int32, (B,), self.device)
+        pp = _dev(positions, "positions", torch.int32, (packed,), self.device)
+        sp = _dev(slots, "slots", torch.int32, (packed,), self.device)
+        first = None if starts is None else _dev(starts, "starts", torch.int32, (B + 1,), self.device)
+        with _on(self.device, stream):
+            rows = _out((2 * n + B,), self.device, torch.int32)
+            pos, slot, lens = rows[:n], rows[n:2 * n], rows[2 * n:]
+            _check("mac_quant_step_rows",
+                   N.lib().mac_quant_step_rows(self._h, B, n // B, packed, first, pp, sp, table, row, cols, lp,
+                                               pos.data_ptr(), slot.data_ptr(), lens.data_ptr(),
+                                               _stream_ptr(stream, self.device)), self._h)
+        _, q, k, v = rotary(qkv, pos, q_weight, k_weight, want_pre=False, stream=stream)
+        self.append(k, v, slot, stream=stream)
+        return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lens, stream=stream)
 
     def sync(self):
         """Wait for the device; raises MacError if its checks met a bad slot, page or length since the last call."""

@@ -351,3 +351,187 @@ def test_rejected_draft_denials(what, bit):
         want = PR.step(lens, new, table, ring, state, T, rejected)
         assert int(want[7][0]) & bit == bit and (bit or int(want[7][0]) == 0)
         _agree(_step(lens, new, table, ring, state, T, in_place, rejected=_i32(rejected)), want)
+
+
+# ---- padded batches through the whole step ---------------------------------------------
+
+class Loop:
+    """A decode loop of B slots: lengths, table and pool on the GPU, and what each request holds in float64."""
+
+    def __init__(self, B, nq, pages=60, H=4, Hkv=2, cols=8):
+        from kv_cache_computation_gb300 import QkvRotary, QuantKV, new_page_pool
+        self.B, self.nq, self.H, self.Hkv = B, nq, H, Hkv
+        self.rot = QkvRotary(H, Hkv, base=10000.0)
+        self.cache = QuantKV(H, Hkv, num_pages=pages, max_batch=B, max_query=nq)
+        self.ring, self.state = new_page_pool(pages)
+        self.lens = torch.zeros(B, dtype=torch.int32).cuda()
+        self.table = torch.full((B, cols), -1, dtype=torch.int32).cuda()
+        self.new = torch.zeros(B, dtype=torch.int32).cuda()
+        self.qkv = torch.zeros((B * nq, (H + 2 * Hkv) * 128), dtype=BF16).cuda()
+        self.held = [[] for _ in range(B)]              # (k, v) of each token, as the store holds them
+
+    def prefill(self, counts, seed=1):
+        from kv_cache_computation_gb300 import page_step
+        T = sum(counts)
+        s = page_step(self.lens, _i32(counts), self.table, self.ring, self.state, max_tokens=T, in_place=True)
+        assert int(s.status) == 0
+        _, _, k, v = self.rot(_randn((T, self.qkv.shape[1]), seed).cuda(), s.positions)
+        self.cache.append(k, v, s.slots)
+        at = 0
+        for b, n in enumerate(counts):
+            self._note(b, k[at:at + n], v[at:at + n])
+            at += n
+
+    def _note(self, b, k, v):
+        self.held[b] += list(zip(R.stored(k.double().cpu().numpy()), R.stored(v.double().cpu().numpy())))
+
+    def step(self, max_tokens=None, with_starts=True):
+        from kv_cache_computation_gb300 import page_step
+        T = self.B * self.nq if max_tokens is None else max_tokens
+        st = page_step(self.lens, self.new, self.table, self.ring, self.state, max_tokens=T, in_place=True)
+        return st, self.cache.decode_step_qkv(self.rot, self.qkv, st.positions, st.slots, self.table, st.lengths,
+                                              starts=st.starts if with_starts else None)
+
+    def check(self, out, lse, served):
+        """The requests in `served` got their nq tokens: their outputs are those of all their tokens; the others give 0."""
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for b in range(self.B):
+            if b not in served:
+                assert (out[b] == 0).all() and np.isneginf(lse[b]).all(), b
+                continue
+            rows = self.qkv[b * self.nq:(b + 1) * self.nq]
+            pos = len(self.held[b]) + torch.arange(self.nq, dtype=torch.int32).cuda()
+            _, q, k, v = self.rot(rows, pos)
+            self._note(b, k, v)
+            K, V = (np.stack(x) for x in zip(*self.held[b]))
+            o, l, mag, top = R.attention(q.double().cpu().numpy(), K, V, 1 / np.sqrt(128))
+            to, tl = R.attention_tolerance(o, mag, top, l, len(K))
+            assert (np.abs(out[b] - o) <= to).all() and (np.abs(lse[b] - l) <= tl).all(), b
+        self.check_store()
+
+    def check_store(self):
+        """Every request's tokens stand where its table says, and nothing else was written over them."""
+        table = self.table.cpu().numpy()
+        for b, held in enumerate(self.held):
+            if held:
+                t = np.arange(len(held))
+                k, v = self.cache.gather(_i32(table[b, t // 16] * 16 + t % 16))
+                for got, want in zip((k, v), zip(*held)):
+                    np.testing.assert_array_equal(got.double().cpu().numpy(), np.stack(want), err_msg=f"request {b}")
+
+
+@pytest.mark.parametrize("capture", [False, True])
+@pytest.mark.parametrize("nq", [1, 3])
+def test_idle_and_finished_requests_in_a_decode_batch(nq, capture):
+    """A batch of five with an idle slot, a request that has no new token and one that finishes, anywhere in the batch:
+    every other request gets its own positions and slots, eager and captured."""
+    lp = Loop(5, nq)
+    lp.prefill([14, 7, 0, 33, 16])
+    if capture:
+        keep = [t.clone() for t in (lp.lens, lp.table, lp.ring, lp.state)]
+        lp.step()                                           # no new tokens: nothing is stored
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res = lp.step()
+        for t, o in zip((lp.lens, lp.table, lp.ring, lp.state), keep):
+            t.copy_(o)
+    # per step: who decodes; -1 finishes
+    for t, new in enumerate(([1, 1, 0, 1, 1], [1, -1, 0, 1, 1], [0, 1, 0, -1, 1], [1, 0, 1, 0, 0], [0, 0, 0, 0, 0], [1] * 5,
+                             [-1] * 5, [0, 0, 1, 1, 0])):
+        lp.new.copy_(_i32(new) * torch.where(_i32(new) > 0, nq, 1))
+        lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 40 + t))
+        if capture:
+            graph.replay()
+            st, (out, lse) = res
+        else:
+            st, (out, lse) = lp.step()
+        lp.cache.sync()
+        assert int(st.status) == 0
+        for b, n in enumerate(new):
+            if n < 0:
+                lp.held[b] = []
+        lp.check(out, lse, [b for b, n in enumerate(new) if n > 0])
+
+
+def test_denied_requests_in_a_decode_batch():
+    """Requests that get no page are left out (their own token is not stored), the others are served; the step's status
+    says so, and nothing is left to report."""
+    lp = Loop(4, 1, pages=5)
+    lp.prefill([16, 3, 32, 15])                             # the pool is empty: 0 and 2 need a page
+    lp.new.fill_(1)
+    lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 9))
+    st, (out, lse) = lp.step()
+    lp.cache.sync()
+    assert int(st.status) == 1 and st.lengths.tolist() == [16, 4, 32, 16]
+    lp.check(out, lse, [1, 3])
+
+
+@pytest.mark.parametrize("what", ["no_starts", "other_count", "other_table", "late", "garbage"])
+def test_tokens_that_are_not_their_rows_are_refused_and_reported(what):
+    """A step whose packed tokens cannot be its rows stores nothing under another request's slots: such requests are left
+    out and sync reports it."""
+    from kv_cache_computation_gb300 import MacError
+    lp = Loop(4, 2)
+    lp.prefill([5, 17, 30, 9])
+    lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 5))
+    new, served, T, starts = [2, 2, 2, 2], [0, 1, 2, 3], 8, None
+    from kv_cache_computation_gb300 import page_step
+    if what == "no_starts":
+        new, served = [2, 0, 2, 2], [0]
+    elif what == "other_count":
+        new, served = [2, 1, 2, 3], [0, 2]
+    elif what == "other_table":
+        served = [0, 3]
+    elif what == "late":
+        T, served = 7, [0, 1, 2]
+    elif what == "garbage":
+        # request 1 is given the packed tokens 0 and 1, which are request 0's
+        starts, served = _i32([-2 ** 31, 0, 2, 2 ** 31 - 1, -5]), []
+    lp.new.copy_(_i32(new))
+    st = page_step(lp.lens, lp.new, lp.table, lp.ring, lp.state, max_tokens=T, in_place=True)
+    starts = st.starts if starts is None else starts
+    table = lp.table[[0, 2, 1, 3]] if what == "other_table" else lp.table
+    if what == "no_starts":
+        out, lse = lp.cache.decode_step_qkv(lp.rot, lp.qkv, st.positions, st.slots, table, st.lengths)
+    else:
+        out, lse = lp.cache.decode_step_qkv(lp.rot, lp.qkv, st.positions, st.slots, table, st.lengths, starts=starts)
+    with pytest.raises(MacError, match="not its rows"):
+        lp.cache.sync()
+    lp.check(out, lse, served)
+    lp.cache.sync()
+
+
+def test_step_without_starts_serves_full_batches():
+    lp = Loop(3, 2)
+    lp.prefill([5, 17, 30])
+    lp.new.fill_(2)
+    for t in range(3):
+        lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 5 + t))
+        st, (out, lse) = lp.step(with_starts=False)
+        lp.cache.sync()
+        lp.check(out, lse, [0, 1, 2])
+
+
+def test_step_on_another_stream_and_refusals():
+    lp = Loop(3, 1)
+    lp.prefill([5, 17, 30])
+    lp.new.fill_(1)
+    lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 5))
+    from kv_cache_computation_gb300 import page_step
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    st = page_step(lp.lens, lp.new, lp.table, lp.ring, lp.state, max_tokens=3, in_place=True, stream=s)
+    args = (lp.rot, lp.qkv, st.positions, st.slots, lp.table, st.lengths)
+    for kw in (dict(starts=st.starts[:3]), dict(starts=st.starts.long()), dict(starts=st.starts.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            lp.cache.decode_step_qkv(*args, **kw)
+    for a in ((lp.rot, lp.qkv, st.positions[:2], st.slots[:2], lp.table, st.lengths),
+              (lp.rot, lp.qkv, st.positions, st.slots[:2], lp.table, st.lengths),
+              (lp.rot, lp.qkv, st.positions.long(), st.slots, lp.table, st.lengths)):
+        with pytest.raises((TypeError, ValueError)):
+            lp.cache.decode_step_qkv(*a)
+    out, lse = lp.cache.decode_step_qkv(*args, starts=st.starts, stream=s)
+    s.synchronize()
+    lp.cache.sync()
+    lp.check(out, lse, [0, 1, 2])

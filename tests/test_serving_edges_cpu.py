@@ -28,3 +28,7 @@ def test_page_step_ex_refusals(native):
         bad += [{name: None}, {name: ODD}]
     for kw in bad:
         assert L.mac_page_step_ex(*{**good, **kw}.values()) == -1, kw
+
+
+def test_step_rows_refuses_a_null_handle(native):
+    assert native.lib().mac_quant_step_rows(None, 1, 1, 1, P, P, P, P, 1, 1, P, P, P, P, None) == -1
