@@ -367,6 +367,7 @@ class Loop:
         self.lens = torch.zeros(B, dtype=torch.int32).cuda()
         self.table = torch.full((B, cols), -1, dtype=torch.int32).cuda()
         self.new = torch.zeros(B, dtype=torch.int32).cuda()
+        self.rejected = torch.zeros(B, dtype=torch.int32).cuda()
         self.qkv = torch.zeros((B * nq, (H + 2 * Hkv) * 128), dtype=BF16).cuda()
         self.held = [[] for _ in range(B)]              # (k, v) of each token, as the store holds them
 
@@ -388,7 +389,8 @@ class Loop:
     def step(self, max_tokens=None, with_starts=True):
         from kv_cache_computation_gb300 import page_step
         T = self.B * self.nq if max_tokens is None else max_tokens
-        st = page_step(self.lens, self.new, self.table, self.ring, self.state, max_tokens=T, in_place=True)
+        st = page_step(self.lens, self.new, self.table, self.ring, self.state, max_tokens=T, in_place=True,
+                       rejected=self.rejected)
         return st, self.cache.decode_step_qkv(self.rot, self.qkv, st.positions, st.slots, self.table, st.lengths,
                                               starts=st.starts if with_starts else None)
 
@@ -535,3 +537,43 @@ def test_step_on_another_stream_and_refusals():
     s.synchronize()
     lp.cache.sync()
     lp.check(out, lse, [0, 1, 2])
+
+
+@pytest.mark.parametrize("capture", [False, True])
+def test_drafted_steps_with_rejections_in_a_decode_batch(capture):
+    """Four slots that verify three drafted tokens a step and take back up to all of them, one idle, one that finishes and
+    starts again: every output is that of the tokens that were kept, and no page is lost."""
+    lp = Loop(4, 3, pages=20, cols=10)
+    lp.prefill([14, 47, 0, 30])
+    if capture:
+        keep = [t.clone() for t in (lp.lens, lp.table, lp.ring, lp.state)]
+        lp.step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res = lp.step()
+        for t, o in zip((lp.lens, lp.table, lp.ring, lp.state), keep):
+            t.copy_(o)
+    r, last = np.random.default_rng(4), [0] * 4
+    for t in range(24):
+        new = [3, 3 if t % 4 else 0, 3 if t > 5 else 0, -1 if t == 12 else 3]
+        back = [int(r.integers(0, n + 1)) if new[b] >= 0 else 0 for b, n in enumerate(last)]
+        for b in range(4):
+            lp.held[b] = [] if new[b] < 0 else lp.held[b][:len(lp.held[b]) - back[b]]
+        lp.new.copy_(_i32(new))
+        lp.rejected.copy_(_i32(back))
+        lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 70 + t))
+        if capture:
+            graph.replay()
+            st, (out, lse) = res
+        else:
+            st, (out, lse) = lp.step()
+        lp.cache.sync()
+        assert int(st.status) == 0
+        lp.check(out, lse, [b for b in range(4) if new[b] > 0])
+        last = [max(n, 0) for n in new]
+        assert st.lengths.tolist() == [len(h) for h in lp.held]
+        N, table, ring = 20, lp.table.cpu().numpy(), lp.ring.cpu().numpy()
+        head, count = lp.state.tolist()
+        held = [int(p) for b in range(4) for p in table[b, :PR.pages(len(lp.held[b]))]]
+        assert sorted(held + [int(ring[(head + i) % N]) for i in range(count)]) == list(range(N))
