@@ -211,7 +211,8 @@ class MacAttention:
     def decode_step_qkv(self, rotary, qkv, positions, q_weight=None, k_weight=None, out=None, lse=None, want_lse=True,
                         stream=None):
         """decode_step from the layer's QKV projection [batch, (heads + 2 kv_heads) * 128]: `rotary` (a QkvRotary of
-        the same heads) makes the four inputs.  positions int32 [batch]: each new token's 0-based index."""
+        the same heads) makes the four inputs.  positions int32 [batch]: each request's new token's 0-based index (a step
+        stores a token for every request of the batch, so these are page_step's only if every one has a new token)."""
         if rotary.heads != self.heads or rotary.kv_heads != self.kv_heads:
             raise ValueError("rotary was made for other heads")
         if qkv.device != self.device:

@@ -13,9 +13,9 @@
 // one.  A division per element would cost more than the rest of the kernel.
 //
 // What bounds them, 32768 tokens of 8 heads: the append (134 MB in, 38 MB out)
-// 32.6 us, 5.3 TB/s, the loads' latency at half occupancy (four tokens' blocks
+// 32 us, 5.4 TB/s, the loads' latency at half occupancy (four tokens' blocks
 // per lane; three or six blocks per SM instead of four: 36 and 40 us); the gather
-// (38 MB in, 134 MB out) 33 us, 4.07 TB/s of writes, which is what a plain fill
+// (38 MB in, 134 MB out) 34 us, 4.0 TB/s of writes, which is what a plain fill
 // reaches (4.03).  8 tokens: 1.7 and 1.5 us in a captured graph, launch and latency.
 #include "../../include/mac.h"
 #include "mac_device.cuh"
@@ -37,8 +37,9 @@ namespace {
 
 constexpr int kThreads = 256;
 // From this many (token, head) pairs on a lane takes four tokens; below, one
-// block per lane spreads further.  Both sides, us, 8 heads: 512 tokens 2.2 (one
-// block) against 2.8, 1024 2.6 / 2.9, 2048 3.8 / 3.6; 32768 43 / 30 (append).
+// block per lane spreads further.  Both sides, us, append of 8 heads: 512 tokens
+// 2.3 (one block) against 3.0, 1024 2.7 / 3.0, 2048 4.1 / 3.9, 8192 9.8 / 7.8,
+// 32768 38 / 32 (gather: 512 3.0 / 3.4, 8192 11.3 / 11.4, 32768 36 / 34).
 constexpr int64_t kQuadPairs = 16384;
 
 // two e2m1 codes (lo in the low four bits) of two floats, ties to even, at most 6
@@ -318,7 +319,8 @@ struct RowArgs {
 // and a lane per row.  A request's rows count only if it has exactly n_query
 // packed tokens and each of their slots is the one that its own table gives the
 // last n_query tokens of its length, which is where the attention reads them.
-// Two dependent reads behind the launch: 2.1 us in a captured graph.
+// Three dependent reads behind the launch: 1.5 us (1 request) to 1.8 (1024) in a
+// captured graph.
 __global__ void __launch_bounds__(kThreads) step_rows_kernel(const __grid_constant__ RowArgs a)
 {
     pdl_wait();

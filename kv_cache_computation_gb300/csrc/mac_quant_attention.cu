@@ -26,9 +26,10 @@
 // Roundings: Q is bf16 and becomes f16 with a power of two per row (exact but
 // for elements below 2^-28 of the row's largest, which keep 2^-39 of it);
 // stored values are exact in f16; the weights P, at most 2^15, are rounded to
-// f16 (2^-11 of each; P's factor 2^9 keeps weights down to 2^-33 of the largest)
-// and summed unrounded in fp32; scores, sums, the reference and the output stay
-// in fp32.
+// f16 (2^-11 of each, an eighth of the bf16 output's own rounding; P's factor 2^9
+// keeps weights down to 2^-33 of the largest; a second product for their low
+// halves would add half again to the tensor work) and summed unrounded in fp32;
+// scores, sums, the reference and the output stay in fp32.
 //
 // Work split.  The units (two pages) of all (request, KV head) groups form one
 // line, which is cut into equal ranges, one per warp, whatever the lengths; the
@@ -39,22 +40,24 @@
 // again by a second kernel.  No block waits for another.
 //
 // Measured (GB300, in a captured graph; stream against the copy peak of 6.7 TB/s):
-//   rows  8 KV heads x 8 x 128K (1208 MB) 204 us, 5.9 TB/s   284 instructions a page
+//   rows  8 KV heads x 8 x 128K (1208 MB) 205 us, 5.9 TB/s   288 instructions a page
 //         8 KV heads x 1 x 128K (151 MB)   37 us, 4.1
-//         8 KV heads x 1 x 4K              11 us
-//    16   1 KV head  x 8 x 128K (151 MB)   50 us, 3.0        384
+//         8 KV heads x 1 x 4K              12 us
+//    16   1 KV head  x 8 x 128K (151 MB)   51 us, 3.0        392
 //    24                                    61 us, 2.5
-//    32                                    74 us, 2.0        473
+//    32                                    77 us, 2.0        477
+// (One power of two for a whole group instead of one per row: 204, 37, 12, 51, 61
+// and 74 us, but one row's size then costs the others their bits.)
 // At 8 rows the stream runs at 6.2 TB/s while it lasts (the ALU, where a
-// conversion takes two cycles, 54 % busy, the half-rate f16 multiplies 42 %); a
+// conversion takes two cycles, 56 % busy, the half-rate f16 multiplies 42 %); a
 // single request pays the fixed chain besides: prologue 1.5 us, first page 1,
 // merge 2, second kernel 4.  Beyond 8 rows a warp's 64 to 128 output registers
 // leave 12 and 8 warps per SM, whose dependent instructions are not hidden
-// (2.2 to 1.6 instructions a cycle, tensor pipe 29 % and 39 % busy).
-// Tried and slower, us: at 8 rows (204) units of one page with 16 or 20 warps
+// (1.9 and 1.5 instructions a cycle, tensor pipe 31 % and 40 % busy).
+// Tried and slower, us: at 8 rows (then 204) units of one page with 16 or 20 warps
 // 248 and 263, 20 warps with spills 246, the next unit's scores in one block
 // with this unit's output 212, value scales for every element block in every lane
-// 240; at 16 / 32 rows (50 / 74) two warps per page with 16 rows each (84 at 32),
+// 240; at 16 / 32 rows (then 50 / 74) two warps per page with 16 rows each (84 at 32),
 // pairs of warps that split scores by page and output by element 57 / 83, a unit's
 // pages one after the other 52 / 80 and, with more warps, 58 / 170, keys
 // and accumulators in tensor memory on tcgen05 71 / 98 (four barrier round trips

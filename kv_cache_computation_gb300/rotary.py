@@ -38,8 +38,8 @@ class QkvRotary:
     (heads + 2 kv_heads) * 128] bf16 (rows may stand apart), positions int32
     [tokens] on the same GPU, the weights bf16 [128] or None for no norm.
 
-    rotary_dim: the first elements of a head that are rotated (a multiple of
-    8); interleaved: pairs (2i, 2i+1) instead of (i, i + rotary_dim/2).
+    The outputs carry no gradient.  rotary_dim: the first elements of a head
+    that are rotated (a multiple of 8); interleaved: pairs (2i, 2i+1) instead of (i, i + rotary_dim/2).
     """
 
     def __init__(self, heads, kv_heads, head_dim=128, rotary_dim=128, base=500000.0, interleaved=False, eps=1e-6):
