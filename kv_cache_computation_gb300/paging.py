@@ -24,7 +24,8 @@ class _PageStep(NamedTuple):
 class PageStep(_PageStep):
     """What page_step returns: six int32 tensors on the GPU (lengths, free_state, starts, positions, slots, status), and
     `unreleased`: of a step in place, [batch] the tokens of each finished request whose pages could not be freed
-    (status RING_FULL, or OUT_OF_RANGE: one is not of the pool), 0 for all others; else None, since the lengths passed still say it."""
+    (status RING_FULL, or OUT_OF_RANGE: one is not of the pool), 0 for all others; else None, since the lengths passed
+    still say it."""
     unreleased = None
 
 

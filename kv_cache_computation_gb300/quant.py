@@ -150,12 +150,12 @@ class QuantKV:
         table, row, cols = _table(page_table, B, self.device)
         if cols < 1 or row < cols:
             raise ValueError("page_table must have a column, and rows that do not overlap")
-        packed = positions.numel()
+        packed = min(positions.numel(), slots.numel())
         if starts is None and packed < n:
-            raise ValueError(f"positions must hold the {n} new tokens, got {packed}")
+            raise ValueError(f"positions and slots must hold the {n} new tokens, got {packed}")
         lp = _dev(lengths, "lengths", torch.int32, (B,), self.device)
-        pp = _dev(positions, "positions", torch.int32, (packed,), self.device)
-        sp = _dev(slots, "slots", torch.int32, (packed,), self.device)
+        pp = _dev(positions, "positions", torch.int32, (positions.numel(),), self.device)
+        sp = _dev(slots, "slots", torch.int32, (slots.numel(),), self.device)
         first = None if starts is None else _dev(starts, "starts", torch.int32, (B + 1,), self.device)
         with _on(self.device, stream):
             rows = _out((2 * n + B,), self.device, torch.int32)
@@ -169,6 +169,6 @@ class QuantKV:
         return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lens, stream=stream)
 
     def sync(self):
-        """Wait for the device; raises MacError if its checks met a bad slot, page or length since the last call."""
+        """Wait for the device; raises MacError if its checks met a bad slot, page, length or row since the last call."""
         with _on(self.device, None):
             _check("mac_quant_sync", N.lib().mac_quant_sync(self._h), self._h)

@@ -539,6 +539,22 @@ def test_step_on_another_stream_and_refusals():
     lp.check(out, lse, [0, 1, 2])
 
 
+def test_positions_and_slots_of_different_lengths():
+    """Only the new tokens' entries are read: either array may be longer."""
+    from kv_cache_computation_gb300 import page_step
+    lp = Loop(3, 1)
+    lp.prefill([5, 17, 30])
+    lp.new.fill_(1)
+    for t, kw in enumerate((dict(), dict(), dict(starts=True), dict(starts=True))):
+        lp.qkv.copy_(_randn(tuple(lp.qkv.shape), 5 + t))
+        st = page_step(lp.lens, lp.new, lp.table, lp.ring, lp.state, max_tokens=8, in_place=True)
+        pos, slots = (st.positions[:3], st.slots) if t % 2 else (st.positions, st.slots[:3].clone())
+        out, lse = lp.cache.decode_step_qkv(lp.rot, lp.qkv, pos, slots, lp.table, st.lengths,
+                                            starts=st.starts if kw else None)
+        lp.cache.sync()
+        lp.check(out, lse, [0, 1, 2])
+
+
 @pytest.mark.parametrize("capture", [False, True])
 def test_drafted_steps_with_rejections_in_a_decode_batch(capture):
     """Four slots that verify three drafted tokens a step and take back up to all of them, one idle, one that finishes and
