@@ -10,7 +10,7 @@ the library's operators (True).
 The 8-bit format (both forms and :func:`exact`): the 16 tokens of a page share,
 per KV head and for keys and values apart, a scale 2^e, and an element x is held
 as e4m3(x / 2^e) (round to nearest even, at most 448).  A token needs the
-smallest e in -100 .. 119 whose 448 * 2^e is at least its largest element.  A
+smallest e in -60 .. 60 whose 448 * 2^e is at least its largest element.  A
 call that stores the first slot of a page starts the page anew: e is the largest
 that its tokens need.  Otherwise e is the larger of that and the page's old e,
 and where it grows, the page's other slots are rounded again at the new scale.
@@ -24,7 +24,7 @@ own = False
 
 D = 128          # head dimension
 PAGE = 16        # tokens per page
-E_MIN, E_MAX = -100, 119
+E_MIN, E_MAX = -60, 60
 
 
 def _dev():
