@@ -521,6 +521,71 @@ mac_status mac_quant_sync(mac_quant_handle h);
 /* Text of the handle's last error, or "" (owned by the handle). */
 const char *mac_quant_last_error(mac_quant_handle h);
 
+/* A paged KV store of 8 bits per value, one layer per handle: between the bf16
+ * store's 512 and the 4-bit store's 144 bytes per token and KV head, 258.  The
+ * 16 tokens of a page share, per KV head and for keys and values apart, a scale
+ * 2^e, and an element x is held as e4m3(x / 2^e) (to nearest even, at most 448;
+ * a NaN or an infinity is held as NaN and does not count towards e).  A token
+ * needs the smallest e in -60 .. 60 whose 448 * 2^e is at least its largest
+ * element. */
+typedef struct mac_block_ctx *mac_block_handle;
+
+typedef struct {
+    int heads, kv_heads;   /* heads % kv_heads == 0, heads <= 4096               */
+    int head_dim;          /* must be 128                                        */
+    int page_size;         /* must be 16                                         */
+    int num_pages;         /* pages in the store, 1 .. 2^27 - 1                  */
+    int max_batch;         /* requests per attention call, 1..1024               */
+    int max_query;         /* query tokens per request and call, >= 1;           */
+                           /* heads / kv_heads * max_query <= 32                 */
+    float sm_scale;        /* score scale; 0 selects 1/sqrt(head_dim)            */
+} mac_block_config;
+
+/* As mac_quant_query_sizes, mac_quant_create and mac_quant_destroy, with their
+ * rules on devices, ordering and shared scratches (64 .. 68 bytes of it per page
+ * are the append's; a shared one may serve handles of different num_pages if it
+ * is large enough for each). */
+mac_status mac_block_query_sizes(const mac_block_config *cfg, size_t *store_bytes, size_t *scratch_bytes);
+mac_status mac_block_create(const mac_block_config *cfg, void *dev_store, size_t store_bytes, void *dev_scratch,
+                            size_t scratch_bytes, mac_block_handle *out);
+mac_status mac_block_destroy(mac_block_handle h);
+
+/* Store n_tokens tokens of K (post-RoPE) and V, bf16, token t's kv_heads x 128
+ * elements at t * stride (elements, multiples of 8; 16-byte aligned), at
+ * dev_slots[t] = page * 16 + offset, in any order; a negative slot skips its
+ * token, one past the store is refused (mac_block_sync reports it), and of tokens
+ * with one slot the last is stored.  A page is filled from its slot 0 on, and a
+ * call that stores slot 0 starts the page anew: its scale is the largest that
+ * the call's tokens need, and its other slots hold zeros.  In any other call the
+ * scale is the larger of that and the page's old one; where it grows, the codes
+ * of the page's other slots are rounded again at the new scale (exact but for
+ * codes that fall below 2^-6).  Async on stream. */
+mac_status mac_block_append(mac_block_handle h, int n_tokens, const void *dev_k, int64_t k_stride, const void *dev_v,
+                            int64_t v_stride, const int32_t *dev_slots, void *stream);
+
+/* Read tokens back: dev_k, dev_v bf16 [n_tokens][kv_heads][128], the stored
+ * values (exact in bf16; zeros for a negative or refused slot).  For the prompt
+ * attention of a chunk behind stored tokens.  Async. */
+mac_status mac_block_gather(mac_block_handle h, int n_tokens, const int32_t *dev_slots, void *dev_k, void *dev_v,
+                            void *stream);
+
+/* mac_quant_attention and mac_quant_step_rows, over and for this store.  A NaN
+ * in a stored value gives NaN in that element of the rows that see it. */
+mac_status mac_block_attention(mac_block_handle h, int batch, int n_query, const void *dev_q, const int32_t *dev_table,
+                               int64_t table_stride, int table_cols, const int32_t *dev_lens, void *dev_out,
+                               float *dev_lse, void *stream);
+mac_status mac_block_step_rows(mac_block_handle h, int batch, int n_query, int n_packed, const int32_t *dev_starts,
+                               const int32_t *dev_pos, const int32_t *dev_slots, const int32_t *dev_table,
+                               int64_t table_stride, int table_cols, const int32_t *dev_lens, int32_t *dev_pos_out,
+                               int32_t *dev_slots_out, int32_t *dev_lens_out, void *stream);
+
+/* Wait for the device and report what its checks met since the last call:
+ * MAC_ERR_STATE (text in mac_block_last_error), which is then cleared. */
+mac_status mac_block_sync(mac_block_handle h);
+
+/* Text of the handle's last error, or "" (owned by the handle). */
+const char *mac_block_last_error(mac_block_handle h);
+
 /* Human-readable text for a status code (static storage). */
 const char *mac_status_string(mac_status s);
 

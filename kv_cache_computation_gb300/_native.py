@@ -55,9 +55,15 @@ class MacQuantConfig(ctypes.Structure):
                 ("max_batch", _i), ("max_query", _i), ("sm_scale", _f), ("k_scale", _f), ("v_scale", _f)]
 
 
+class MacBlockConfig(ctypes.Structure):
+    _fields_ = [("heads", _i), ("kv_heads", _i), ("head_dim", _i), ("page_size", _i), ("num_pages", _i),
+                ("max_batch", _i), ("max_query", _i), ("sm_scale", _f)]
+
+
 _pcfg = ctypes.POINTER(MacConfig)
 _prope = ctypes.POINTER(MacRope)
 _pqcfg = ctypes.POINTER(MacQuantConfig)
+_pbcfg = ctypes.POINTER(MacBlockConfig)
 # Every entry point include/mac.h declares: name -> (restype, argtypes).
 SIGNATURES = {
     "mac_query_sizes": (_i, [_pcfg, _psz, _psz, _psz]),
@@ -93,6 +99,15 @@ SIGNATURES = {
     "mac_quant_step_rows": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp]),
     "mac_quant_sync": (_i, [_vp]),
     "mac_quant_last_error": (ctypes.c_char_p, [_vp]),
+    "mac_block_query_sizes": (_i, [_pbcfg, _psz, _psz]),
+    "mac_block_create": (_i, [_pbcfg, _vp, _sz, _vp, _sz, ctypes.POINTER(_vp)]),
+    "mac_block_destroy": (_i, [_vp]),
+    "mac_block_append": (_i, [_vp, _i, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "mac_block_gather": (_i, [_vp, _i, _vp, _vp, _vp, _vp]),
+    "mac_block_attention": (_i, [_vp, _i, _i, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp]),
+    "mac_block_step_rows": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp]),
+    "mac_block_sync": (_i, [_vp]),
+    "mac_block_last_error": (ctypes.c_char_p, [_vp]),
     "mac_status_string": (ctypes.c_char_p, [_i]),
     "mac_last_error": (ctypes.c_char_p, [_vp]),
 }

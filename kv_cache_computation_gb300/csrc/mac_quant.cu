@@ -307,21 +307,13 @@ __global__ void __launch_bounds__(kThreads, 4) quant_quads_kernel(const __grid_c
     }
 }
 
-struct RowArgs {
-    int batch, n_query, n_packed, table_cols;
-    int64_t table_stride;
-    const int32_t *starts, *pos, *slots, *table, *lens;
-    int32_t *pos_out, *slots_out, *lens_out;
-    uint32_t *err;
-};
-
 // Packed new tokens laid out as n_query rows per request, a warp per request
 // and a lane per row.  A request's rows count only if it has exactly n_query
 // packed tokens and each of their slots is the one that its own table gives the
 // last n_query tokens of its length, which is where the attention reads them.
 // Three dependent reads behind the launch: 1.5 us (1 request) to 1.8 (1024) in a
 // captured graph.
-__global__ void __launch_bounds__(kThreads) step_rows_kernel(const __grid_constant__ RowArgs a)
+__global__ void __launch_bounds__(kThreads) step_rows_kernel(const __grid_constant__ StepRowArgs a)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31, b = (int)((blockIdx.x * kThreads + threadIdx.x) >> 5), nq = a.n_query;
@@ -388,6 +380,30 @@ Sizes sizes_of(const mac_quant_config *c)
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 }  // namespace
+
+bool step_row_args_good(const StepRowArgs &a)
+{
+    const void *need[] = {a.pos, a.slots, a.table, a.lens, a.pos_out, a.slots_out, a.lens_out};
+    for (const void *x : need)
+        if (!x || ((uintptr_t)x & 3)) return false;
+    if ((uintptr_t)a.starts & 3) return false;
+    if (!a.starts && a.n_packed < a.batch * a.n_query) return false;
+    return a.table_cols >= 1 && a.table_cols <= (1 << 26) && a.table_stride >= a.table_cols;
+}
+
+cudaError_t launch_step_rows(const StepRowArgs &a, cudaStream_t s)
+{
+    return launch_maybe_pdl(step_rows_kernel, dim3((a.batch * 32 + kThreads - 1) / kThreads), dim3(kThreads), 0, s, true, a);
+}
+
+void quant_error_text(uint32_t bits, char *text, size_t n)
+{
+    std::snprintf(text, n, "device checks met:%s%s%s%s%s", bits & kQErrPage ? " a page outside the pool" : "",
+                  bits & kQErrSlot ? " a slot outside the pool" : "",
+                  bits & kQErrLen ? " a length outside the page table" : "",
+                  bits & kQErrTimeout ? " a copy that did not arrive" : "",
+                  bits & kQErrRow ? " a request whose new tokens are not its rows of the step" : "");
+}
 
 }  // namespace macgpu
 
@@ -629,16 +645,10 @@ mac_status mac_quant_step_rows(mac_quant_handle h, int batch, int n_query, int n
     if (st != MAC_OK) return st;
     if (batch < 0 || batch > h->cfg.max_batch || n_query < 1 || n_query > h->cfg.max_query || n_packed < 0) return refuse(h);
     if (batch == 0) return MAC_OK;
-    const void *need[] = {dev_pos, dev_slots, dev_table, dev_lens, dev_pos_out, dev_slots_out, dev_lens_out};
-    for (const void *x : need)
-        if (!x || ((uintptr_t)x & 3)) return refuse(h);
-    if ((uintptr_t)dev_starts & 3) return refuse(h);
-    if (!dev_starts && n_packed < batch * n_query) return refuse(h);
-    if (table_cols < 1 || table_cols > (1 << 26) || table_stride < table_cols) return refuse(h);
-    const RowArgs a{batch,    n_query,  n_packed, table_cols,  table_stride,  dev_starts,   dev_pos,  dev_slots,
-                    dev_table, dev_lens, dev_pos_out, dev_slots_out, dev_lens_out, h->st.err};
-    const cudaError_t e = launch_maybe_pdl(step_rows_kernel, dim3((batch * 32 + kThreads - 1) / kThreads), dim3(kThreads), 0,
-                                           (cudaStream_t)stream, true, a);
+    const StepRowArgs a{batch,    n_query,  n_packed, table_cols,  table_stride,  dev_starts,   dev_pos,  dev_slots,
+                        dev_table, dev_lens, dev_pos_out, dev_slots_out, dev_lens_out, h->st.err};
+    if (!step_row_args_good(a)) return refuse(h);
+    const cudaError_t e = launch_step_rows(a, (cudaStream_t)stream);
     return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, "step rows launch");
 }
 
@@ -653,11 +663,7 @@ mac_status mac_quant_sync(mac_quant_handle h)
     if (e != cudaSuccess) return fail_cuda(h, e, "mac_quant_sync");
     h->errbuf[0] = 0;
     if (!bits) return MAC_OK;
-    std::snprintf(h->errbuf, sizeof h->errbuf, "device checks met:%s%s%s%s%s", bits & kQErrPage ? " a page outside the pool" : "",
-                  bits & kQErrSlot ? " a slot outside the pool" : "",
-                  bits & kQErrLen ? " a length outside the page table" : "",
-                  bits & kQErrTimeout ? " a copy that did not arrive" : "",
-                  bits & kQErrRow ? " a request whose new tokens are not its rows of the step" : "");
+    quant_error_text(bits, h->errbuf, sizeof h->errbuf);
     return MAC_ERR_STATE;
 }
 

@@ -85,6 +85,20 @@ struct QuantAttnArgs {
     int4 *meta;                         // groups that cross blocks: {group or -1, last block, first block, 0}
 };
 
+// A step's packed new tokens as rows (mac_quant_step_rows): arguments as in
+// include/mac.h.
+struct StepRowArgs {
+    int batch, n_query, n_packed, table_cols;
+    int64_t table_stride;
+    const int32_t *starts, *pos, *slots, *table, *lens;
+    int32_t *pos_out, *slots_out, *lens_out;
+    uint32_t *err;
+};
+
+bool step_row_args_good(const StepRowArgs &a);
+cudaError_t launch_step_rows(const StepRowArgs &a, cudaStream_t s);
+void quant_error_text(uint32_t bits, char *text, size_t n);    // the error word in words
+
 cudaError_t quant_attention_config(int sm_count);
 cudaError_t launch_quant_attention(const QuantAttnArgs &a, int sm_count, cudaStream_t s);
 

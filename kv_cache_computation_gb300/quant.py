@@ -1,5 +1,5 @@
-"""A paged KV store of 4 bits per value and decode attention over it (the
-mac_quant_* calls of include/mac.h)."""
+"""Paged KV stores of 4 and of 8 bits per value and decode attention over them
+(the mac_quant_* and mac_block_* calls of include/mac.h)."""
 from __future__ import annotations
 
 import ctypes
@@ -11,61 +11,64 @@ from .attention import _dev, _on, _out, _stream_ptr, _table
 from .rotary import _rows
 
 
-def _check(fn, status, handle=None):
-    if status != N.MAC_OK:
-        detail = (N.lib().mac_quant_last_error(handle) or b"").decode() if handle is not None and handle.value else ""
-        raise N.MacError(fn, status, detail)
-
-
 def quant_query_sizes(cfg: N.MacQuantConfig):
-    """(store_bytes, scratch_bytes) for a configuration (host only)."""
+    """(store_bytes, scratch_bytes) of a 4-bit store (host only)."""
+    return _query_sizes("mac_quant", cfg)
+
+
+def block_query_sizes(cfg: N.MacBlockConfig):
+    """(store_bytes, scratch_bytes) of an 8-bit store (host only)."""
+    return _query_sizes("mac_block", cfg)
+
+
+def _query_sizes(prefix, cfg):
     store, scratch = ctypes.c_size_t(), ctypes.c_size_t()
-    _check("mac_quant_query_sizes",
-           N.lib().mac_quant_query_sizes(ctypes.byref(cfg), ctypes.byref(store), ctypes.byref(scratch)))
+    fn = prefix + "_query_sizes"
+    status = getattr(N.lib(), fn)(ctypes.byref(cfg), ctypes.byref(store), ctypes.byref(scratch))
+    if status != N.MAC_OK:
+        raise N.MacError(fn, status)
     return store.value, scratch.value
 
 
-class QuantKV:
-    """One attention layer's 4-bit paged KV store on the current CUDA device.
+class _PagedStore:
+    """What the two stores have in common: the calls of `_prefix`, made with `cfg`."""
+    _prefix = ""
 
-    append stores post-RoPE keys and values at slots (page * 16 + offset, as
-    page_step makes them), gather reads them back, attention decodes over the
-    pages of a page table.  max_query new tokens per request and call at most
-    (heads / kv_heads * max_query <= 32).  Calls on one object must be ordered
-    with one another (they share its scratch); layers whose calls are ordered
-    may share scratch: pass another QuantKV as `share` (sync of either then
-    reports what the calls of both met).
-    """
-
-    def __init__(self, heads, kv_heads, num_pages, head_dim=128, page_size=16, max_batch=1, max_query=1, sm_scale=0.0,
-                 k_scale=1.0, v_scale=1.0, device=None, share=None):
-        self.cfg = N.MacQuantConfig(heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_query, float(sm_scale),
-                                    float(k_scale), float(v_scale))
-        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
-        self.num_pages, self.page_size, self.max_batch, self.max_query = num_pages, page_size, max_batch, max_query
+    def _create(self, cfg, device, share):
+        self.cfg = cfg
+        self.heads, self.kv_heads, self.head_dim = cfg.heads, cfg.kv_heads, cfg.head_dim
+        self.num_pages, self.page_size = cfg.num_pages, cfg.page_size
+        self.max_batch, self.max_query = cfg.max_batch, cfg.max_query
         device = torch.device("cuda" if device is None else device)
         self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
         self._h = ctypes.c_void_p()
-        store, scratch = quant_query_sizes(self.cfg)
+        store, scratch = _query_sizes(self._prefix, cfg)
         self.sizes = dict(store=store, scratch=scratch)
         with torch.cuda.device(self.device):
             self._store = torch.empty(store, dtype=torch.uint8, device=self.device)
             if share is not None:
-                if share.device != self.device or share._scratch.numel() < scratch:
-                    raise ValueError("share must be a QuantKV on the same device with as large a scratch")
+                if type(share) is not type(self) or share.device != self.device or share._scratch.numel() < scratch:
+                    raise ValueError(f"share must be a {type(self).__name__} on the same device with as large a scratch")
                 self._scratch = share._scratch
             else:
                 self._scratch = torch.empty(scratch, dtype=torch.uint8, device=self.device)
             h = ctypes.c_void_p()
-            _check("mac_quant_create",
-                   N.lib().mac_quant_create(ctypes.byref(self.cfg), self._store.data_ptr(), store, self._scratch.data_ptr(),
-                                            scratch, ctypes.byref(h)))
+            self._call("create", ctypes.byref(cfg), self._store.data_ptr(), store, self._scratch.data_ptr(), scratch,
+                       ctypes.byref(h))
         self._h = h
+
+    def _call(self, what, *args):
+        status = getattr(N.lib(), f"{self._prefix}_{what}")(*args)
+        if status != N.MAC_OK:
+            detail = ""
+            if self._h.value:
+                detail = (getattr(N.lib(), f"{self._prefix}_last_error")(self._h) or b"").decode()
+            raise N.MacError(f"{self._prefix}_{what}", status, detail)
 
     # -- lifetime -----------------------------------------------------------
     def close(self):
         if getattr(self, "_h", None) is not None and self._h.value:
-            N.lib().mac_quant_destroy(self._h)
+            getattr(N.lib(), f"{self._prefix}_destroy")(self._h)
             self._h = ctypes.c_void_p()
 
     def __del__(self):
@@ -86,8 +89,7 @@ class QuantKV:
         vp, vs = _rows(v, "v", self.kv_heads, self.head_dim)
         s = _dev(slots, "slots", torch.int32, (n,), self.device)
         with _on(self.device, stream):
-            _check("mac_quant_append", N.lib().mac_quant_append(self._h, n, kp, ks, vp, vs, s,
-                                                                _stream_ptr(stream, self.device)), self._h)
+            self._call("append", self._h, n, kp, ks, vp, vs, s, _stream_ptr(stream, self.device))
 
     def gather(self, slots, stream=None):
         """The stored k, v bf16 [tokens, kv_heads, 128] at slots int32 [tokens]; zeros where negative."""
@@ -96,8 +98,7 @@ class QuantKV:
         shape = (n, self.kv_heads, self.head_dim)
         with _on(self.device, stream):
             k, v = _out(shape, self.device), _out(shape, self.device)
-            _check("mac_quant_gather", N.lib().mac_quant_gather(self._h, n, s, k.data_ptr(), v.data_ptr(),
-                                                                _stream_ptr(stream, self.device)), self._h)
+            self._call("gather", self._h, n, s, k.data_ptr(), v.data_ptr(), _stream_ptr(stream, self.device))
         return k, v
 
     # -- attention ------------------------------------------------------------
@@ -118,12 +119,10 @@ class QuantKV:
                 out = _out(shape, self.device)
             if lse is None and want_lse:
                 lse = _out(shape[:-1], self.device, torch.float32)
-            _check("mac_quant_attention",
-                   N.lib().mac_quant_attention(self._h, B, nq, qp, table, row, cols, lp,
-                                               _dev(out, "out", torch.bfloat16, shape, self.device),
-                                               None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1],
-                                                                             self.device),
-                                               _stream_ptr(stream, self.device)), self._h)
+            self._call("attention", self._h, B, nq, qp, table, row, cols, lp,
+                       _dev(out, "out", torch.bfloat16, shape, self.device),
+                       None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1], self.device),
+                       _stream_ptr(stream, self.device))
         return out, lse
 
     def decode_step_qkv(self, rotary, qkv, positions, slots, page_table, lengths, q_weight=None, k_weight=None,
@@ -160,10 +159,8 @@ class QuantKV:
         with _on(self.device, stream):
             rows = _out((2 * n + B,), self.device, torch.int32)
             pos, slot, lens = rows[:n], rows[n:2 * n], rows[2 * n:]
-            _check("mac_quant_step_rows",
-                   N.lib().mac_quant_step_rows(self._h, B, n // B, packed, first, pp, sp, table, row, cols, lp,
-                                               pos.data_ptr(), slot.data_ptr(), lens.data_ptr(),
-                                               _stream_ptr(stream, self.device)), self._h)
+            self._call("step_rows", self._h, B, n // B, packed, first, pp, sp, table, row, cols, lp, pos.data_ptr(),
+                       slot.data_ptr(), lens.data_ptr(), _stream_ptr(stream, self.device))
         _, q, k, v = rotary(qkv, pos, q_weight, k_weight, want_pre=False, stream=stream)
         self.append(k, v, slot, stream=stream)
         return self.attention(q.view(B, n // B, self.heads, self.head_dim), page_table, lens, stream=stream)
@@ -171,4 +168,38 @@ class QuantKV:
     def sync(self):
         """Wait for the device; raises MacError if its checks met a bad slot, page, length or row since the last call."""
         with _on(self.device, None):
-            _check("mac_quant_sync", N.lib().mac_quant_sync(self._h), self._h)
+            self._call("sync", self._h)
+
+
+class QuantKV(_PagedStore):
+    """One attention layer's 4-bit paged KV store on the current CUDA device.
+
+    append stores post-RoPE keys and values at slots (page * 16 + offset, as
+    page_step makes them), gather reads them back, attention decodes over the
+    pages of a page table.  max_query new tokens per request and call at most
+    (heads / kv_heads * max_query <= 32).  Calls on one object must be ordered
+    with one another (they share its scratch); layers whose calls are ordered
+    may share scratch: pass another QuantKV as `share` (sync of either then
+    reports what the calls of both met).
+    """
+    _prefix = "mac_quant"
+
+    def __init__(self, heads, kv_heads, num_pages, head_dim=128, page_size=16, max_batch=1, max_query=1, sm_scale=0.0,
+                 k_scale=1.0, v_scale=1.0, device=None, share=None):
+        self._create(N.MacQuantConfig(heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_query,
+                                      float(sm_scale), float(k_scale), float(v_scale)), device, share)
+
+
+class BlockKV(_PagedStore):
+    """One attention layer's 8-bit paged KV store on the current CUDA device: e4m3 values with one power of two per
+    page and KV head, for keys and values apart (258 bytes per token and KV head, against QuantKV's 144 and 512 in
+    bf16).  Its calls, and what they ask for, are QuantKV's, but for two points of append: a page is filled from its
+    first slot on (a call that stores that slot starts the page anew: its other slots then hold zeros), and of tokens
+    of a call with the same slot the last one is stored.  A page's scale grows with the tokens that come to it, and
+    the tokens that it holds are rounded again when it does."""
+    _prefix = "mac_block"
+
+    def __init__(self, heads, kv_heads, num_pages, head_dim=128, page_size=16, max_batch=1, max_query=1, sm_scale=0.0,
+                 device=None, share=None):
+        self._create(N.MacBlockConfig(heads, kv_heads, head_dim, page_size, num_pages, max_batch, max_query,
+                                      float(sm_scale)), device, share)
