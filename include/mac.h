@@ -586,6 +586,67 @@ mac_status mac_block_sync(mac_block_handle h);
 /* Text of the handle's last error, or "" (owned by the handle). */
 const char *mac_block_last_error(mac_block_handle h);
 
+/* Causal attention of whole prompts, packed behind one another.  Sequence b
+ * has n = starts[b + 1] - starts[b] query tokens and m = k_starts[b + 1] -
+ * k_starts[b] keys, of which its queries are the last: query i sees the first
+ *   seen(i) = m - n + i + 1 - lag, at least 0 and at most m,
+ * and out = AS_{1:seen} of the post-RoPE query over the sequence's keys and values,
+ * lse its natural-log log-sum-exp (out 0, lse -inf where nothing is seen).  So a
+ * prompt has n = m, a chunk behind tokens that were there before n < m, and with
+ * lag = r and fp32 outputs the rows are the summaries AS_{1:pos-r} that
+ * mac_seed_ring takes. */
+typedef struct mac_prompt_ctx *mac_prompt_handle;
+
+typedef struct {
+    int heads, kv_heads;   /* heads % kv_heads == 0, heads <= 4096,              */
+                           /* heads / kv_heads <= 128                            */
+    int head_dim;          /* must be 128                                        */
+    int max_tokens;        /* query tokens per call, 1 .. 2^24                   */
+    int max_batch;         /* sequences per call, 1..1024                        */
+    float sm_scale;        /* score scale; 0 selects 1/sqrt(head_dim)            */
+} mac_prompt_config;
+
+/* Bytes of the backing buffer (host arithmetic): partial results of the items
+ * that several SMs work on, and the error word. */
+mac_status mac_prompt_query_sizes(const mac_prompt_config *cfg, size_t *scratch_bytes);
+
+/* A handle over a caller-allocated device buffer (256-byte aligned, at least
+ * that size; MAC_ERR_OOM if not) on the current device, with mac_quant_create's
+ * rules on devices, ordering and shared scratches.  Synchronous. */
+mac_status mac_prompt_create(const mac_prompt_config *cfg, void *dev_scratch, size_t scratch_bytes, mac_prompt_handle *out);
+
+/* Waits for the device, then frees the handle; the buffer stays the caller's. */
+mac_status mac_prompt_destroy(mac_prompt_handle h);
+
+/* The attention of `batch` sequences (0: nothing is done).
+ *   n_q, n_kv     tokens of q, and of k and v (n_kv at most 2^26)
+ *   lag           0 .. 2^30
+ *   dev_q, dev_k, dev_v  bf16, token t's heads x 128 (kv_heads x 128) elements at
+ *                 t * stride (elements, multiples of 8; 16-byte aligned)
+ *   dev_starts    int32 [batch + 1], 0 <= starts[b] <= starts[b + 1] <= n_q
+ *   dev_k_starts  int32 [batch + 1] likewise up to n_kv, or NULL: starts.  A
+ *                 sequence whose starts are not so is left out, which
+ *                 mac_prompt_sync reports
+ *   dev_out       [n_q][heads][128], bf16, or fp32 where out_fp32 is 1
+ *   dev_lse       fp32 [n_q][heads], or NULL
+ * Rows of no sequence are left as they are.  A key or value has no effect, NaN
+ * included, on a query that does not see it; one that sees a value that is not
+ * finite gives NaN in that element (or the infinity that the sum comes to).
+ * The softmax weights are rounded to bf16 (fp32 outputs: to 16 bits).  Results
+ * do not depend on other sequences' values, but the split of the work, and with
+ * it the order of sums, depends on all starts of the call.  Async on stream. */
+mac_status mac_prompt_attention(mac_prompt_handle h, int batch, int n_q, int n_kv, int lag, const void *dev_q, int64_t q_stride,
+                                const void *dev_k, int64_t k_stride, const void *dev_v, int64_t v_stride,
+                                const int32_t *dev_starts, const int32_t *dev_k_starts, void *dev_out, int out_fp32,
+                                float *dev_lse, void *stream);
+
+/* Wait for the device and report what its checks met since the last call:
+ * MAC_ERR_STATE (text in mac_prompt_last_error), which is then cleared. */
+mac_status mac_prompt_sync(mac_prompt_handle h);
+
+/* Text of the handle's last error, or "" (owned by the handle). */
+const char *mac_prompt_last_error(mac_prompt_handle h);
+
 /* Human-readable text for a status code (static storage). */
 const char *mac_status_string(mac_status s);
 

@@ -23,6 +23,7 @@ there is no CPU fallback.
 """
 from .attention import MacAttention, make_config, query_sizes, status_string  # noqa: F401
 from .paging import PageStep, new_page_pool, page_step  # noqa: F401
+from .prompt import PromptAttention, prompt_query_sizes  # noqa: F401
 from .quant import BlockKV, QuantKV, block_query_sizes, quant_query_sizes  # noqa: F401
 from .rotary import QkvRotary  # noqa: F401
 from ._native import MacError  # noqa: F401

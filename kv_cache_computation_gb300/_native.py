@@ -60,10 +60,16 @@ class MacBlockConfig(ctypes.Structure):
                 ("max_batch", _i), ("max_query", _i), ("sm_scale", _f)]
 
 
+class MacPromptConfig(ctypes.Structure):
+    _fields_ = [("heads", _i), ("kv_heads", _i), ("head_dim", _i), ("max_tokens", _i), ("max_batch", _i),
+                ("sm_scale", _f)]
+
+
 _pcfg = ctypes.POINTER(MacConfig)
 _prope = ctypes.POINTER(MacRope)
 _pqcfg = ctypes.POINTER(MacQuantConfig)
 _pbcfg = ctypes.POINTER(MacBlockConfig)
+_pmcfg = ctypes.POINTER(MacPromptConfig)
 # Every entry point include/mac.h declares: name -> (restype, argtypes).
 SIGNATURES = {
     "mac_query_sizes": (_i, [_pcfg, _psz, _psz, _psz]),
@@ -108,6 +114,12 @@ SIGNATURES = {
     "mac_block_step_rows": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp]),
     "mac_block_sync": (_i, [_vp]),
     "mac_block_last_error": (ctypes.c_char_p, [_vp]),
+    "mac_prompt_query_sizes": (_i, [_pmcfg, _psz]),
+    "mac_prompt_create": (_i, [_pmcfg, _vp, _sz, ctypes.POINTER(_vp)]),
+    "mac_prompt_destroy": (_i, [_vp]),
+    "mac_prompt_attention": (_i, [_vp, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i, _vp, _vp]),
+    "mac_prompt_sync": (_i, [_vp]),
+    "mac_prompt_last_error": (ctypes.c_char_p, [_vp]),
     "mac_status_string": (ctypes.c_char_p, [_i]),
     "mac_last_error": (ctypes.c_char_p, [_vp]),
 }

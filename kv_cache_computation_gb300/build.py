@@ -13,9 +13,9 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libmac.so")
 SOURCES = ["mac_api.cu", "mac_kernels.cu", "mac_attention.cu", "mac_attention_tc.cu", "mac_noalloc.cu",
            "mac_qkv.cu", "mac_pages.cu", "mac_quant.cu", "mac_quant_attention.cu",
-           "mac_block.cu", "mac_block_attention.cu"]
+           "mac_block.cu", "mac_block_attention.cu", "mac_prompt.cu", "mac_prompt_attention.cu"]
 HEADERS = ["mac_internal.cuh", "mac_device.cuh", "mac_plan.cuh", "mac_quant.cuh", "mac_quant_line.cuh",
-           "mac_quant_merge.cuh", "mac_block.cuh", os.path.join("..", "..", "include", "mac.h")]
+           "mac_quant_merge.cuh", "mac_block.cuh", "mac_prompt.cuh", os.path.join("..", "..", "include", "mac.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC"] + ARCH
 

@@ -1,0 +1,46 @@
+// Prompt attention: what the host layer (mac_prompt.cu) and the kernels
+// (mac_prompt_attention.cu) share.
+#pragma once
+#include "mac_internal.cuh"
+
+namespace macgpu {
+
+constexpr int kPMaxBatch = 1024;        // sequences per call (their item counts stand in shared memory)
+constexpr int kPMaxGroup = 128;         // query heads per KV head: a tile has at least one token
+constexpr int kPMaxCtas = 256;          // upper bound of the grid (one CTA per SM)
+constexpr int kPRows = 256;             // query rows of an item: two tiles of 128
+
+// bits of the device error word
+enum : uint32_t { kPErrStarts = 1u, kPErrTimeout = 2u };
+
+// An item that several CTAs worked on: CTA first holds its part behind its own
+// slot 1, the CTAs up to last behind their slots 0.  seq < 0: none.
+struct PromptMeta {
+    int seq, head, tile, first, last, pad[3];
+};
+
+struct PromptArgs {
+    int heads, kv_heads, G, tile_tokens;    // tile_tokens: 128 / G query tokens to a tile of 128 rows
+    int batch, lag;
+    int n_q, n_kv;                          // tokens of q and of k, v
+    const int32_t *starts, *k_starts;
+    void *out;                              // bf16, or fp32 where wide
+    int wide;
+    float *lse;
+    float scale_log2;                       // score scale x log2(e)
+    float *part_o;                          // [CTA][2][kPRows][128] unnormalised partial outputs
+    float2 *part_ml;                        // [CTA][2][kPRows] reference (log2) and sum
+    PromptMeta *meta;                       // [2 CTAs]
+    uint32_t *err;
+};
+
+struct PromptMaps {
+    CUtensorMap q, k, v;
+};
+
+cudaError_t prompt_attention_config(int sm_count);
+cudaError_t prompt_maps(const PromptArgs &a, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, PromptMaps &maps);
+cudaError_t launch_prompt_attention(const PromptArgs &a, const PromptMaps &maps, int sm_count, cudaStream_t s);
+
+}  // namespace macgpu
