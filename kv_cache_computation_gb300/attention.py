@@ -180,6 +180,32 @@ class MacAttention:
                                      pos.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)),
                                      _stream_ptr(stream, self.device)), self._h)
 
+    def prefill(self, prompt, req: int, q_pre, q_post, k, v, stream=None):
+        """A whole prompt of request `req`, which starts anew: its keys and values are stored, its attention is computed by
+        `prompt` (a PromptAttention of the same heads and scale), and the ring is seeded with its last queries and their
+        summaries AS_{1:pos-r}, so that the first decode steps can already reuse them.  q_pre, q_post bf16 [tokens, heads,
+        128] (before and after the rotation), k, v bf16 [tokens, kv_heads, 128]; at least one token.  Returns (out, lse).
+        Waits for the stream, as seed_ring does."""
+        n, L = q_post.shape[0], self.ring_len
+        if prompt.heads != self.heads or prompt.kv_heads != self.kv_heads or prompt.device != self.device:
+            raise ValueError("prompt was made for other heads or another device")
+        if (prompt.cfg.sm_scale or self.head_dim ** -0.5) != (self.cfg.sm_scale or self.head_dim ** -0.5):
+            raise ValueError("prompt was made with another scale")
+        if not 1 <= n <= prompt.max_tokens:
+            raise ValueError(f"a prompt of {n} tokens; the PromptAttention was made for 1 to {prompt.max_tokens}")
+        qs, ks = (n, self.heads, self.head_dim), (n, self.kv_heads, self.head_dim)
+        for t, name, shape in ((q_pre, "q_pre", qs), (q_post, "q_post", qs), (k, "k", ks), (v, "v", ks)):
+            _dev(t, name, torch.bfloat16, shape, self.device)
+        last = min(L, n)
+        with _guard(self.device, stream):
+            starts = torch.tensor([[0, n], [0, last]], dtype=torch.int32, device=self.device)
+            self.reset_request(req)
+            self.append_kv(req, k, v)
+            out, lse = prompt(q_post, k, v, starts[0])
+            o, z = prompt(q_post[n - last:], k, v, starts[1], starts[0], lag=self.band_r, out_dtype=torch.float32)
+            self.seed_ring(req, q_pre[n - last:], o, z, np.arange(n - last + 1, n + 1))
+        return out, lse
+
     def reset_request(self, req: int, stream=None):
         _check("mac_reset_request", N.lib().mac_reset_request(self._h, req, _stream_ptr(stream, self.device)), self._h)
 
