@@ -69,26 +69,27 @@ constexpr float kLowest = -3e38f;                   // the reference before the 
 constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescO = kIdescS | (1u << 16);
 
-// Shared-memory matrix descriptor, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// Shared-memory matrix descriptors, 128-byte swizzle, rows of 8 every 1024
+// bytes: the high word is the same for all, the low word holds the address and
+// the leading offset, both / 16, so that a step through a tile is one addition.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return addr >> 4 | (lbo >> 4) << 16; }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// D (tensor memory) = or += A B; A in shared memory (ss) or in tensor memory (ts).
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n.reg .pred p;\n.reg .b64 x, y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 x, {%1, %5};\nmov.b64 y, {%2, %5};\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n"
+                 :: "r"(d), "r"(a), "r"(b), "r"(idesc), "n"(kAdd ? 1 : 0), "n"(kDescHigh)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add)
 {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n.reg .pred p;\n.reg .b64 y;\nsetp.ne.b32 p, %4, 0;\nmov.b64 y, {%2, %5};\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n"
+                 :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kDescHigh)
                  : "memory");
 }
 
@@ -214,15 +215,20 @@ __device__ __forceinline__ Seq sequence(const PromptArgs &a, int b, bool report)
 }
 
 // One item, or the part of it that a CTA does: blocks j0 .. j1 - 1 of its keys.
+// (Scalars and selections, no arrays: an index that varies would put it in memory.)
 struct Piece {
     Seq s;
     int seq, head, tile;
-    int tok[2], rows[2];        // first query token and valid rows of tiles A and B
-    int nblk[2];                // key blocks each tile sees
+    int tok0;                   // first query token of tile A; tile B's come behind its tile_tokens
+    int rows_a, rows_b;         // valid rows
+    int nblk_a, nblk_b;         // key blocks each tile sees
     int edge;                   // first block that not every row sees whole
     int j0, j1;
     int slot;                   // -1: the whole item, else the partial slot
-    __device__ __forceinline__ int last(int x) const { return min(j1, nblk[x]); }    // tile x does blocks j0 .. last - 1
+    __device__ __forceinline__ int tok(const PromptArgs &a, int x) const { return tok0 + (x ? a.tile_tokens : 0); }
+    __device__ __forceinline__ int rows(int x) const { return x ? rows_b : rows_a; }
+    // tile x does blocks j0 .. last - 1
+    __device__ __forceinline__ int last(int x) const { return min(j1, x ? nblk_b : nblk_a); }
     __device__ __forceinline__ bool uses(int x) const { return last(x) > j0; }
 };
 
@@ -251,16 +257,15 @@ __device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, i
     const int down = in / a.kv_heads, T = a.tile_tokens;
     p.head = in - down * a.kv_heads;
     p.tile = tiles - 1 - down;
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-        p.tok[x] = (2 * p.tile + x) * T;
-        const int t = min(T, p.s.n - p.tok[x]);
-        p.rows[x] = t > 0 ? t * a.G : 0;
-        p.nblk[x] = t > 0 ? (p.s.seen(a, p.tok[x] + t - 1) + kTok - 1) / kTok : 0;
-    }
-    p.edge = p.s.seen(a, p.tok[0]) / kTok;
+    p.tok0 = 2 * p.tile * T;
+    const int ta = min(T, p.s.n - p.tok0), tb = min(T, p.s.n - p.tok0 - T);     // the item exists: ta >= 1
+    p.rows_a = ta * a.G;
+    p.rows_b = max(tb, 0) * a.G;
+    p.nblk_a = (p.s.seen(a, p.tok0 + ta - 1) + kTok - 1) / kTok;
+    p.nblk_b = tb > 0 ? (p.s.seen(a, p.tok0 + T + tb - 1) + kTok - 1) / kTok : 0;
+    p.edge = p.s.seen(a, p.tok0) / kTok;
     p.j0 = 0;
-    p.j1 = max(p.nblk[0], p.nblk[1]);
+    p.j1 = max(p.nblk_a, p.nblk_b);
     p.slot = -1;
     return p;
 }
@@ -417,6 +422,116 @@ __device__ __forceinline__ void fewer_registers()
 
 // ---- the attention --------------------------------------------------------------
 
+// O of the row times f, in tensor memory.
+__device__ __forceinline__ void rescale(uint32_t tO, float f)
+{
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        float o[16];
+        tmem_ld16(tO + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[i] *= f;
+        tmem_st16(tO + 16 * c, reinterpret_cast<const uint32_t *>(o));
+    }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ void fma2(float &x, float &y, float scale, float add)
+{
+    asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %2};\nmov.b64 c, {%3, %3};\n"
+        "fma.rn.f32x2 a, a, b, c;\nmov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(scale), "f"(add));
+}
+
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b)
+{
+    asm("{\n.reg .b64 a, b;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %3};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+// The scores of a chunk of 32 keys whose first `live` the row sees.
+__device__ __forceinline__ void hide(float *s, int live)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        if (i >= live) s[i] = -CUDART_INF_F;
+}
+
+__device__ __forceinline__ float chunk_max(const float *s, float top)
+{
+    float m[4] = {fmaxf(top, s[0]), s[1], s[2], s[3]};
+#pragma unroll
+    for (int i = 4; i < 28; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; k++) m[k] = max3(m[k], s[i + k], s[i + k + 4]);
+#pragma unroll
+    for (int k = 0; k < 4; k++) m[k] = fmaxf(m[k], s[28 + k]);
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// One block of one row: its scores in tensor memory become weights, in bf16, or
+// (kWide) as bf16 pairs hi + lo, which take the place of all 128 scores.
+template <bool kWide>
+__device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float sc, int live, bool edge, bool later, float &ref,
+                                              float &sum)
+{
+    float s[128], top = -CUDART_INF_F, part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; c++) tmem_ld32(tS + 32 * c, s + 32 * c);
+    tmem_wait_ld();
+    if (edge) {
+#pragma unroll
+        for (int c = 0; c < 4; c++) hide(s + 32 * c, live - 32 * c);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; c++) top = chunk_max(s + 32 * c, top);
+    top *= sc;
+    if (__any_sync(0xffffffffu, top - ref > kMargin)) {
+        const float now = top - ref > kMargin ? top : ref, f = ex2_approx(ref - now);
+        ref = now;
+        sum *= f;
+        // the product of the block before is complete: these scores were issued behind it
+        if (later) rescale(tO, f);
+    }
+    // 2^(s sc - ref), the exponent fused; that is off by the reference's rounding, which could pass any weight's range
+    // for references beyond 2^28: those rows take the product first
+    const bool far = fabsf(ref) >= 0x1p28f;
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+        for (int i = 0; i < 128; i++) s[i] = far ? __fmul_rn(s[i], sc) : s[i];
+        if (far) sc = 1.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        float *v = s + 32 * c;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) fma2(v[i], v[i + 1], sc, -ref);
+#pragma unroll
+        for (int i = 0; i < 32; i++) v[i] = ex2_approx(v[i]);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            add2(part[0], part[1], v[i], v[i + 1]);
+            add2(part[2], part[3], v[i + 2], v[i + 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i++) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+        tmem_st16(tS + 16 * c, w);
+        if (kWide) {
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                w[i] = bf16_pair(v[2 * i] - __uint_as_float(w[i] << 16), v[2 * i + 1] - __uint_as_float(w[i] & 0xffff0000u));
+            tmem_st16(tS + 64 + 16 * c, w);
+        }
+    }
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
+}
+
 struct Bars {
     unsigned long long full[kStages], empty[kStages];   // ring of key and value blocks
     unsigned long long q_full[2], q_empty[2];           // Q of a tile
@@ -434,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     __shared__ int s_bad[2][kD], s_dirty[2];            // first token whose value is not finite, by element; two items in turn
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail, s_written[8];                // pieces that each softmax warp is done with
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int *fail = &s_fail;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sQ = smem_u32(base), sKV = sQ + 2 * kBlockBytes;
@@ -444,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     if (tid == 0) {
         for (int i = 0; i < kStages; i++) {
             mbar_init(B_(bars.full[i]), 1);
-            mbar_init(B_(bars.empty[i]), 1);
+            mbar_init(B_(bars.empty[i]), i & 1 ? 2 : 1);        // value blocks stand in odd stages: warp 10 reads them too
         }
         for (int x = 0; x < 2; x++) {
             mbar_init(B_(bars.q_full[x]), 1);
@@ -489,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         if (sp.quota[blockIdx.x] == sp.quota[blockIdx.x + 1])
             a.part_ml[(int64_t)blockIdx.x * 2 * kPRows + tid] = make_float2(0.f, 0.f);
         for (int k = 0; ok && walk.next(a, sp, p); k++) {
-            const bool valid = row < p.rows[x];
-            const int lim = valid ? p.s.seen(a, p.tok[x] + row_tok) : 0;       // keys the row sees
+            const bool valid = row < p.rows(x);
+            const int lim = valid ? p.s.seen(a, p.tok(a, x) + row_tok) : 0;       // keys the row sees
             float ref = kLowest, sum = 0.f;
             const int last = p.last(x);
             for (int j = p.j0; j < last; j++) {
@@ -500,71 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 ns++;
                 fence_after();
-                float s[128];
-#pragma unroll
-                for (int c = 0; c < 4; c++) tmem_ld32(tS + 32 * c, s + 32 * c);
-                tmem_wait_ld();
-                if (j >= p.edge) {
-                    const int live = lim - j * kTok;
-#pragma unroll
-                    for (int c = 0; c < 128; c++)
-                        if (c >= live) s[c] = -CUDART_INF_F;
-                }
-                float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-                for (int c = 4; c < 128; c += 4) {
-                    m0 = fmaxf(m0, s[c]);
-                    m1 = fmaxf(m1, s[c + 1]);
-                    m2 = fmaxf(m2, s[c + 2]);
-                    m3 = fmaxf(m3, s[c + 3]);
-                }
-                const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;
-                const bool moves = top - ref > kMargin;
-                if (__any_sync(0xffffffffu, moves)) {
-                    const float now = moves ? top : ref, f = ex2_approx(ref - now);
-                    ref = now;
-                    sum *= f;
-                    if (j > p.j0) {
-                        // the product of the block before is complete: these scores were issued behind it
-#pragma unroll
-                        for (int c = 0; c < 8; c++) {
-                            float o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; i++) o[i] *= f;
-                            tmem_st16(tO + 16 * c, reinterpret_cast<const uint32_t *>(o));
-                        }
-                    }
-                }
-                // a fused product is off by the reference's rounding, which could pass any weight's range beyond 2^28
-                const bool far = fabsf(ref) >= 0x1p28f && ref != kLowest;
-                if (far) {
-#pragma unroll
-                    for (int c = 0; c < 128; c++) s[c] = __fmul_rn(s[c], sc);
-                }
-                const float scale = far ? 1.f : sc;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        s[32 * c + i] = ex2_approx(__fmaf_rn(s[32 * c + i], scale, -ref));
-                        part[i & 3] += s[32 * c + i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) w[i] = bf16_pair(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]);
-                    tmem_st16(tS + 16 * c, w);
-                    if (kWide) {
-#pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            w[i] = bf16_pair(s[32 * c + 2 * i] - __uint_as_float(w[i] << 16),
-                                             s[32 * c + 2 * i + 1] - __uint_as_float(w[i] & 0xffff0000u));
-                        tmem_st16(tS + 64 + 16 * c, w);
-                    }
-                }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                const int live = lim - j * kTok;        // of the block's keys, those that the row sees
+                softmax_block<kWide>(tS, tO, sc, live, j >= p.edge, j > p.j0, ref, sum);
                 tmem_wait_st();
                 fence_before();
                 mbar_arrive(B_(bars.p_full[x]));
@@ -581,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const bool dirty = some && *(volatile int *)&s_dirty[k & 1];
             const bool part = p.slot >= 0;
             const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t at = (int64_t)(p.s.q0 + p.tok[x] + row_tok) * a.heads + p.head * a.G + row_head;
+            const int64_t at = (int64_t)(p.s.q0 + p.tok(a, x) + row_tok) * a.heads + p.head * a.G + row_head;
             const int64_t prow = ((int64_t)blockIdx.x * 2 + p.slot) * kPRows + 128 * x + row;
 #pragma unroll
             for (int c = 0; c < 4; c++) {
@@ -645,77 +697,86 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                uint32_t n = 0;             // ring uses of the pieces before
-                uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-                bool ok = true;
-                auto wait = [&](unsigned long long &bar, uint32_t k) {
-                    ok = ok && wait_or_fail(B_(bar), k & 1, fail);
-                    return ok;
-                };
-                while (ok && walk.next(a, sp, p)) {
-                    const int blocks = p.j1 - p.j0;
-                    // scores of tile x against key block j
-                    auto score = [&](int x, int j) {
-                        const uint32_t kst = sKV + (n + 2 * (j - p.j0)) % kStages * kBlockBytes, q = sQ + x * kBlockBytes;
-                        fence_after();
+            // The whole warp walks and waits, so that addresses stay uniform, and one lane issues.  A wait that gives up is
+            // noted and the walk goes on: every later wait then gives up soon, and nothing is read out of bounds.
+            uint32_t n = 0;             // ring uses of the pieces before
+            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            const uint32_t q_low = desc_low(sQ, 16), key_low = desc_low(sKV, 16), value_low = desc_low(sKV, kBlockBytes / 2);
+            auto wait = [&](unsigned long long &bar, uint32_t k) { wait_or_fail(B_(bar), k & 1, fail); };
+            auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+            // scores of tile x against the key block in stage st
+            auto score = [&](int x, uint32_t st, bool final) {
+                const uint32_t d = tmem + 128 * x, q = q_low + x * (kBlockBytes >> 4), b = key_low + st * (kBlockBytes >> 4);
+                fence_after();
+                if (lane == 0) {
+                    mma_ss<false>(d, q, b, kIdescS);
 #pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const uint32_t off = (k >> 2) * (kBlockBytes / 2) + (k & 3) * 32;
-                            mma_ss(tmem + 128 * x, smem_desc(q + off, 16, 1024), smem_desc(kst + off, 16, 1024), kIdescS, k > 0);
-                        }
-                        commit(B_(bars.s_full[x]));
-                        if (j + 1 == p.last(x)) commit(B_(bars.q_empty[x]));
-                    };
-                    // weights of tile x times value block j
-                    auto output = [&](int x, int j) {
-                        const uint32_t vst = sKV + (n + 2 * (j - p.j0) + 1) % kStages * kBlockBytes, o = tmem + 256 + 128 * x;
-                        fence_after();
-#pragma unroll
-                        for (int part = 0; part < (kWide ? 2 : 1); part++)
-#pragma unroll
-                            for (int k = 0; k < 8; k++)
-                                mma_ts(o, tmem + 128 * x + 64 * part + 8 * k, smem_desc(vst + k * 2048, kBlockBytes / 2, 1024), kIdescO,
-                                       j > p.j0 || k > 0 || part > 0);
-                        if (j + 1 == p.last(x)) commit(B_(bars.o_full[x]));
-                    };
-                    auto full = [&](uint32_t use) { return wait(bars.full[use % kStages], use / kStages); };
-                    if (blocks > 0) {
-                        if (!full(n)) break;
-                        for (int x = 0; x < 2; x++)
-                            if (p.uses(x)) {
-                                if (!wait(bars.q_full[x], nq[x]++)) break;
-                                score(x, p.j0);
-                            }
-                        if (!ok) break;
-                        commit(B_(bars.empty[n % kStages]));
+                    for (int k = 1; k < 8; k++) {
+                        const uint32_t off = ((k >> 2) * (kBlockBytes / 2) + (k & 3) * 32) >> 4;
+                        mma_ss<true>(d, q + off, b + off, kIdescS);
                     }
-                    for (int j = p.j0; j < p.j1 && ok; j++) {
-                        const uint32_t kuse = n + 2 * (j - p.j0);       // K of j; V of j is the next use, then K of j + 1
-                        const bool more = j + 1 < p.j1;
-                        if (!full(kuse + 1) || !wait(bars.v_ok[(kuse + 1) % kStages >> 1], (kuse + 1) / kStages)) break;
-                        bool next_keys = false;
-                        for (int x = 0; x < 2; x++) {
-                            if (j < p.last(x)) {
-                                if (!wait(bars.p_full[x], np[x]++)) break;
-                                output(x, j);
-                            }
-                            if (x == 1) commit(B_(bars.empty[(kuse + 1) % kStages]));
-                            if (more && !next_keys) {
-                                if (!full(kuse + 2)) break;
-                                next_keys = true;
-                            }
-                            if (j + 1 < p.last(x)) score(x, j + 1);
-                        }
-                        if (!ok) break;
-                        if (more) commit(B_(bars.empty[(kuse + 2) % kStages]));
-                    }
-                    n += 2 * blocks;
+                    commit(B_(bars.s_full[x]));
+                    if (final) commit(B_(bars.q_empty[x]));
                 }
-                // every product issued is complete before the CTA frees its tensor memory
+            };
+            // weights of tile x times the value block in stage st
+            auto output = [&](int x, uint32_t st, bool first, bool final) {
+                const uint32_t d = tmem + 256 + 128 * x, w = tmem + 128 * x, b = value_low + st * (kBlockBytes >> 4);
+                fence_after();
+                if (lane == 0) {
+                    mma_ts(d, w, b, kIdescO, !first);
+#pragma unroll
+                    for (int k = 1; k < 8; k++) mma_ts(d, w + 8 * k, b + k * (2048 >> 4), kIdescO, 1);
+                    if (kWide) {
+#pragma unroll
+                        for (int k = 0; k < 8; k++) mma_ts(d, w + 64 + 8 * k, b + k * (2048 >> 4), kIdescO, 1);
+                    }
+                    if (final) commit(B_(bars.o_full[x]));
+                }
+            };
+            auto release = [&](uint32_t use) {
+                if (lane == 0) commit(B_(bars.empty[use % kStages]));
+            };
+            while (walk.next(a, sp, p)) {
+                const int j0 = same(p.j0), j1 = same(p.j1), edge = same(p.edge), last[2] = {same(p.last(0)), same(p.last(1))};
+                if (j1 > j0) {
+                    wait(bars.full[n % kStages], n / kStages);
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+                        if (last[x] > j0) {
+                            wait(bars.q_full[x], nq[x]++);
+                            score(x, n % kStages, j0 + 1 == last[x]);
+                        }
+                    release(n);
+                }
+                for (int j = j0; j < j1; j++, n += 2) {
+                    // uses of the ring: n keys of j, n + 1 values of j, n + 2 keys of j + 1
+                    const uint32_t vst = (n + 1) % kStages, kst = (n + 2) % kStages;
+                    bool next_keys = j + 1 == j1;
+                    wait(bars.full[vst], (n + 1) / kStages);
+                    if (j >= edge) wait(bars.v_ok[vst >> 1], (n + 1) / kStages);
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        if (j < last[x]) {
+                            wait(bars.p_full[x], np[x]++);
+                            output(x, vst, j == j0, j + 1 == last[x]);
+                        }
+                        if (x == 1) release(n + 1);
+                        if (j + 1 < last[x]) {
+                            if (!next_keys) wait(bars.full[kst], (n + 2) / kStages);
+                            next_keys = true;
+                            score(x, kst, j + 2 == last[x]);
+                        }
+                    }
+                    if (j + 1 < j1) release(n + 2);
+                }
+            }
+            // every product issued is complete before the CTA frees its tensor memory
+            if (lane == 0) {
                 commit(B_(bars.done));
                 wait_bounded(B_(bars.done), 0);
             }
+            __syncwarp();
         } else if (warp == kCheckWarp) {
             uint32_t n = 0, nq[2] = {0, 0}, q_bytes = (uint32_t)a.tile_tokens * a.G * 256;
             bool ok = true;
@@ -744,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                             mbar_expect(B_(bars.q_full[x]), q_bytes);
                             for (int h = 0; h < 2; h++)
                                 tma_load(sQ + x * kBlockBytes + h * (kBlockBytes / 2), &maps.q, 64 * h, p.head * a.G,
-                                         p.s.q0 + p.tok[x], B_(bars.q_full[x]));
+                                         p.s.q0 + p.tok(a, x), B_(bars.q_full[x]));
                         }
                         nq[x]++;
                     }
@@ -788,7 +849,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(B_(bars.v_ok[st >> 1]));
+                    if (lane == 0) {
+                        mbar_arrive(B_(bars.v_ok[st >> 1]));
+                        mbar_arrive(B_(bars.empty[st]));
+                    }
                 }
                 n += 2 * (p.j1 - p.j0);
             }
