@@ -45,6 +45,7 @@
 #include "mac_prompt.cuh"
 
 #include <climits>
+#include <type_traits>
 #include <cudaTypedefs.h>
 
 namespace macgpu {
@@ -54,7 +55,9 @@ namespace {
 constexpr int kTok = 128;                           // keys per block
 constexpr int kBlockBytes = 2 * kTok * 128;         // two column halves of 128 rows x 128 bytes
 constexpr int kStages = 4;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;       // warp 11 announces the pieces
+constexpr int kPieces = 4;                          // pieces announced ahead
+constexpr int kStageBytes = 32 * 64;                // a warp's rows on their way out, 64 bytes of each
 constexpr int kThreads = 12 * 32;                   // three warpgroups; warp 11 has no role
 // registers: 168 per thread at launch (three warpgroups: 504), then 208 for the
 // softmax's two and 88 for the others'
@@ -142,6 +145,25 @@ __device__ __forceinline__ bool wait_or_fail(uint32_t mbar, uint32_t parity, vol
     return false;
 }
 
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
+// Whether a phase is complete; does not wait.
+__device__ __forceinline__ uint32_t phase_done(uint32_t mbar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(mbar), "r"(parity)
+                 : "memory");
+    return ok;
+}
+
 // Bounded wait for copies and products in flight when the CTA winds down.
 __device__ __forceinline__ void wait_bounded(uint32_t mbar, uint32_t parity)
 {
@@ -193,15 +215,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16x
 
 // ---- the work split -----------------------------------------------------------
 
-// A sequence's query tokens, keys, and the keys that query 0 sees less one
-// (before clipping).
+// A sequence: its first query row and number of queries, its first key row and
+// number of keys.
 struct Seq {
     int q0, n, k0, m;
-    __device__ __forceinline__ int seen(const PromptArgs &a, int i) const
-    {
-        const long long s = (long long)m - n - a.lag + i + 1;
-        return s <= 0 ? 0 : s < m ? (int)s : m;
-    }
 };
 
 __device__ __forceinline__ Seq sequence(const PromptArgs &a, int b, bool report)
@@ -217,32 +234,33 @@ __device__ __forceinline__ Seq sequence(const PromptArgs &a, int b, bool report)
 // One item, or the part of it that a CTA does: blocks j0 .. j1 - 1 of its keys.
 // (Scalars and selections, no arrays: an index that varies would put it in memory.)
 struct Piece {
-    Seq s;
-    int seq, head, tile;
-    int tok0;                   // first query token of tile A; tile B's come behind its tile_tokens
+    int seq, head, tile;        // seq < 0: no more pieces
+    int row0;                   // row of q and out of tile A's first token; tile B's come behind its tile_tokens
+    int key0, keys;             // the sequence's first key row, its keys
+    int first_seen;             // keys that tile A's first token sees, before clipping to 0 .. keys; one more for each token behind
     int rows_a, rows_b;         // valid rows
     int nblk_a, nblk_b;         // key blocks each tile sees
     int edge;                   // first block that not every row sees whole
     int j0, j1;
     int slot;                   // -1: the whole item, else the partial slot
-    __device__ __forceinline__ int tok(const PromptArgs &a, int x) const { return tok0 + (x ? a.tile_tokens : 0); }
     __device__ __forceinline__ int rows(int x) const { return x ? rows_b : rows_a; }
     // tile x does blocks j0 .. last - 1
     __device__ __forceinline__ int last(int x) const { return min(j1, x ? nblk_b : nblk_a); }
     __device__ __forceinline__ bool uses(int x) const { return last(x) > j0; }
+    __device__ __forceinline__ int seen(int token) const { return min(max(first_seen + token, 0), keys); }
 };
 
 struct Split {
     int pre[kPMaxBatch + 1];    // items of the sequences before b
     int scan[kThreads / 32];
     int cost[2 * kPMaxCtas];    // prefix of the blocks of the items of the line
-    int load[kPMaxCtas];        // blocks that the CTAs do in whole items
+    unsigned long long load[kPMaxCtas];     // blocks that the CTAs do in whole items
     int quota[kPMaxCtas + 1];   // where the CTAs' shares of the line begin
-    int rounds, line_items;
+    int rounds, line_items, line_blocks;
 };
 
-// Item `i` of the call.
-__device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, int i)
+// Item `i` of the call; known: the sequences, where they are at hand.
+__device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, int i, const Seq *known)
 {
     int lo = 0, hi = a.batch;           // the last b with pre[b] <= i
     while (hi - lo > 1) {
@@ -252,18 +270,22 @@ __device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, i
     }
     Piece p;
     p.seq = lo;
-    p.s = sequence(a, lo, false);
-    const int in = i - sp.pre[lo], tiles = (sp.pre[lo + 1] - sp.pre[lo]) / a.kv_heads;
-    const int down = in / a.kv_heads, T = a.tile_tokens;
+    const Seq s = known ? known[lo] : sequence(a, lo, false);
+    const uint32_t in = i - sp.pre[lo], tiles = (uint32_t)(sp.pre[lo + 1] - sp.pre[lo]) / (uint32_t)a.kv_heads;
+    const uint32_t down = in / (uint32_t)a.kv_heads;
+    const int T = a.tile_tokens;
     p.head = in - down * a.kv_heads;
     p.tile = tiles - 1 - down;
-    p.tok0 = 2 * p.tile * T;
-    const int ta = min(T, p.s.n - p.tok0), tb = min(T, p.s.n - p.tok0 - T);     // the item exists: ta >= 1
+    const int tok0 = 2 * p.tile * T, ta = min(T, s.n - tok0), tb = max(min(T, s.n - tok0 - T), 0);  // the item exists: ta >= 1
+    p.row0 = s.q0 + tok0;
+    p.key0 = s.k0;
+    p.keys = s.m;
+    p.first_seen = s.m - s.n - a.lag + tok0 + 1;
     p.rows_a = ta * a.G;
-    p.rows_b = max(tb, 0) * a.G;
-    p.nblk_a = (p.s.seen(a, p.tok0 + ta - 1) + kTok - 1) / kTok;
-    p.nblk_b = tb > 0 ? (p.s.seen(a, p.tok0 + T + tb - 1) + kTok - 1) / kTok : 0;
-    p.edge = p.s.seen(a, p.tok0) / kTok;
+    p.rows_b = tb * a.G;
+    p.nblk_a = (p.seen(ta - 1) + kTok - 1) / kTok;
+    p.nblk_b = tb > 0 ? (p.seen(T + tb - 1) + kTok - 1) / kTok : 0;
+    p.edge = p.seen(0) / kTok;
     p.j0 = 0;
     p.j1 = max(p.nblk_a, p.nblk_b);
     p.slot = -1;
@@ -295,8 +317,9 @@ __device__ __forceinline__ int block_scan(Split &sp, int v, int *total)
     return before + x - v;
 }
 
-// The whole split, by all threads of the CTA.
-__device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
+// The whole split, by all threads of the CTA.  known: room for the sequences,
+// which all items are looked up in.
+__device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *known)
 {
     const int tid = threadIdx.x, grid = gridDim.x;
     int items = 0;
@@ -305,6 +328,7 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
         int own = 0, all;
         if (b < a.batch) {
             const Seq s = sequence(a, b, blockIdx.x == 0);
+            known[b] = s;
             own = (s.n + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) * a.kv_heads;
         }
         const int at = block_scan(sp, own, &all);
@@ -312,21 +336,20 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
         items += all;
     }
     if (tid == 0) sp.pre[a.batch] = items;
+    if (tid < kPMaxCtas) sp.load[tid] = 0;
     __syncthreads();
     const int rounds = max(items / grid - 1, 0), first = rounds * grid, line = items - first;
     // blocks of the whole items
-    for (int c = tid; c < grid; c += kThreads) {
-        int load = 0;
-        for (int r = 0; r < rounds; r++)
-            load = min(load + item_cost(item_at(a, sp, r * grid + (r & 1 ? grid - 1 - c : c))), 1 << 29);
-        sp.load[c] = load;
+    for (int i = tid; i < first; i += kThreads) {
+        const int r = i / grid, at = i - r * grid;
+        atomicAdd(&sp.load[r & 1 ? grid - 1 - at : at], (unsigned long long)item_cost(item_at(a, sp, i, known)));
     }
     // blocks of the line
     int total = 0;
     for (int i0 = 0; i0 < line; i0 += kThreads) {
         const int i = i0 + tid;
         int all;
-        const int own = i < line ? item_cost(item_at(a, sp, first + i)) : 0;
+        const int own = i < line ? item_cost(item_at(a, sp, first + i, known)) : 0;
         const int at = block_scan(sp, own, &all);
         if (i < line) sp.cost[i] = total + at;
         total += all;
@@ -334,35 +357,47 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
     __syncthreads();
     if (tid < 32) {
         // the level at which the CTAs' shares, level - load, add up to the line
-        int top = 0;
-        for (int c = tid; c < grid; c += 32) top = max(top, sp.load[c]);
-        top = __reduce_max_sync(0xffffffffu, top);
-        int lo = 0, hi = top + (total + grid - 1) / grid;       // hi is enough
-        while (lo < hi) {
-            const int mid = lo + (hi - lo) / 2;
-            long long sum = 0;
-            for (int c = tid; c < grid; c += 32) sum += max(mid - sp.load[c], 0);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (sum >= total) hi = mid;
-            else lo = mid + 1;
+        long long top = 0, sum = 0;
+        for (int c = tid; c < grid; c += 32) {
+            top = max(top, (long long)sp.load[c]);
+            sum += sp.load[c];
         }
-        int at = 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        long long lo = (sum + total + grid - 1) / grid, hi = lo;
+        if (lo < top) {                 // some CTAs are past it already
+            hi = top + (total + grid - 1) / grid;
+            while (lo < hi) {
+                const long long mid = lo + (hi - lo) / 2;
+                sum = 0;
+                for (int c = tid; c < grid; c += 32) sum += max(mid - (long long)sp.load[c], 0ll);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (sum >= total) hi = mid;
+                else lo = mid + 1;
+            }
+        }
+        long long at = 0;
         for (int c0 = 0; c0 < grid; c0 += 32) {
-            const int c = c0 + tid, own = c < grid ? max(hi - sp.load[c], 0) : 0;
-            int x = own;
+            const int c = c0 + tid;
+            const long long own = c < grid ? max(hi - (long long)sp.load[c], 0ll) : 0;
+            long long x = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
                 if (tid >= o) x += y;
             }
-            if (c < grid) sp.quota[c] = min(at + x - own, total);
-            at = min(at + __shfl_sync(0xffffffffu, x, 31), total);
+            if (c < grid) sp.quota[c] = (int)min(at + x - own, (long long)total);
+            at = min(at + __shfl_sync(0xffffffffu, x, 31), (long long)total);
         }
         if (tid == 0) {
             sp.quota[grid] = total;
             sp.rounds = rounds;
             sp.line_items = line;
+            sp.line_blocks = total;
         }
     }
     __syncthreads();
@@ -385,28 +420,52 @@ struct Walk {
         }
         item = lo;
     }
-    __device__ __forceinline__ bool next(const PromptArgs &a, const Split &sp, Piece &p)
+    __device__ __forceinline__ Piece next(const PromptArgs &a, const Split &sp)
     {
         const int grid = gridDim.x;
+        Piece p;
+        p.seq = -1;
         if (round < sp.rounds) {
-            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x));
+            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x), nullptr);
             round++;
-            return true;
+        } else if (at < end) {
+            p = item_at(a, sp, sp.rounds * grid + item, nullptr);
+            const int start = sp.cost[item], stop = start + item_cost(p);
+            const bool begins = start >= at, ends = stop <= end;
+            if (!begins || !ends) {
+                p.slot = begins ? 1 : 0;
+                p.j0 = at - start;
+                p.j1 = min(p.j1, end - start);
+            }
+            at = min(stop, end);
+            item++;
         }
-        if (at >= end) return false;
-        p = item_at(a, sp, sp.rounds * grid + item);
-        const int start = sp.cost[item], stop = start + item_cost(p);
-        const bool begins = start >= at, ends = stop <= end;
-        if (!begins || !ends) {
-            p.slot = begins ? 1 : 0;
-            p.j0 = at - start;
-            p.j1 = min(p.j1, end - start);
-        }
-        at = min(stop, end);
-        item++;
-        return true;
+        return p;
     }
 };
+
+// A warp's 32 rows of 64 bytes in shared memory, the 16-byte quarter q of row r
+// at q ^ (r / 2 % 4): row by row (a lane's own) and, eight rows at a time, quarter
+// by quarter without bank conflicts.
+__device__ __forceinline__ void put_row(uint32_t stage, int row, const uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n"
+                     :: "r"(stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4)), "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]),
+                        "r"(w[4 * q + 3])
+                     : "memory");
+}
+
+__device__ __forceinline__ uint4 get_quarter(uint32_t stage, int row, int q)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4))
+                 : "memory");
+    return v;
+}
 
 template <int N>
 __device__ __forceinline__ void more_registers()
@@ -537,6 +596,35 @@ struct Bars {
     unsigned long long q_full[2], q_empty[2];           // Q of a tile
     unsigned long long s_full[2], p_full[2], o_full[2]; // scores made, weights written, output complete
     unsigned long long v_ok[2], done;                   // values of an odd stage looked through
+    unsigned long long next[kPieces], free[kPieces];    // pieces announced, and taken back by all that follow them
+};
+
+// The pieces ahead, and for each the first token whose value is not finite, by
+// element.
+struct Queue {
+    Piece piece[kPieces];
+    int bad[kPieces][kD], dirty[kPieces];
+};
+
+// Follows the queue: take(p) waits for the next piece (false: none, or a wait
+// gave up), done() gives its place back.
+struct Follow {
+    Queue &q;
+    Bars &bars;
+    volatile int *fail;
+    uint32_t k = 0;
+    __device__ __forceinline__ int place() const { return k % kPieces; }
+    __device__ __forceinline__ const Piece *take()
+    {
+        if (!wait_or_fail(smem_u32(&bars.next[place()]), k / kPieces & 1, fail)) return nullptr;
+        const Piece *p = &q.piece[place()];
+        return p->seq < 0 ? nullptr : p;
+    }
+    __device__ __forceinline__ void done(bool one)
+    {
+        if (one) mbar_arrive(smem_u32(&bars.free[place()]));
+        k++;
+    }
 };
 
 template <bool kWide>
@@ -546,9 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     extern __shared__ __align__(1024) uint8_t dyn_raw[];
     __shared__ Split sp;
     __shared__ __align__(8) Bars bars;
-    __shared__ int s_bad[2][kD], s_dirty[2];            // first token whose value is not finite, by element; two items in turn
+    __shared__ Queue queue;
+    __shared__ __align__(16) uint8_t stage_raw[8][kStageBytes];     // a softmax warp's rows on their way out
     __shared__ uint32_t s_tmem;
-    __shared__ int s_fail, s_written[8];                // pieces that each softmax warp is done with
+    __shared__ int s_fail;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int *fail = &s_fail;
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
@@ -570,12 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             mbar_init(B_(bars.v_ok[x]), 1);
         }
         mbar_init(B_(bars.done), 1);
+        for (int i = 0; i < kPieces; i++) {
+            mbar_init(B_(bars.next[i]), 1);
+            mbar_init(B_(bars.free[i]), 11);                    // the softmax warps, the products', the loader and warp 10
+        }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s_fail = 0;
     }
-    if (tid < 2 * kD) s_bad[tid / kD][tid % kD] = INT_MAX;
-    if (tid < 2) s_dirty[tid] = 0;
-    if (tid < 8) s_written[tid] = 0;
+    for (int i = tid; i < kPieces * kD; i += kThreads) queue.bad[i / kD][i % kD] = INT_MAX;
+    if (tid < kPieces) queue.dirty[tid] = 0;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n"
                      :: "r"(smem_u32(&s_tmem)), "r"(kTmemCols) : "memory");
@@ -584,17 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = 0;            // all 512 columns: the allocation starts at column 0
+    if (tid == 0 && s_tmem != 0) s_fail = 1;
     pdl_wait();
-    make_split(a, sp);
+    make_split(a, sp, reinterpret_cast<Seq *>(base));
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");      // copies will land where the sequences stood
+    __syncthreads();
 
-    Piece p;
-    Walk walk(sp);
+    Follow follow{queue, bars, fail};
     if (warp < 8) {
         more_registers<kSoftmaxRegs>();
         // softmax and output: a thread per row of its tile
         const int x = warp >> 2, row = tid & 127;
-        const int row_tok = row / a.G, row_head = row - row_tok * a.G;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + 128 * x + lanes, tO = tmem + 256 + 128 * x + lanes;
         const float sc = a.scale_log2;
@@ -603,12 +696,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         // a CTA without a share of the line has no part in the items that span it
         if (sp.quota[blockIdx.x] == sp.quota[blockIdx.x + 1])
             a.part_ml[(int64_t)blockIdx.x * 2 * kPRows + tid] = make_float2(0.f, 0.f);
-        for (int k = 0; ok && walk.next(a, sp, p); k++) {
-            const bool valid = row < p.rows(x);
-            const int lim = valid ? p.s.seen(a, p.tok(a, x) + row_tok) : 0;       // keys the row sees
+        while (const Piece *p = follow.take()) {
+            const int j0 = p->j0, last = p->last(x), edge = p->edge;
+            const bool valid = row < p->rows(x);
+            const int lim = valid ? p->seen(x * a.tile_tokens + row / a.G) : 0;       // keys the row sees
             float ref = kLowest, sum = 0.f;
-            const int last = p.last(x);
-            for (int j = p.j0; j < last; j++) {
+            for (int j = j0; j < last; j++) {
                 if (!wait_or_fail(B_(bars.s_full[x]), ns & 1, fail)) {
                     ok = false;
                     break;
@@ -616,25 +709,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 ns++;
                 fence_after();
                 const int live = lim - j * kTok;        // of the block's keys, those that the row sees
-                softmax_block<kWide>(tS, tO, sc, live, j >= p.edge, j > p.j0, ref, sum);
+                softmax_block<kWide>(tS, tO, sc, live, j >= edge, j > j0, ref, sum);
                 tmem_wait_st();
                 fence_before();
                 mbar_arrive(B_(bars.p_full[x]));
             }
             if (!ok) break;
 
-            // the row's output, or its part of one
-            const bool some = last > p.j0;
+            // The rows' outputs, or their part of them: scaled by the row's thread, then through shared memory, 64 bytes of
+            // each of the warp's rows at a time, so that four lanes write 64 bytes of a row.
+            const bool some = last > j0;
             if (some) {
                 if (!wait_or_fail(B_(bars.o_full[x]), no & 1, fail)) break;
                 no++;
                 fence_after();
             }
-            const bool dirty = some && *(volatile int *)&s_dirty[k & 1];
-            const bool part = p.slot >= 0;
-            const float inv = part ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t at = (int64_t)(p.s.q0 + p.tok(a, x) + row_tok) * a.heads + p.head * a.G + row_head;
-            const int64_t prow = ((int64_t)blockIdx.x * 2 + p.slot) * kPRows + 128 * x + row;
+            const int slot = p->slot, rows = p->rows(x);
+            const bool part = slot >= 0, dirty = some && *(volatile int *)&queue.dirty[follow.place()];
+            const float scale = !some || sum == 0.f ? 0.f : part ? 1.f : 1.f / sum;
+            // where the rows 8 i + lane / 4 of the warp's 32 go, in elements: -1 where they are not valid
+            const int64_t out_row = (int64_t)(p->row0 + x * a.tile_tokens) * a.heads + p->head * a.G;
+            const int64_t part_row = ((int64_t)blockIdx.x * 2 + slot) * kPRows + 128 * x;
+            int64_t to[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = (warp & 3) * 32 + 8 * i + (lane >> 2), t = r / a.G;
+                to[i] = r >= rows ? -1 : (part ? part_row + r : out_row + (int64_t)t * a.heads + (r - t * a.G)) * kD;
+            }
+            const uint32_t stage = smem_u32(stage_raw[warp]);
+            const bool fp32 = part || kWide;
+            float *out32 = part ? a.part_o : reinterpret_cast<float *>(a.out);
 #pragma unroll
             for (int c = 0; c < 4; c++) {
                 float o[32];
@@ -645,29 +749,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
 #pragma unroll
                 for (int i = 0; i < 32; i++) {
-                    o[i] = some && sum != 0.f ? o[i] * inv : 0.f;
-                    if (dirty && s_bad[k & 1][32 * c + i] < lim) o[i] = CUDART_NAN_F;
+                    o[i] = scale != 0.f ? o[i] * scale : 0.f;
+                    if (dirty && queue.bad[follow.place()][32 * c + i] < lim) o[i] = CUDART_NAN_F;
                 }
-                if (!valid) continue;
-                if (part || kWide) {
-                    float *dst = part ? a.part_o + prow * kD + 32 * c : reinterpret_cast<float *>(a.out) + at * kD + 32 * c;
+                if (fp32) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int half = 0; half < 2; half++) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) w[i] = __float_as_uint(o[16 * half + i]);
+                        put_row(stage, lane, w);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
+                            if (to[i] >= 0) *reinterpret_cast<uint4 *>(out32 + to[i] + 32 * c + 16 * half + 4 * (lane & 3)) = v;
+                        }
+                        __syncwarp();
+                    }
                 } else {
-                    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(a.out) + at * kD + 32 * c;
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(bf16_pair(o[i], o[i + 1]), bf16_pair(o[i + 2], o[i + 3]),
-                                                                         bf16_pair(o[i + 4], o[i + 5]), bf16_pair(o[i + 6], o[i + 7]));
+                    for (int i = 0; i < 16; i++) w[i] = bf16_pair(o[2 * i], o[2 * i + 1]);
+                    put_row(stage, lane, w);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
+                        if (to[i] >= 0)
+                            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + to[i] + 32 * c + 8 * (lane & 3)) = v;
+                    }
+                    __syncwarp();
                 }
             }
             if (valid) {
-                if (part) a.part_ml[prow] = make_float2(ref, sum);
-                else if (a.lse) a.lse[at] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
+                const int t = row / a.G;
+                if (part) a.part_ml[part_row + row] = make_float2(ref, sum);
+                else if (a.lse)
+                    a.lse[out_row + (int64_t)t * a.heads + (row - t * a.G)] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) *(volatile int *)&s_written[warp] = k + 1;
+            follow.done(lane == 0);
         }
     } else {
         fewer_registers<kOtherRegs>();
@@ -675,8 +798,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             if (lane == 0) {
                 uint32_t n = 0;             // blocks issued: use n of the ring is in stage n % kStages
                 bool ok = true;
-                while (ok && walk.next(a, sp, p)) {
-                    for (int j = p.j0; j < p.j1 && ok; j++)
+                while (const Piece *p = follow.take()) {
+                    const int j1 = p->j1, head = p->head, key0 = p->key0;
+                    for (int j = p->j0; j < j1 && ok; j++)
                         for (int kv = 0; kv < 2; kv++, n++) {
                             const uint32_t st = n % kStages, turn = n / kStages;
                             if (turn && !wait_or_fail(B_(bars.empty[st]), (turn - 1) & 1, fail)) {
@@ -687,8 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                             const CUtensorMap *map = kv ? &maps.v : &maps.k;
                             mbar_expect(full, kBlockBytes);
                             for (int h = 0; h < 2; h++)
-                                tma_load(dst + h * (kBlockBytes / 2), map, 64 * h, p.head, p.s.k0 + j * kTok, full);
+                                tma_load(dst + h * (kBlockBytes / 2), map, 64 * h, head, key0 + j * kTok, full);
                         }
+                    if (!ok) break;
+                    follow.done(true);
                 }
                 // before the CTA exits, the copies that it issued have landed
                 for (uint32_t s = 0; s < kStages; s++) {
@@ -697,125 +823,176 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
             }
         } else if (warp == kMmaWarp) {
-            // The whole warp walks and waits, so that addresses stay uniform, and one lane issues.  A wait that gives up is
-            // noted and the walk goes on: every later wait then gives up soon, and nothing is read out of bounds.
-            uint32_t n = 0;             // ring uses of the pieces before
+            // The whole warp walks and waits, so that addresses stay uniform, and one lane issues.  The pipe takes one product
+            // ahead of the one that it works on, so what stands between two products must be short (stages are constants:
+            // the body comes twice, for the two halves of the ring), and a wait behind the last of eight would leave the pipe
+            // idle for the 100 to 200 cycles that even a completed barrier costs here: the next eight's barriers are tested
+            // before the last three.  A wait that gives up is noted and the piece goes on: every later wait then gives up
+            // soon, and nothing is read out of bounds.
+            constexpr int kAhead = 5;
+            constexpr uint32_t kStep = kBlockBytes >> 4;        // a stage, or a tile of Q, in descriptor units
+            uint32_t m = 0;             // blocks so far: block m's keys are use 2 m of the ring, its values use 2 m + 1
             uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
             const uint32_t q_low = desc_low(sQ, 16), key_low = desc_low(sKV, 16), value_low = desc_low(sKV, kBlockBytes / 2);
             auto wait = [&](unsigned long long &bar, uint32_t k) { wait_or_fail(B_(bar), k & 1, fail); };
+            auto test = [&](unsigned long long &bar, uint32_t k) { return phase_done(B_(bar), k & 1); };
             auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-            // scores of tile x against the key block in stage st
-            auto score = [&](int x, uint32_t st, bool final) {
-                const uint32_t d = tmem + 128 * x, q = q_low + x * (kBlockBytes >> 4), b = key_low + st * (kBlockBytes >> 4);
+            // scores of tile x against the key block in stage st; `ahead` is called before the last products
+            auto score = [&](auto X, auto St, bool final, auto &&ahead) {
+                constexpr int x = decltype(X)::value, st = decltype(St)::value;
+                auto product = [&](int k) {
+                    const uint32_t off = ((k >> 2) * (kBlockBytes / 2) + (k & 3) * 32) >> 4;
+                    if (k == 0) mma_ss<false>(128 * x, q_low + x * kStep + off, key_low + st * kStep + off, kIdescS);
+                    else mma_ss<true>(128 * x, q_low + x * kStep + off, key_low + st * kStep + off, kIdescS);
+                };
                 fence_after();
-                if (lane == 0) {
-                    mma_ss<false>(d, q, b, kIdescS);
+                if (elect_one()) {
 #pragma unroll
-                    for (int k = 1; k < 8; k++) {
-                        const uint32_t off = ((k >> 2) * (kBlockBytes / 2) + (k & 3) * 32) >> 4;
-                        mma_ss<true>(d, q + off, b + off, kIdescS);
-                    }
+                    for (int k = 0; k < kAhead; k++) product(k);
+                }
+                ahead();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kAhead; k < 8; k++) product(k);
                     commit(B_(bars.s_full[x]));
                     if (final) commit(B_(bars.q_empty[x]));
                 }
             };
             // weights of tile x times the value block in stage st
-            auto output = [&](int x, uint32_t st, bool first, bool final) {
-                const uint32_t d = tmem + 256 + 128 * x, w = tmem + 128 * x, b = value_low + st * (kBlockBytes >> 4);
+            auto output = [&](auto X, auto St, bool first, bool final, auto &&ahead) {
+                constexpr int x = decltype(X)::value, st = decltype(St)::value;
+                auto product = [&](int part, int k, uint32_t add) {
+                    mma_ts(256 + 128 * x, 128 * x + 64 * part + 8 * k, value_low + st * kStep + k * (2048 >> 4), kIdescO, add);
+                };
                 fence_after();
-                if (lane == 0) {
-                    mma_ts(d, w, b, kIdescO, !first);
-#pragma unroll
-                    for (int k = 1; k < 8; k++) mma_ts(d, w + 8 * k, b + k * (2048 >> 4), kIdescO, 1);
+                if (elect_one()) {
+                    product(0, 0, !first);
                     if (kWide) {
 #pragma unroll
-                        for (int k = 0; k < 8; k++) mma_ts(d, w + 64 + 8 * k, b + k * (2048 >> 4), kIdescO, 1);
+                        for (int k = 0; k < 8; k++) product(1, k, 1);
                     }
+#pragma unroll
+                    for (int k = 1; k < kAhead; k++) product(0, k, 1);
+                }
+                ahead();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kAhead; k < 8; k++) product(0, k, 1);
                     if (final) commit(B_(bars.o_full[x]));
                 }
             };
-            auto release = [&](uint32_t use) {
-                if (lane == 0) commit(B_(bars.empty[use % kStages]));
+            auto release = [&](int st) {
+                if (elect_one()) commit(B_(bars.empty[st]));
             };
-            while (walk.next(a, sp, p)) {
-                const int j0 = same(p.j0), j1 = same(p.j1), edge = same(p.edge), last[2] = {same(p.last(0)), same(p.last(1))};
-                if (j1 > j0) {
-                    wait(bars.full[n % kStages], n / kStages);
-#pragma unroll
-                    for (int x = 0; x < 2; x++)
-                        if (last[x] > j0) {
-                            wait(bars.q_full[x], nq[x]++);
-                            score(x, n % kStages, j0 + 1 == last[x]);
-                        }
-                    release(n);
+            using Zero = std::integral_constant<int, 0>;
+            using One = std::integral_constant<int, 1>;
+            uint32_t ready_v = 0, ready_a = 0;
+            int j0 = 0, j1 = 0, edge = 0, last_a = 0, last_b = 0;
+            // a piece's first scores; half: which half of the ring (stages 2 half, 2 half + 1) block m has
+            auto begin = [&](auto Half) {
+                constexpr int half = decltype(Half)::value;
+                using K = std::integral_constant<int, 2 * half>;
+                wait(bars.full[K::value], m >> 1);
+                if (last_a > j0) {
+                    wait(bars.q_full[0], nq[0]++);
+                    score(Zero{}, K{}, j0 + 1 == last_a, [] {});
                 }
-                for (int j = j0; j < j1; j++, n += 2) {
-                    // uses of the ring: n keys of j, n + 1 values of j, n + 2 keys of j + 1
-                    const uint32_t vst = (n + 1) % kStages, kst = (n + 2) % kStages;
-                    bool next_keys = j + 1 == j1;
-                    wait(bars.full[vst], (n + 1) / kStages);
-                    if (j >= edge) wait(bars.v_ok[vst >> 1], (n + 1) / kStages);
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        if (j < last[x]) {
-                            wait(bars.p_full[x], np[x]++);
-                            output(x, vst, j == j0, j + 1 == last[x]);
-                        }
-                        if (x == 1) release(n + 1);
-                        if (j + 1 < last[x]) {
-                            if (!next_keys) wait(bars.full[kst], (n + 2) / kStages);
-                            next_keys = true;
-                            score(x, kst, j + 2 == last[x]);
-                        }
+                if (last_b > j0) {
+                    wait(bars.q_full[1], nq[1]++);
+                    score(One{}, K{}, j0 + 1 == last_b, [] {});
+                }
+                release(K::value);
+            };
+            // block j: outputs, and the scores of j + 1; kSteady: both tiles go on, and no row is at its edge
+            auto block = [&](auto Half, auto Steady, int j) {
+                constexpr int half = decltype(Half)::value;
+                constexpr bool kSteady = decltype(Steady)::value != 0;
+                using V = std::integral_constant<int, 2 * half + 1>;
+                using K = std::integral_constant<int, 2 - 2 * half>;        // of block m + 1, and its values behind it
+                const uint32_t turn = m >> 1, turn_next = (m + 1) >> 1;
+                const bool more = kSteady || j + 1 < j1, now_a = kSteady || j < last_a, now_b = kSteady || j < last_b,
+                           next_a = kSteady || j + 1 < last_a, next_b = kSteady || j + 1 < last_b;
+                uint32_t ready_k = !more, ready_b = 0;
+                auto test_k = [&] {
+                    if (more) ready_k = test(bars.full[K::value], turn_next);
+                };
+                auto test_b = [&] {
+                    if (now_b) ready_b = test(bars.p_full[1], np[1]);
+                };
+                auto test_next = [&] {
+                    if (more) ready_v = test(bars.full[K::value + 1], turn_next);
+                    if (next_a) ready_a = test(bars.p_full[0], np[0]);
+                };
+                if (!ready_v) wait(bars.full[V::value], turn);
+                if (!kSteady && j >= edge) wait(bars.v_ok[half], turn);
+                ready_v = 0;
+                if (now_a) {
+                    if (!ready_a) wait(bars.p_full[0], np[0]);
+                    ready_a = 0;
+                    np[0]++;
+                    output(Zero{}, V{}, !kSteady && j == j0, !kSteady && j + 1 == last_a, test_k);
+                }
+                if (!ready_k) wait(bars.full[K::value], turn_next);
+                if (next_a) score(Zero{}, K{}, !kSteady && j + 2 == last_a, test_b);
+                if (now_b) {
+                    if (!ready_b) wait(bars.p_full[1], np[1]);
+                    np[1]++;
+                    output(One{}, V{}, !kSteady && j == j0, !kSteady && j + 1 == last_b, [] {});
+                }
+                release(V::value);
+                if (next_b) score(One{}, K{}, !kSteady && j + 2 == last_b, test_next);
+                if (more) release(K::value);
+                m++;
+            };
+            while (const Piece *p = follow.take()) {
+                j0 = same(p->j0), j1 = same(p->j1), edge = same(p->edge), last_a = same(p->last(0)), last_b = same(p->last(1));
+                __syncwarp();
+                follow.done(lane == 0);
+                ready_v = ready_a = 0;
+                if (j1 > j0) {
+                    if (m & 1) begin(One{});
+                    else begin(Zero{});
+                }
+                const int steady = min(min(last_a, last_b) - 2, edge);      // blocks j0 + 1 .. steady - 1
+                for (int j = j0; j < j1; j++) {
+                    if (j > j0 && j < steady) {
+                        if (m & 1) block(One{}, One{}, j);
+                        else block(Zero{}, One{}, j);
+                    } else {
+                        if (m & 1) block(One{}, Zero{}, j);
+                        else block(Zero{}, Zero{}, j);
                     }
-                    if (j + 1 < j1) release(n + 2);
                 }
             }
             // every product issued is complete before the CTA frees its tensor memory
-            if (lane == 0) {
-                commit(B_(bars.done));
-                wait_bounded(B_(bars.done), 0);
-            }
-            __syncwarp();
+            if (elect_one()) commit(B_(bars.done));
+            wait_bounded(B_(bars.done), 0);
         } else if (warp == kCheckWarp) {
-            uint32_t n = 0, nq[2] = {0, 0}, q_bytes = (uint32_t)a.tile_tokens * a.G * 256;
+            uint32_t n = 0, nq[2] = {0, 0};
+            const uint32_t q_bytes = (uint32_t)a.tile_tokens * a.G * 256;
             bool ok = true;
-            for (int k = 0; ok && walk.next(a, sp, p); k++) {
-                // marks of the item two before this one: taken back once that item is written
-                if (*(volatile int *)&s_dirty[k & 1]) {
-                    for (uint32_t i = 0; ok && !__all_sync(0xffffffffu, *(volatile int *)&s_written[lane & 7] >= k - 1); i++)
-                        if (i > kSpin || *fail) {
-                            *fail = 1;
-                            ok = false;
-                        }
-                    ok = __all_sync(0xffffffffu, ok);
-                    for (int d = lane; d < kD; d += 32) s_bad[k & 1][d] = INT_MAX;
-                    __syncwarp();
-                    if (lane == 0) s_dirty[k & 1] = 0;
-                    __threadfence_block();
-                    __syncwarp();
-                }
-                for (int x = 0; x < 2 && ok; x++)
-                    if (p.uses(x)) {
+            while (const Piece *p = follow.take()) {
+                const int j0 = p->j0, j1 = p->j1, edge = p->edge;
+#pragma unroll
+                for (int x = 0; x < 2; x++)
+                    if (ok && p->uses(x)) {
                         if (nq[x] && !wait_or_fail(B_(bars.q_empty[x]), (nq[x] - 1) & 1, fail)) {
                             ok = false;
-                            break;
-                        }
-                        if (lane == 0) {
+                        } else if (lane == 0) {
                             mbar_expect(B_(bars.q_full[x]), q_bytes);
                             for (int h = 0; h < 2; h++)
-                                tma_load(sQ + x * kBlockBytes + h * (kBlockBytes / 2), &maps.q, 64 * h, p.head * a.G,
-                                         p.s.q0 + p.tok(a, x), B_(bars.q_full[x]));
+                                tma_load(sQ + x * kBlockBytes + h * (kBlockBytes / 2), &maps.q, 64 * h, p->head * a.G,
+                                         p->row0 + x * a.tile_tokens, B_(bars.q_full[x]));
                         }
-                        nq[x]++;
+                        if (ok) nq[x]++;
                     }
-                for (int j = p.j0; j < p.j1 && ok; j++) {
-                    const uint32_t use = n + 2 * (j - p.j0) + 1, st = use % kStages;
+                for (int j = j0; j < j1 && ok; j++) {
+                    const uint32_t use = n + 2 * (j - j0) + 1, st = use % kStages;
                     if (!wait_or_fail(B_(bars.full[st]), use / kStages & 1, fail)) {
                         ok = false;
                         break;
                     }
-                    if (j >= p.edge) {
+                    if (j >= edge) {
                         uint8_t *v = base + (2 + st) * kBlockBytes;
                         // 0 * x is 0 but for a NaN or an infinity
                         const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
@@ -832,6 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 #pragma unroll
                         for (int i = 0; i < 4; i++) any |= bf16x2_bits(acc[i]) & 0x7fff7fffu;
                         if (__any_sync(0xffffffffu, any != 0)) {
+                            const int at = follow.place();
 #pragma unroll 1
                             for (int i = lane; i < kBlockBytes / 2; i += 32) {
                                 uint16_t *e = reinterpret_cast<uint16_t *>(v) + i;
@@ -839,10 +1017,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                                 // element i of the swizzled tile: half, row (token), 16-byte chunk
                                 const int half = i >> 13, row = i >> 6 & 127, chunk = (i >> 3 & 7) ^ (row & 7);
                                 *e = 0;
-                                atomicMin(&s_bad[k & 1][half * 64 + chunk * 8 + (i & 7)], j * kTok + row);
+                                atomicMin(&queue.bad[at][half * 64 + chunk * 8 + (i & 7)], j * kTok + row);
                             }
                             __syncwarp();
-                            if (lane == 0) s_dirty[k & 1] = 1;
+                            if (lane == 0) queue.dirty[at] = 1;
                             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                             __threadfence_block();
                             __syncwarp();
@@ -854,12 +1032,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                         mbar_arrive(B_(bars.empty[st]));
                     }
                 }
-                n += 2 * (p.j1 - p.j0);
+                if (!ok) break;
+                n += 2 * (j1 - j0);
+                __syncwarp();
+                follow.done(lane == 0);
             }
             // before the CTA exits, the copies that it issued have landed
             if (lane == 0)
                 for (int x = 0; x < 2; x++)
                     if (nq[x]) wait_bounded(B_(bars.q_full[x]), (nq[x] - 1) & 1);
+        } else {
+            // announces the pieces, a few ahead: finding one takes more time than a block of keys
+            Walk walk(sp);
+            for (uint32_t k = 0;; k++) {
+                const int at = k % kPieces;
+                const Piece p = walk.next(a, sp);
+                if (k >= kPieces) {
+                    if (!wait_or_fail(B_(bars.free[at]), (k / kPieces - 1) & 1, fail)) break;
+                    if (queue.dirty[at]) {
+                        for (int d = lane; d < kD; d += 32) queue.bad[at][d] = INT_MAX;
+                        __syncwarp();
+                        if (lane == 0) queue.dirty[at] = 0;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    queue.piece[at] = p;
+                    mbar_arrive(B_(bars.next[at]));
+                }
+                if (p.seq < 0) break;
+            }
         }
     }
 
@@ -869,10 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         for (int i = lane; i < sp.line_items; i += 32) {
             const int start = sp.cost[i];
             if (start < lo || start >= hi) continue;
-            const int stop = i + 1 < sp.line_items ? sp.cost[i + 1] : sp.quota[grid];
+            const int stop = i + 1 < sp.line_items ? sp.cost[i + 1] : sp.line_blocks;
             PromptMeta m{-1, 0, 0, 0, 0, {0, 0, 0}};
             if (stop > hi) {
-                const Piece q = item_at(a, sp, sp.rounds * grid + i);
+                const Piece q = item_at(a, sp, sp.rounds * grid + i, nullptr);
                 int c = blockIdx.x;
                 while (sp.quota[c + 1] < stop) c++;
                 m = PromptMeta{q.seq, q.head, q.tile, (int)blockIdx.x, c, {0, 0, 0}};
