@@ -254,28 +254,50 @@ struct Split {
     int pre[kPMaxBatch + 1];    // items of the sequences before b
     int scan[kThreads / 32];
     int cost[2 * kPMaxCtas];    // prefix of the blocks of the items of the line
-    unsigned long long load[kPMaxCtas];     // blocks that the CTAs do in whole items
+    int load[kPMaxCtas];        // blocks that the CTAs do in whole items
     int quota[kPMaxCtas + 1];   // where the CTAs' shares of the line begin
     int rounds, line_items, line_blocks;
 };
 
-// Item `i` of the call; known: the sequences, where they are at hand.
-__device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, int i, const Seq *known)
+// The last b with pre[b] <= i: item i's sequence.
+__device__ __forceinline__ int sequence_of(const PromptArgs &a, const Split &sp, int i)
 {
-    int lo = 0, hi = a.batch;           // the last b with pre[b] <= i
+    int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sp.pre[mid] <= i) lo = mid;
         else hi = mid;
     }
+    return lo;
+}
+
+__device__ __forceinline__ int tiles_of(const PromptArgs &a, const Seq &s)
+{
+    return (uint32_t)(s.n + 2 * a.tile_tokens - 1) / (uint32_t)(2 * a.tile_tokens);
+}
+
+// Key blocks that the tokens up to `token` (inclusive) of a sequence see.
+__device__ __forceinline__ int blocks_seen(const PromptArgs &a, const Seq &s, int token)
+{
+    return (min(max(s.m - s.n - a.lag + token + 1, 0), s.m) + kTok - 1) / kTok;
+}
+
+// Work of an item in blocks; one that sees no key still has its output to write.
+__device__ __forceinline__ int item_cost(const PromptArgs &a, const Seq &s, int tile)
+{
+    return max(blocks_seen(a, s, min((tile + 1) * 2 * a.tile_tokens, s.n) - 1), 1);
+}
+
+// Item `i` of the call.
+__device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, int i)
+{
     Piece p;
-    p.seq = lo;
-    const Seq s = known ? known[lo] : sequence(a, lo, false);
-    const uint32_t in = i - sp.pre[lo], tiles = (uint32_t)(sp.pre[lo + 1] - sp.pre[lo]) / (uint32_t)a.kv_heads;
-    const uint32_t down = in / (uint32_t)a.kv_heads;
+    p.seq = sequence_of(a, sp, i);
+    const Seq s = sequence(a, p.seq, false);
+    const uint32_t in = i - sp.pre[p.seq], down = in / (uint32_t)a.kv_heads;
     const int T = a.tile_tokens;
     p.head = in - down * a.kv_heads;
-    p.tile = tiles - 1 - down;
+    p.tile = tiles_of(a, s) - 1 - down;
     const int tok0 = 2 * p.tile * T, ta = min(T, s.n - tok0), tb = max(min(T, s.n - tok0 - T), 0);  // the item exists: ta >= 1
     p.row0 = s.q0 + tok0;
     p.key0 = s.k0;
@@ -283,17 +305,14 @@ __device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, i
     p.first_seen = s.m - s.n - a.lag + tok0 + 1;
     p.rows_a = ta * a.G;
     p.rows_b = tb * a.G;
-    p.nblk_a = (p.seen(ta - 1) + kTok - 1) / kTok;
-    p.nblk_b = tb > 0 ? (p.seen(T + tb - 1) + kTok - 1) / kTok : 0;
+    p.nblk_a = blocks_seen(a, s, tok0 + ta - 1);
+    p.nblk_b = tb > 0 ? blocks_seen(a, s, tok0 + T + tb - 1) : 0;
     p.edge = p.seen(0) / kTok;
     p.j0 = 0;
     p.j1 = max(p.nblk_a, p.nblk_b);
     p.slot = -1;
     return p;
 }
-
-// Work of an item in blocks; one that sees no key still has its output to write.
-__device__ __forceinline__ int item_cost(const Piece &p) { return max(p.j1, 1); }
 
 __device__ __forceinline__ int block_scan(Split &sp, int v, int *total)
 {
@@ -317,8 +336,7 @@ __device__ __forceinline__ int block_scan(Split &sp, int v, int *total)
     return before + x - v;
 }
 
-// The whole split, by all threads of the CTA.  known: room for the sequences,
-// which all items are looked up in.
+// The whole split, by all threads of the CTA.  known: room for the sequences.
 __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *known)
 {
     const int tid = threadIdx.x, grid = gridDim.x;
@@ -329,7 +347,7 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
         if (b < a.batch) {
             const Seq s = sequence(a, b, blockIdx.x == 0);
             known[b] = s;
-            own = (s.n + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens) * a.kv_heads;
+            own = tiles_of(a, s) * a.kv_heads;
         }
         const int at = block_scan(sp, own, &all);
         if (b < a.batch) sp.pre[b] = items + at;
@@ -339,17 +357,40 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
     if (tid < kPMaxCtas) sp.load[tid] = 0;
     __syncthreads();
     const int rounds = max(items / grid - 1, 0), first = rounds * grid, line = items - first;
-    // blocks of the whole items
-    for (int i = tid; i < first; i += kThreads) {
-        const int r = i / grid, at = i - r * grid;
-        atomicAdd(&sp.load[r & 1 ? grid - 1 - at : at], (unsigned long long)item_cost(item_at(a, sp, i, known)));
+    // Blocks of the whole items: a thread goes through consecutive items, one search for all of them.
+    const int per = (first + kThreads - 1) / kThreads, stop = min(first, (tid + 1) * per);
+    if (tid * per < stop) {
+        int i = tid * per, b = sequence_of(a, sp, i), r = i / grid, at = i - r * grid;
+        Seq s = known[b];
+        int in = i - sp.pre[b], down = in / a.kv_heads, head = in - down * a.kv_heads, tile = tiles_of(a, s) - 1 - down;
+        int cost = item_cost(a, s, tile);
+#pragma unroll 1
+        for (; i < stop; i++) {
+            atomicAdd(&sp.load[r & 1 ? grid - 1 - at : at], cost);
+            if (++at == grid) {
+                at = 0;
+                r++;
+            }
+            if (++head < a.kv_heads || i + 1 == stop) continue;
+            head = 0;
+            if (--tile < 0) {
+                do s = known[++b];
+                while (s.n == 0);       // there is another item, so another sequence with queries
+                tile = tiles_of(a, s) - 1;
+            }
+            cost = item_cost(a, s, tile);
+        }
     }
     // blocks of the line
     int total = 0;
     for (int i0 = 0; i0 < line; i0 += kThreads) {
         const int i = i0 + tid;
-        int all;
-        const int own = i < line ? item_cost(item_at(a, sp, first + i, known)) : 0;
+        int all, own = 0;
+        if (i < line) {
+            const int b = sequence_of(a, sp, first + i);
+            const Seq s = known[b];
+            own = item_cost(a, s, tiles_of(a, s) - 1 - (int)((uint32_t)(first + i - sp.pre[b]) / (uint32_t)a.kv_heads));
+        }
         const int at = block_scan(sp, own, &all);
         if (i < line) sp.cost[i] = total + at;
         total += all;
@@ -357,23 +398,23 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
     __syncthreads();
     if (tid < 32) {
         // the level at which the CTAs' shares, level - load, add up to the line
-        long long top = 0, sum = 0;
+        int top = 0;
+        long long sum = 0;
         for (int c = tid; c < grid; c += 32) {
-            top = max(top, (long long)sp.load[c]);
+            top = max(top, sp.load[c]);
             sum += sp.load[c];
         }
+        top = __reduce_max_sync(0xffffffffu, top);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        long long lo = (sum + total + grid - 1) / grid, hi = lo;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        int lo = (int)((sum + total + grid - 1) / grid), hi = lo;
         if (lo < top) {                 // some CTAs are past it already
             hi = top + (total + grid - 1) / grid;
+#pragma unroll 1
             while (lo < hi) {
-                const long long mid = lo + (hi - lo) / 2;
+                const int mid = lo + (hi - lo) / 2;
                 sum = 0;
-                for (int c = tid; c < grid; c += 32) sum += max(mid - (long long)sp.load[c], 0ll);
+                for (int c = tid; c < grid; c += 32) sum += max(mid - sp.load[c], 0);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (sum >= total) hi = mid;
@@ -383,7 +424,7 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
         long long at = 0;
         for (int c0 = 0; c0 < grid; c0 += 32) {
             const int c = c0 + tid;
-            const long long own = c < grid ? max(hi - (long long)sp.load[c], 0ll) : 0;
+            const long long own = c < grid ? max(hi - sp.load[c], 0) : 0;
             long long x = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -426,11 +467,11 @@ struct Walk {
         Piece p;
         p.seq = -1;
         if (round < sp.rounds) {
-            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x), nullptr);
+            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x));
             round++;
         } else if (at < end) {
-            p = item_at(a, sp, sp.rounds * grid + item, nullptr);
-            const int start = sp.cost[item], stop = start + item_cost(p);
+            p = item_at(a, sp, sp.rounds * grid + item);
+            const int start = sp.cost[item], stop = start + max(p.j1, 1);
             const bool begins = start >= at, ends = stop <= end;
             if (!begins || !ends) {
                 p.slot = begins ? 1 : 0;
@@ -739,47 +780,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const uint32_t stage = smem_u32(stage_raw[warp]);
             const bool fp32 = part || kWide;
             float *out32 = part ? a.part_o : reinterpret_cast<float *>(a.out);
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                float o[32];
+            const int *bad = queue.bad[follow.place()];
+            // (rolled up: once per piece, its instructions come from far away)
+#pragma unroll 1
+            for (int c = 0; c < (fp32 ? 8 : 4); c++) {
+                uint32_t w[16];
                 __syncwarp();
-                if (some) {
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    o[i] = scale != 0.f ? o[i] * scale : 0.f;
-                    if (dirty && queue.bad[follow.place()][32 * c + i] < lim) o[i] = CUDART_NAN_F;
-                }
                 if (fp32) {
+                    float o[16];
+                    tmem_ld16(tO + 16 * c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        uint32_t w[16];
+                    for (int i = 0; i < 16; i++) w[i] = __float_as_uint(scale != 0.f ? o[i] * scale : 0.f);
+                    if (dirty) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++) w[i] = __float_as_uint(o[16 * half + i]);
-                        put_row(stage, lane, w);
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
-                            if (to[i] >= 0) *reinterpret_cast<uint4 *>(out32 + to[i] + 32 * c + 16 * half + 4 * (lane & 3)) = v;
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < 16; i++)
+                            if (bad[16 * c + i] < lim) w[i] = 0x7fffffffu;
                     }
                 } else {
-                    uint32_t w[16];
+                    float o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = scale != 0.f ? o[i] * scale : 0.f;
+                    if (dirty) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            if (bad[32 * c + i] < lim) o[i] = CUDART_NAN_F;
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; i++) w[i] = bf16_pair(o[2 * i], o[2 * i + 1]);
-                    put_row(stage, lane, w);
-                    __syncwarp();
+                }
+                put_row(stage, lane, w);
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
-                        if (to[i] >= 0)
-                            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + to[i] + 32 * c + 8 * (lane & 3)) = v;
-                    }
-                    __syncwarp();
+                for (int i = 0; i < 4; i++) {
+                    const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
+                    if (to[i] < 0) continue;
+                    if (fp32) *reinterpret_cast<uint4 *>(out32 + to[i] + 16 * c + 4 * (lane & 3)) = v;
+                    else *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + to[i] + 32 * c + 8 * (lane & 3)) = v;
                 }
             }
             if (valid) {
@@ -1074,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const int stop = i + 1 < sp.line_items ? sp.cost[i + 1] : sp.line_blocks;
             PromptMeta m{-1, 0, 0, 0, 0, {0, 0, 0}};
             if (stop > hi) {
-                const Piece q = item_at(a, sp, sp.rounds * grid + i, nullptr);
+                const Piece q = item_at(a, sp, sp.rounds * grid + i);
                 int c = blockIdx.x;
                 while (sp.quota[c + 1] < stop) c++;
                 m = PromptMeta{q.seq, q.head, q.tile, (int)blockIdx.x, c, {0, 0, 0}};
@@ -1193,7 +1232,7 @@ cudaError_t launch_prompt_attention(const PromptArgs &a, const PromptMaps &maps,
     const int64_t line = most < 2 * sm_count ? most : 2 * sm_count;
     const auto kernel = a.wide ? prompt_attention_kernel<true> : prompt_attention_kernel<false>;
     const cudaError_t e = launch_maybe_pdl(kernel, dim3(sm_count), dim3(kThreads), kDynBytes, s, true, a, maps);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.n_kv <= kTok) return e;       // items of one block are not cut
     const auto merge = a.wide ? prompt_merge_kernel<true> : prompt_merge_kernel<false>;
     return launch_maybe_pdl(merge, dim3((unsigned)line, kPRows / kMergeRows), dim3(kMergeWarps * 32), 0, s, true, a);
 }
