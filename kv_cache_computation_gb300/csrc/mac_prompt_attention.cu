@@ -57,7 +57,6 @@ constexpr int kBlockBytes = 2 * kTok * 128;         // two column halves of 128 
 constexpr int kStages = 4;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;       // warp 11 announces the pieces
 constexpr int kPieces = 4;                          // pieces announced ahead
-constexpr int kStageBytes = 32 * 64;                // a warp's rows on their way out, 64 bytes of each
 constexpr int kThreads = 12 * 32;                   // three warpgroups; warp 11 has no role
 // registers: 168 per thread at launch (three warpgroups: 504), then 208 for the
 // softmax's two and 88 for the others'
@@ -485,27 +484,12 @@ struct Walk {
     }
 };
 
-// A warp's 32 rows of 64 bytes in shared memory, the 16-byte quarter q of row r
-// at q ^ (r / 2 % 4): row by row (a lane's own) and, eight rows at a time, quarter
-// by quarter without bank conflicts.
-__device__ __forceinline__ void put_row(uint32_t stage, int row, const uint32_t (&w)[16])
+// 32 bytes of a row.
+__device__ __forceinline__ void store32(void *to, const uint32_t *w)
 {
-#pragma unroll
-    for (int q = 0; q < 4; q++)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n"
-                     :: "r"(stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4)), "r"(w[4 * q]), "r"(w[4 * q + 1]), "r"(w[4 * q + 2]),
-                        "r"(w[4 * q + 3])
-                     : "memory");
-}
-
-__device__ __forceinline__ uint4 get_quarter(uint32_t stage, int row, int q)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(stage + row * 64 + ((q ^ (row >> 1 & 3)) << 4))
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n"
+                 :: "l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-    return v;
 }
 
 template <int N>
@@ -676,7 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     __shared__ Split sp;
     __shared__ __align__(8) Bars bars;
     __shared__ Queue queue;
-    __shared__ __align__(16) uint8_t stage_raw[8][kStageBytes];     // a softmax warp's rows on their way out
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -757,75 +740,67 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             }
             if (!ok) break;
 
-            // The rows' outputs, or their part of them: scaled by the row's thread, then through shared memory, 64 bytes of
-            // each of the warp's rows at a time, so that four lanes write 64 bytes of a row.
+            // the row's output, or its part of one
             const bool some = last > j0;
             if (some) {
                 if (!wait_or_fail(B_(bars.o_full[x]), no & 1, fail)) break;
                 no++;
                 fence_after();
             }
-            const int slot = p->slot, rows = p->rows(x);
+            const int slot = p->slot;
             const bool part = slot >= 0, dirty = some && *(volatile int *)&queue.dirty[follow.place()];
             const float scale = !some || sum == 0.f ? 0.f : part ? 1.f : 1.f / sum;
-            // where the rows 8 i + lane / 4 of the warp's 32 go, in elements: -1 where they are not valid
-            const int64_t out_row = (int64_t)(p->row0 + x * a.tile_tokens) * a.heads + p->head * a.G;
-            const int64_t part_row = ((int64_t)blockIdx.x * 2 + slot) * kPRows + 128 * x;
-            int64_t to[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = (warp & 3) * 32 + 8 * i + (lane >> 2), t = r / a.G;
-                to[i] = r >= rows ? -1 : (part ? part_row + r : out_row + (int64_t)t * a.heads + (r - t * a.G)) * kD;
-            }
-            const uint32_t stage = smem_u32(stage_raw[warp]);
+            const int row_tok = row / a.G;
+            const int64_t out_row = (int64_t)(p->row0 + x * a.tile_tokens + row_tok) * a.heads + p->head * a.G + row - row_tok * a.G;
+            const int64_t part_row = ((int64_t)blockIdx.x * 2 + slot) * kPRows + 128 * x + row;
             const bool fp32 = part || kWide;
-            float *out32 = part ? a.part_o : reinterpret_cast<float *>(a.out);
+            char *to = fp32 ? reinterpret_cast<char *>(part ? a.part_o + part_row * kD : reinterpret_cast<float *>(a.out) + out_row * kD)
+                            : reinterpret_cast<char *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row * kD);
             const int *bad = queue.bad[follow.place()];
+            const bool every = __all_sync(0xffffffffu, scale != 0.f);       // else some rows' O was never written, or is to be 0
             // (rolled up: once per piece, its instructions come from far away)
 #pragma unroll 1
             for (int c = 0; c < (fp32 ? 8 : 4); c++) {
                 uint32_t w[16];
-                __syncwarp();
                 if (fp32) {
                     float o[16];
                     tmem_ld16(tO + 16 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i++) w[i] = __float_as_uint(scale != 0.f ? o[i] * scale : 0.f);
-                    if (dirty) {
+                    for (int i = 0; i < 16; i++) o[i] *= scale;
+                    if (!every || dirty) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            if (bad[16 * c + i] < lim) w[i] = 0x7fffffffu;
+                        for (int i = 0; i < 16; i++) {
+                            if (scale == 0.f) o[i] = 0.f;
+                            if (dirty && bad[16 * c + i] < lim) o[i] = CUDART_NAN_F;
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; i++) w[i] = __float_as_uint(o[i]);
                 } else {
                     float o[32];
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i++) o[i] = scale != 0.f ? o[i] * scale : 0.f;
-                    if (dirty) {
+                    for (int i = 0; i < 32; i++) o[i] *= scale;
+                    if (!every || dirty) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            if (bad[32 * c + i] < lim) o[i] = CUDART_NAN_F;
+                        for (int i = 0; i < 32; i++) {
+                            if (scale == 0.f) o[i] = 0.f;
+                            if (dirty && bad[32 * c + i] < lim) o[i] = CUDART_NAN_F;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i++) w[i] = bf16_pair(o[2 * i], o[2 * i + 1]);
                 }
-                put_row(stage, lane, w);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint4 v = get_quarter(stage, 8 * i + (lane >> 2), lane & 3);
-                    if (to[i] < 0) continue;
-                    if (fp32) *reinterpret_cast<uint4 *>(out32 + to[i] + 16 * c + 4 * (lane & 3)) = v;
-                    else *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + to[i] + 32 * c + 8 * (lane & 3)) = v;
+                if (valid) {
+                    store32(to + 64 * c, w);
+                    store32(to + 64 * c + 32, w + 8);
                 }
             }
             if (valid) {
-                const int t = row / a.G;
-                if (part) a.part_ml[part_row + row] = make_float2(ref, sum);
-                else if (a.lse)
-                    a.lse[out_row + (int64_t)t * a.heads + (row - t * a.G)] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
+                if (part) a.part_ml[part_row] = make_float2(ref, sum);
+                else if (a.lse) a.lse[out_row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
             }
             fence_before();
             __syncwarp();
