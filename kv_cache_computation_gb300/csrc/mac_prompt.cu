@@ -40,7 +40,7 @@ Sizes scratch_sizes()
     Sizes z;
     z.err = 0;
     z.meta = 256;
-    z.part_ml = z.meta + align_up(2 * kPMaxCtas * sizeof(PromptMeta));
+    z.part_ml = z.meta + align_up(kPMaxCtas * sizeof(PromptMeta));
     z.part_o = z.part_ml + align_up((size_t)kPMaxCtas * 2 * kPRows * sizeof(float2));
     z.scratch = z.part_o + (size_t)kPMaxCtas * 2 * kPRows * kD * sizeof(float);
     return z;

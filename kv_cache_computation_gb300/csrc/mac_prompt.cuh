@@ -13,8 +13,8 @@ constexpr int kPRows = 256;             // query rows of an item: two tiles of 1
 // bits of the device error word
 enum : uint32_t { kPErrStarts = 1u, kPErrTimeout = 2u };
 
-// An item that several CTAs worked on: CTA first holds its part behind its own
-// slot 1, the CTAs up to last behind their slots 0.  seq < 0: none.
+// An item that begins in CTA first's share of the line and ends in last's: the
+// first holds its part in its slot 1, the others in their slots 0.  seq < 0: none.
 struct PromptMeta {
     int seq, head, tile, first, last, pad[3];
 };
@@ -30,7 +30,7 @@ struct PromptArgs {
     float scale_log2;                       // score scale x log2(e)
     float *part_o;                          // [CTA][2][kPRows][128] unnormalised partial outputs
     float2 *part_ml;                        // [CTA][2][kPRows] reference (log2) and sum
-    PromptMeta *meta;                       // [2 CTAs]
+    PromptMeta *meta;                       // [CTA]
     uint32_t *err;
 };
 

@@ -396,43 +396,46 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
     }
     __syncthreads();
     if (tid < 32) {
-        // the level at which the CTAs' shares, level - load, add up to the line
-        int top = 0;
-        long long sum = 0;
-        for (int c = tid; c < grid; c += 32) {
-            top = max(top, sp.load[c]);
-            sum += sp.load[c];
+        // The level at which the CTAs' shares, level - load, add up to the line: the mean over all, or, where some CTAs are
+        // past that already, over the others, until none is left out any more.  A lane has kPer consecutive CTAs.
+        constexpr int kPer = kPMaxCtas / 32;
+        const int per = (grid + 31) / 32;
+        int load[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; i++) load[i] = i < per && tid * per + i < grid ? sp.load[tid * per + i] : INT_MAX;
+        int level = INT_MAX, in = 0;
+        for (;;) {
+            int n = 0;
+            long long sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; i++)
+                if (load[i] < level) {
+                    n++;
+                    sum += load[i];
+                }
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (n == in || n == 0) break;
+            in = n;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            level = (int)((sum + total + n - 1) / n);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        int share = 0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        int lo = (int)((sum + total + grid - 1) / grid), hi = lo;
-        if (lo < top) {                 // some CTAs are past it already
-            hi = top + (total + grid - 1) / grid;
-#pragma unroll 1
-            while (lo < hi) {
-                const int mid = lo + (hi - lo) / 2;
-                sum = 0;
-                for (int c = tid; c < grid; c += 32) sum += max(mid - sp.load[c], 0);
+        for (int i = 0; i < kPer; i++) share += max(level - load[i], 0);
+        int at = share;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (sum >= total) hi = mid;
-                else lo = mid + 1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (tid >= o) at += y;
+        }
+        at -= share;
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (i < per && tid * per + i < grid) {
+                sp.quota[tid * per + i] = min(at, total);
+                at += max(level - load[i], 0);
             }
-        }
-        long long at = 0;
-        for (int c0 = 0; c0 < grid; c0 += 32) {
-            const int c = c0 + tid;
-            const long long own = c < grid ? max(hi - sp.load[c], 0) : 0;
-            long long x = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (tid >= o) x += y;
-            }
-            if (c < grid) sp.quota[c] = (int)min(at + x - own, (long long)total);
-            at = min(at + __shfl_sync(0xffffffffu, x, 31), (long long)total);
-        }
         if (tid == 0) {
             sp.quota[grid] = total;
             sp.rounds = rounds;
@@ -568,7 +571,7 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float sc
 #pragma unroll
     for (int c = 0; c < 4; c++) tmem_ld32(tS + 32 * c, s + 32 * c);
     tmem_wait_ld();
-    if (edge) {
+    if (edge && __any_sync(0xffffffffu, live < kTok)) {
 #pragma unroll
         for (int c = 0; c < 4; c++) hide(s + 32 * c, live - 32 * c);
     }
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             mbar_init(B_(bars.q_full[x]), 1);
             mbar_init(B_(bars.q_empty[x]), 1);
             mbar_init(B_(bars.s_full[x]), 1);
-            mbar_init(B_(bars.p_full[x]), 128);
+            mbar_init(B_(bars.p_full[x]), 4);                  // one arrival per warp
             mbar_init(B_(bars.o_full[x]), 1);
             mbar_init(B_(bars.v_ok[x]), 1);
         }
@@ -736,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 softmax_block<kWide>(tS, tO, sc, live, j >= edge, j > j0, ref, sum);
                 tmem_wait_st();
                 fence_before();
-                mbar_arrive(B_(bars.p_full[x]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B_(bars.p_full[x]));
             }
             if (!ok) break;
 
@@ -841,9 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             // ahead of the one that it works on, so what stands between two products must be short (stages are constants:
             // the body comes twice, for the two halves of the ring), and a wait behind the last of eight would leave the pipe
             // idle for the 100 to 200 cycles that even a completed barrier costs here: the next eight's barriers are tested
-            // before the last three.  A wait that gives up is noted and the piece goes on: every later wait then gives up
+            // before the last.  A wait that gives up is noted and the piece goes on: every later wait then gives up
             // soon, and nothing is read out of bounds.
-            constexpr int kAhead = 5;
+            constexpr int kAhead = 7;
             constexpr uint32_t kStep = kBlockBytes >> 4;        // a stage, or a tile of Q, in descriptor units
             uint32_t m = 0;             // blocks so far: block m's keys are use 2 m of the ring, its values use 2 m + 1
             uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
@@ -1079,24 +1083,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         }
     }
 
-    // the items of the line that begin in this CTA's share: which CTAs the second kernel finds them in
-    if (warp == kLoadWarp) {
+    // the item that begins in this CTA's share and runs on behind it, for the second kernel
+    if (tid == kLoadWarp * 32) {
         const int lo = sp.quota[blockIdx.x], hi = sp.quota[blockIdx.x + 1], grid = gridDim.x;
-        for (int i = lane; i < sp.line_items; i += 32) {
-            const int start = sp.cost[i];
-            if (start < lo || start >= hi) continue;
+        PromptMeta m{-1, 0, 0, 0, 0, {0, 0, 0}};
+        if (lo < hi) {
+            int i = 0, end = sp.line_items;         // the line's item that holds block hi - 1
+            while (end - i > 1) {
+                const int mid = (i + end) >> 1;
+                if (sp.cost[mid] < hi) i = mid;
+                else end = mid;
+            }
             const int stop = i + 1 < sp.line_items ? sp.cost[i + 1] : sp.line_blocks;
-            PromptMeta m{-1, 0, 0, 0, 0, {0, 0, 0}};
-            if (stop > hi) {
+            if (sp.cost[i] >= lo && stop > hi) {
                 const Piece q = item_at(a, sp, sp.rounds * grid + i);
                 int c = blockIdx.x;
                 while (sp.quota[c + 1] < stop) c++;
                 m = PromptMeta{q.seq, q.head, q.tile, (int)blockIdx.x, c, {0, 0, 0}};
             }
-            a.meta[i] = m;
         }
-        if (blockIdx.x == 0)
-            for (int i = sp.line_items + lane; i < 2 * grid; i += 32) a.meta[i] = PromptMeta{-1, 0, 0, 0, 0, {0, 0, 0}};
+        a.meta[blockIdx.x] = m;
     }
     __syncthreads();
     if (*fail && tid == 0) atomicOr(a.err, kPErrTimeout);
@@ -1108,9 +1114,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     }
 }
 
-// The items that several CTAs worked on: block (i, y) merges rows of item i of
-// the line, a warp per row, a lane with four elements.
-constexpr int kMergeWarps = 8, kMergeRows = 32;
+// The items that several CTAs worked on: block (c, y) merges rows of the one that
+// begins in CTA c's share, a warp two rows (one of tile A, one of B), a lane four
+// elements; the parts' loads are four ahead of one another.
+constexpr int kMergeWarps = 8, kMergeAhead = 4;
 
 template <bool kWide>
 __global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const __grid_constant__ PromptArgs a)
@@ -1118,34 +1125,52 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const __
     pdl_wait();
     const PromptMeta meta = a.meta[blockIdx.x];
     if (meta.seq < 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = a.tile_tokens;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), T = a.tile_tokens;
+    if (row >= T * a.G) return;
     const Seq s = sequence(a, meta.seq, false);
-    for (int r = blockIdx.y * kMergeRows + warp; r < (int)(blockIdx.y + 1) * kMergeRows; r += kMergeWarps) {
-        const int row = r & 127, tok = (2 * meta.tile + (r >> 7)) * T + row / a.G;
-        if (row >= T * a.G || tok >= s.n) continue;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float m = -CUDART_INF_F, l = 0.f;
-        for (int c = meta.first; c <= meta.last; c++) {
-            const int64_t at = ((int64_t)c * 2 + (c == meta.first)) * kPRows + r;
-            const float2 ml = a.part_ml[at];
-            const float4 x = reinterpret_cast<const float4 *>(a.part_o + at * kD)[lane];
-            if (ml.y == 0.f) continue;          // saw no key
-            const float top = fmaxf(m, ml.x), f = ex2_approx(m - top), g = ex2_approx(ml.x - top);
-            o = make_float4(o.x * f + x.x * g, o.y * f + x.y * g, o.z * f + x.z * g, o.w * f + x.w * g);
-            l = l * f + ml.y * g;
-            m = top;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int64_t at = (int64_t)(s.q0 + tok) * a.heads + meta.head * a.G + row % a.G;
-        if (kWide) {
-            reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at * kD)[lane] =
-                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        } else {
+    const int row_tok = row / a.G, row_head = row - row_tok * a.G, tok[2] = {2 * meta.tile * T + row_tok, (2 * meta.tile + 1) * T + row_tok};
+    float4 o[2] = {};
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    for (int c0 = meta.first; c0 <= meta.last; c0 += kMergeAhead) {
+        float2 ml[2][kMergeAhead];
+        float4 part[2][kMergeAhead];
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; i++) {
+                const int c = c0 + i;
+                ml[x][i] = make_float2(-CUDART_INF_F, 0.f);
+                part[x][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c <= meta.last && tok[x] < s.n) {
+                    const int64_t at = ((int64_t)c * 2 + (c == meta.first)) * kPRows + 128 * x + row;
+                    ml[x][i] = __ldcg(a.part_ml + at);
+                    part[x][i] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kD) + lane);
+                }
+            }
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < kMergeAhead; i++) {
+                if (ml[x][i].y == 0.f) continue;        // saw no key
+                const float top = fmaxf(m[x], ml[x][i].x), f = ex2_approx(m[x] - top), g = ex2_approx(ml[x][i].x - top);
+                const float4 v = part[x][i];
+                o[x] = make_float4(o[x].x * f + v.x * g, o[x].y * f + v.y * g, o[x].z * f + v.z * g, o[x].w * f + v.w * g);
+                l[x] = l[x] * f + ml[x][i].y * g;
+                m[x] = top;
+            }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+        if (tok[x] >= s.n) continue;
+        const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
+        const float4 v = l[x] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                     : make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
+        const int64_t at = (int64_t)(s.q0 + tok[x]) * a.heads + meta.head * a.G + row_head;
+        if (kWide) reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at * kD)[lane] = v;
+        else
             reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + at * kD)[lane] =
-                make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-        }
-        if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+                make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+        if (lane == 0 && a.lse) a.lse[at] = l[x] == 0.f ? -CUDART_INF_F : (m[x] + log2f(l[x])) * kLn2;
     }
 }
 
@@ -1202,14 +1227,11 @@ cudaError_t prompt_maps(const PromptArgs &a, const void *q, int64_t q_stride, co
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, const PromptMaps &maps, int sm_count, cudaStream_t s)
 {
-    // items at most: no sequence has more than a partly filled one per head besides
-    const int64_t most = ((int64_t)a.n_q / (2 * a.tile_tokens) + a.batch) * a.kv_heads;
-    const int64_t line = most < 2 * sm_count ? most : 2 * sm_count;
     const auto kernel = a.wide ? prompt_attention_kernel<true> : prompt_attention_kernel<false>;
     const cudaError_t e = launch_maybe_pdl(kernel, dim3(sm_count), dim3(kThreads), kDynBytes, s, true, a, maps);
     if (e != cudaSuccess || a.n_kv <= kTok) return e;       // items of one block are not cut
     const auto merge = a.wide ? prompt_merge_kernel<true> : prompt_merge_kernel<false>;
-    return launch_maybe_pdl(merge, dim3((unsigned)line, kPRows / kMergeRows), dim3(kMergeWarps * 32), 0, s, true, a);
+    return launch_maybe_pdl(merge, dim3(sm_count, 128 / kMergeWarps), dim3(kMergeWarps * 32), 0, s, true, a);
 }
 
 }  // namespace macgpu
