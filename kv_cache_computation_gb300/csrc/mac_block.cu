@@ -34,9 +34,17 @@ namespace macgpu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kScanTokens = 1024;       // most tokens of a call whose blocks look through all slots
+// Tokens of a call up to which every token's block looks through all slots.  Both
+// sides, us, 8 heads, scan against marks: 256 requests' tokens 3.6 against 8.8,
+// 1000 requests' 7.7 / 17; 1024 tokens in whole pages 13 / 10.
+constexpr int kScanTokens = 1024;
+constexpr int kMostBlocks = 1024;       // of a call through the marks, while a block takes fewer than 16 tokens
+constexpr int kFewTokens = 4;           // of a page: stored one after another
+// (token, head) pairs below which a gather's warp takes 4 tokens instead of 16
+// (us: 8 tokens 2.6 against 4.1, 1024 2.7 / 3.7, 8192 10.4 / 10.1, 32768 41 / 37).
+constexpr int kSmallGather = 16384;
 
-// A word of four bf16 pairs' magnitudes without NaN and infinities: the larger pattern of each half.
+// Two bf16 elements' magnitude patterns, 0 for a NaN or an infinity.
 __device__ __forceinline__ uint32_t finite_magnitudes(uint32_t two)
 {
     const uint32_t m = two & 0x7fff7fffu;
@@ -61,6 +69,17 @@ __device__ __forceinline__ uint32_t to_codes(uint2 u, float inv)
     unsigned short lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
+    return lo | (uint32_t)hi << 16;
+}
+
+// The same for finite elements.
+__device__ __forceinline__ uint32_t finite_codes(uint2 u, float inv)
+{
+    unsigned short lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
+        : "=h"(lo) : "f"(__uint_as_float(u.x & 0xffff0000u) * inv), "f"(__uint_as_float(u.x << 16) * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
+        : "=h"(hi) : "f"(__uint_as_float(u.y & 0xffff0000u) * inv), "f"(__uint_as_float(u.y << 16) * inv));
     return lo | (uint32_t)hi << 16;
 }
 
@@ -132,11 +151,69 @@ __global__ void __launch_bounds__(kThreads) block_mark_kernel(const __grid_const
     atomicMax(&m.token[slot % kPage], (uint32_t)t + 1u);    // of tokens that share a slot the last one counts
 }
 
-// One page of one KV head, keys or values, by a warp.  token[i]: which token
-// comes to offset i, or -1.
-__device__ __forceinline__ void store_page(const BlockMoveArgs &a, const int (&token)[kPage], uint8_t *page, bool is_v, int h)
+// One page of one KV head, keys or values, by a warp.  token[i], in shared memory:
+// which token comes to offset i, for the offsets of mask.  One token after
+// another: little code to fetch, which is what bounds a small call.
+__device__ __noinline__ void store_tokens(const BlockMoveArgs &a, const int *token, uint32_t mask, uint8_t *page, bool is_v, int h)
 {
     const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *src = (is_v ? a.v : a.k) + h * kD + 4 * lane;
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    auto load = [&](int i) { return *reinterpret_cast<const uint2 *>(src + token[i] * stride); };
+    uint32_t *tail = reinterpret_cast<uint32_t *>(page + kBTail) + is_v;
+    const bool fresh = mask & 1;
+    const int before = fresh ? 0 : min((int)*tail, kBExpTop);
+    uint32_t two = 0;
+#pragma unroll 1
+    for (uint32_t m = mask; m; m &= m - 1) {
+        const uint2 u = load(__ffs(m) - 1);
+        two = __vmaxu2(two, __vmaxu2(finite_magnitudes(u.x), finite_magnitudes(u.y)));
+    }
+    const int need = needed_exponent(__reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16)));
+    const int now = max(before, need);
+    const bool grows = !fresh && now > before, others = fresh || grows;
+    const float inv = power_of_two(kBExpBias - now), down = power_of_two(max(before - now, -60));
+    __syncwarp();                       // every lane has read the page's exponent
+    if (lane == 0 && others) *tail = now;
+    if (!is_v) {
+#pragma unroll 1
+        for (uint32_t m = others ? 0xffffu : mask; m; m &= m - 1) {
+            const int i = __ffs(m) - 1;
+            uint32_t *at = reinterpret_cast<uint32_t *>(page + b_k_at(i, lane));
+            *at = mask >> i & 1 ? to_codes(load(i), inv) : fresh ? 0u : requantise(*at, down);
+        }
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < kPage / 4; c++) {
+            const uint32_t mine = mask >> 4 * c & 15;
+            if (!mine && !others) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(page + b_v_at(c, lane));
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (mine != 15 && !fresh) {
+                const uint4 old = *at;
+                w[0] = old.x, w[1] = old.y, w[2] = old.z, w[3] = old.w;
+                transpose4(w);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (mine >> i & 1) w[i] = to_codes(load(4 * c + i), inv);
+                else if (grows) w[i] = requantise(w[i], down);
+            }
+            transpose4(w);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// The same for many tokens at once, all loads in flight together.  Elements that
+// are not finite, which do not count towards the scale and become NaN, are left
+// to the function above, so that nobody else pays for them.
+__device__ __forceinline__ void store_page(const BlockMoveArgs &a, const int *tokens, uint32_t mask, uint8_t *page, bool is_v, int h)
+{
+    const int lane = threadIdx.x & 31;
+    int token[kPage];
+#pragma unroll
+    for (int i = 0; i < kPage; i++) token[i] = tokens[i];
     const __nv_bfloat16 *src = (is_v ? a.v : a.k) + h * kD + 4 * lane;
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     uint2 u[kPage];
@@ -150,8 +227,13 @@ __device__ __forceinline__ void store_page(const BlockMoveArgs &a, const int (&t
     }
     uint32_t two = 0;
 #pragma unroll
-    for (int i = 0; i < kPage; i++) two = __vmaxu2(two, __vmaxu2(finite_magnitudes(u[i].x), finite_magnitudes(u[i].y)));
-    const int need = needed_exponent(__reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16)));
+    for (int i = 0; i < kPage; i++) two = __vimax3_u16x2(two, u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
+    if (top >= 0x7f80u) {
+        store_tokens(a, tokens, mask, page, is_v, h);
+        return;
+    }
+    const int need = needed_exponent(top);
     const int now = max(before, need);
     const bool grows = !fresh && now > before;
     const float inv = power_of_two(kBExpBias - now), down = power_of_two(max(before - now, -60));
@@ -161,118 +243,129 @@ __device__ __forceinline__ void store_page(const BlockMoveArgs &a, const int (&t
 #pragma unroll
         for (int i = 0; i < kPage; i++) {
             uint32_t *at = reinterpret_cast<uint32_t *>(page + b_k_at(i, lane));
-            if (token[i] >= 0) *at = to_codes(u[i], inv);
+            if (token[i] >= 0) *at = finite_codes(u[i], inv);
             else if (fresh) *at = 0;
             else if (grows) *at = requantise(*at, down);
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < kPage / 4; c++) {
-            uint4 *at = reinterpret_cast<uint4 *>(page + b_v_at(c, lane));
-            const bool any = token[4 * c] >= 0 || token[4 * c + 1] >= 0 || token[4 * c + 2] >= 0 || token[4 * c + 3] >= 0;
-            const bool all = token[4 * c] >= 0 && token[4 * c + 1] >= 0 && token[4 * c + 2] >= 0 && token[4 * c + 3] >= 0;
-            if (!any && !fresh && !grows) continue;
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (!all && !fresh) {
-                const uint4 old = *at;
-                w[0] = old.x, w[1] = old.y, w[2] = old.z, w[3] = old.w;
-                transpose4(w);          // a word per token
-            }
+        for (int c = 0; c < kPage / 4; c += 2) {
+            // two quads of tokens are 32 bytes, one whole sector
+            uint32_t w[8];
+            bool any = false;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (token[4 * c + i] >= 0) w[i] = to_codes(u[4 * c + i], inv);
-                else if (grows) w[i] = requantise(w[i], down);
+            for (int q = 0; q < 2; q++) {
+                const int t = 4 * (c + q);
+                const bool some = token[t] >= 0 || token[t + 1] >= 0 || token[t + 2] >= 0 || token[t + 3] >= 0;
+                const bool all = token[t] >= 0 && token[t + 1] >= 0 && token[t + 2] >= 0 && token[t + 3] >= 0;
+                any |= some;
+                uint32_t x[4] = {0, 0, 0, 0};
+                if (!all && !fresh) {
+                    const uint4 old = *reinterpret_cast<const uint4 *>(page + b_v_at(c + q, lane));
+                    x[0] = old.x, x[1] = old.y, x[2] = old.z, x[3] = old.w;
+                    transpose4(x);      // a word per token
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (token[t + i] >= 0) x[i] = finite_codes(u[t + i], inv);
+                    else if (grows) x[i] = requantise(x[i], down);
+                }
+                transpose4(x);          // a word per element
+#pragma unroll
+                for (int i = 0; i < 4; i++) w[4 * q + i] = x[i];
             }
-            transpose4(w);              // a word per element
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            if (any || fresh || grows)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n"
+                             :: "l"(page + b_v_at(c, lane)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                                "r"(w[6]), "r"(w[7])
+                             : "memory");
         }
     }
 }
 
-// kScan: a block per token, which looks through the slots; else a block per 16
-// tokens, which takes the pages whose lowest slot is among them from the marks.
-template <bool kScan>
-__global__ void __launch_bounds__(kThreads) block_append_kernel(const __grid_constant__ BlockMoveArgs a)
+// Up to kScanTokens tokens: a block per token and eight (head, keys or values),
+// a warp each, which looks through the slots for the others of its page.
+__global__ void __launch_bounds__(kThreads) block_append_scan_kernel(const __grid_constant__ BlockMoveArgs a)
 {
-    __shared__ int s_token[kPage], s_page[kPage];
-    __shared__ uint32_t s_lead;
-    const int tid = threadIdx.x, warp = tid >> 5, Hkv = a.st.kv_heads;
+    __shared__ int s_token[kPage];
+    __shared__ uint32_t s_mask;
+    const int tid = threadIdx.x, Hkv = a.st.kv_heads, item = blockIdx.y * (kThreads / 32) + (tid >> 5);
     pdl_wait();
-    uint32_t lead = 0;
-    int scan_page = 0;
-    if (kScan) {
-        const int slot = slot_inside(a, blockIdx.x, tid == 0);
-        if (slot < 0) return;
-        if (tid < kPage) s_token[tid] = -1;
-        __syncthreads();
-        for (int t = tid; t < a.n_tokens; t += kThreads) {
-            const int other = a.slots[t];
-            if (other >= 0 && other / kPage == slot / kPage) atomicMax(&s_token[other % kPage], t);
+    const int slot = slot_inside(a, blockIdx.x, tid == 0 && blockIdx.y == 0);
+    if (slot < 0) return;
+    const int page = slot / kPage;
+    if (tid < kPage) s_token[tid] = -1;
+    if (tid == kPage) s_mask = 0;
+    __syncthreads();
+    for (int t = tid; t < a.n_tokens; t += kThreads) {
+        const int other = a.slots[t];
+        if (other >= 0 && other / kPage == page) {
+            atomicMax(&s_token[other % kPage], t);          // of tokens that share a slot the last one counts
+            atomicOr(&s_mask, 1u << other % kPage);
         }
-        __syncthreads();
-        for (int i = 0; i < slot % kPage; i++)
-            if (s_token[i] >= 0) return;
-        if (s_token[slot % kPage] != (int)blockIdx.x) return;
-        scan_page = slot / kPage;
-        lead = 1;
-    } else {
-        if (warp == 0) {
-            const int t = blockIdx.x * kPage + tid;
-            const int slot = tid < kPage && t < a.n_tokens ? slot_inside(a, t, false) : -1;
-            bool own = false;
-            if (slot >= 0) {
-                // a page that another block has stored already has an empty mark
-                const volatile BlockMark *m = a.marks + slot / kPage;
-                const uint32_t mask = m->mask;
-                own = mask && __ffs(mask) - 1 == slot % kPage && m->token[slot % kPage] == (uint32_t)t + 1u;
-                if (own) s_page[tid] = slot / kPage;
-            }
-            const uint32_t all = __ballot_sync(0xffffffffu, own);
-            if (tid == 0) s_lead = all;
-        }
-        __syncthreads();
-        lead = s_lead;
     }
-    while (lead) {
-        const int i = __ffs(lead) - 1;
-        lead &= lead - 1;
-        const int page = kScan ? scan_page : s_page[i];
-        if (!kScan) {
-            __syncthreads();            // the page before has been read
-            if (tid < kPage) {
-                BlockMark &m = a.marks[page];
-                s_token[tid] = (int)m.token[tid] - 1;
-                m.token[tid] = 0;
-                if (tid == 0) m.mask = 0;
-            }
+    __syncthreads();
+    // the block that has the page's lowest slot stores the page
+    if (__ffs(s_mask) - 1 != slot % kPage || s_token[slot % kPage] != (int)blockIdx.x || item >= 2 * Hkv) return;
+    store_tokens(a, s_token, s_mask, a.st.pages + ((size_t)page * Hkv + (item >> 1)) * kBPageBytes, item & 1, item >> 1);
+}
+
+// More tokens: a block takes the pages whose lowest slot is among its `tokens`
+// consecutive tokens (kept in the marks), and its warps go through their heads'
+// keys and values.
+__global__ void __launch_bounds__(kThreads, 4) block_append_kernel(const __grid_constant__ BlockMoveArgs a, int tokens)
+{
+    __shared__ int s_page[kPage], s_token[kPage][kPage], s_pages;
+    const int tid = threadIdx.x, Hkv = a.st.kv_heads;
+    if (tid == 0) s_pages = 0;
+    __syncthreads();
+    pdl_wait();
+    if (tid < tokens) {
+        const int64_t t = (int64_t)blockIdx.x * tokens + tid;
+        const int slot = t < a.n_tokens ? slot_inside(a, (int)t, false) : -1;
+        if (slot >= 0) {
+            // a page that another block has stored already has an empty mark
+            const volatile BlockMark *m = a.marks + slot / kPage;
+            const uint32_t mask = m->mask;
+            if (mask && __ffs(mask) - 1 == slot % kPage && m->token[slot % kPage] == (uint32_t)t + 1u)
+                s_page[atomicAdd(&s_pages, 1)] = slot / kPage;
         }
-        __syncthreads();
-        int token[kPage];
-#pragma unroll
-        for (int k = 0; k < kPage; k++) token[k] = s_token[k];
-        for (int w = warp; w < 2 * Hkv; w += kThreads / 32) {
-            const int h = w >> 1;
-            store_page(a, token, a.st.pages + ((size_t)page * Hkv + h) * kBPageBytes, w & 1, h);
-        }
+    }
+    __syncthreads();
+    const int pages = s_pages;
+    for (int i = tid; i < pages * kPage; i += kThreads) {
+        BlockMark &m = a.marks[s_page[i / kPage]];
+        s_token[i / kPage][i % kPage] = (int)m.token[i % kPage] - 1;
+        m.token[i % kPage] = 0;
+        if (i % kPage == 0) m.mask = 0;
+    }
+    __syncthreads();
+    for (int w = tid >> 5; w < pages * 2 * Hkv; w += kThreads / 32) {
+        const int i = w / (2 * Hkv), item = w - i * 2 * Hkv, h = item >> 1, lane = tid & 31;
+        uint8_t *page = a.st.pages + ((size_t)s_page[i] * Hkv + h) * kBPageBytes;
+        const uint32_t mask = __ballot_sync(0xffffffffu, lane < kPage && s_token[i][lane & (kPage - 1)] >= 0);
+        if (__popc(mask) <= kFewTokens) store_tokens(a, s_token[i], mask, page, item & 1, h);
+        else store_page(a, s_token[i], mask, page, item & 1, h);
     }
 }
 
-// A warp reads 16 consecutive tokens' keys or values of one head, lane l the
-// elements 4 l .. 4 l + 3.  The values of four tokens that are an aligned quad
+// A warp reads 4 kQuads consecutive tokens' keys or values of one head, lane l
+// the elements 4 l .. 4 l + 3.  The values of four tokens that are an aligned quad
 // of a page, as a prefill's are, come with one load.
+template <int kQuads>
 __global__ void __launch_bounds__(kThreads) block_gather_kernel(const __grid_constant__ BlockMoveArgs a)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31, Hkv = a.st.kv_heads;
-    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;   // [16 tokens][head][K or V]
+    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;   // [4 kQuads tokens][head][K or V]
     const bool is_v = warp & 1;
     const int h = (int)((warp >> 1) % Hkv);
-    const int64_t t0 = (warp >> 1) / Hkv * kPage;
+    const int64_t t0 = (warp >> 1) / Hkv * (4 * kQuads);
     if (t0 >= a.n_tokens) return;
-    const int own = lane < kPage && t0 + lane < a.n_tokens ? slot_inside(a, (int)t0 + lane, h == 0 && !is_v) : -1;
+    const int own = lane < 4 * kQuads && t0 + lane < a.n_tokens ? slot_inside(a, (int)t0 + lane, h == 0 && !is_v) : -1;
     __nv_bfloat16 *out = (is_v ? a.v_out : a.k_out) + (t0 * Hkv + h) * kD + 4 * lane;
 #pragma unroll
-    for (int c = 0; c < kPage / 4; c++) {
+    for (int c = 0; c < kQuads; c++) {
         int slot[4];
         uint32_t w[4] = {0, 0, 0, 0}, e[4] = {kBExpBias, kBExpBias, kBExpBias, kBExpBias};
 #pragma unroll
@@ -529,13 +622,17 @@ mac_status mac_block_append(mac_block_handle h, int n_tokens, const void *dev_k,
     a.v_stride = v_stride;
     cudaError_t e;
     if (n_tokens <= kScanTokens) {
-        e = launch_maybe_pdl(block_append_kernel<true>, dim3(n_tokens), dim3(kThreads), 0, (cudaStream_t)stream, true, a);
+        e = launch_maybe_pdl(block_append_scan_kernel, dim3(n_tokens, (2 * h->cfg.kv_heads * 32 + kThreads - 1) / kThreads), dim3(kThreads), 0,
+                             (cudaStream_t)stream, true, a);
     } else {
         e = launch_maybe_pdl(block_mark_kernel, dim3((n_tokens + kThreads - 1) / kThreads), dim3(kThreads), 0,
                              (cudaStream_t)stream, true, a);
+        // few to a block while they may all be of different pages, and no more than one page's where they fill them
+        int tokens = 1;
+        while (tokens < kPage && n_tokens / tokens > kMostBlocks) tokens *= 2;
         if (e == cudaSuccess)
-            e = launch_maybe_pdl(block_append_kernel<false>, dim3((n_tokens + kPage - 1) / kPage), dim3(kThreads), 0,
-                                 (cudaStream_t)stream, true, a);
+            e = launch_maybe_pdl(block_append_kernel, dim3((n_tokens + tokens - 1) / tokens), dim3(kThreads), 0,
+                                 (cudaStream_t)stream, true, a, tokens);
     }
     return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, "append launch");
 }
@@ -553,9 +650,12 @@ mac_status mac_block_gather(mac_block_handle h, int n_tokens, const int32_t *dev
     BlockMoveArgs a = move_args(h, n_tokens, dev_slots);
     a.k_out = (__nv_bfloat16 *)dev_k;
     a.v_out = (__nv_bfloat16 *)dev_v;
-    const int64_t warps = 2 * (((int64_t)n_tokens + kPage - 1) / kPage) * h->cfg.kv_heads;
-    const cudaError_t e = launch_maybe_pdl(block_gather_kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
-                                           dim3(kThreads), 0, (cudaStream_t)stream, true, a);
+    const bool small = (int64_t)n_tokens * h->cfg.kv_heads < kSmallGather;
+    const int tokens = small ? 4 : 16;
+    const int64_t warps = 2 * (((int64_t)n_tokens + tokens - 1) / tokens) * h->cfg.kv_heads;
+    const cudaError_t e = launch_maybe_pdl(small ? block_gather_kernel<1> : block_gather_kernel<4>,
+                                           dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0,
+                                           (cudaStream_t)stream, true, a);
     return e == cudaSuccess ? MAC_OK : fail_cuda(h, e, "gather launch");
 }
 
