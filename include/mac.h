@@ -627,7 +627,8 @@ mac_status mac_prompt_destroy(mac_prompt_handle h);
  *   dev_k_starts  int32 [batch + 1] likewise up to n_kv, or NULL: starts.  A
  *                 sequence whose starts are not so is left out, which
  *                 mac_prompt_sync reports
- *   dev_out       [n_q][heads][128], bf16, or fp32 where out_fp32 is 1
+ *   dev_out       [n_q][heads][128], bf16, or fp32 where out_fp32 is 1; 32-byte
+ *                 aligned
  *   dev_lse       fp32 [n_q][heads], or NULL
  * Rows of no sequence are left as they are.  A key or value has no effect, NaN
  * included, on a query that does not see it; one that sees a value that is not

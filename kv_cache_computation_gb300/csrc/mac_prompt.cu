@@ -190,7 +190,7 @@ mac_status mac_prompt_attention(mac_prompt_handle h, int batch, int n_q, int n_k
     if (n_kv < 0 || n_kv > (1 << 26) || lag < 0 || lag > (1 << 30) || (out_fp32 != 0 && out_fp32 != 1)) return refuse(h);
     if (!dev_starts || !aligned(dev_starts, 4) || !aligned(dev_k_starts, 4) || !aligned(dev_lse, 4)) return refuse(h);
     if (batch == 0 || n_q == 0) return MAC_OK;
-    if (!dev_q || !dev_out || !aligned(dev_q, 16) || !aligned(dev_out, 16)) return refuse(h);
+    if (!dev_q || !dev_out || !aligned(dev_q, 16) || !aligned(dev_out, 32)) return refuse(h);   // outputs go out 32 bytes at a time
     if (n_kv > 0 && (!dev_k || !dev_v || !aligned(dev_k, 16) || !aligned(dev_v, 16))) return refuse(h);
     const int64_t q_row = (int64_t)c.heads * kD, kv_row = (int64_t)c.kv_heads * kD, most = (int64_t)1 << 38;
     if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride > most || k_stride > most || v_stride > most)

@@ -78,8 +78,8 @@ class PromptAttention:
     # -- attention ------------------------------------------------------------
     def __call__(self, q, k, v, starts, k_starts=None, lag=0, out=None, lse=None, want_lse=True, out_dtype=torch.bfloat16,
                  stream=None):
-        """out [tokens, heads, 128] (out_dtype: bfloat16 or float32) and lse float32 [tokens, heads] (natural log).  The
-        outputs carry no gradient."""
+        """out [tokens, heads, 128] (out_dtype: bfloat16 or float32) and lse float32 [tokens, heads] (natural log); an out
+        of the caller's starts on a multiple of 32 bytes.  The outputs carry no gradient."""
         dev, n, m = self.device, q.shape[0], k.shape[0]
         if v.shape[0] != m:
             raise ValueError("k and v must hold the same tokens")

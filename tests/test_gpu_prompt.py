@@ -341,6 +341,23 @@ def test_refusals():
     assert torch.equal(again[0], good[0])
 
 
+@pytest.mark.parametrize("dtype,off", [(BF16, 8), (torch.float32, 4), (torch.float32, 12)])
+def test_refuses_outputs_off_their_32_bytes(dtype, off):
+    """The rows are stored 32 bytes at a time: an out of the caller's that starts elsewhere is refused on the host."""
+    from kv_cache_computation_gb300 import MacError
+    c = Case([(30, 30), (12, 12)], 8, 2, seed=92, spare=0)
+    good = c.attend(c.q, c.k, c.v, c.starts, out_dtype=dtype)[0]
+    buf = torch.zeros(good.numel() + 64, dtype=dtype).cuda()
+    at = -buf.data_ptr() % 32 // buf.element_size()
+    with pytest.raises(MacError):
+        c.attend(c.q, c.k, c.v, c.starts, out=buf[at + off:at + off + good.numel()].view(good.shape), out_dtype=dtype)
+    torch.cuda.synchronize()
+    assert (buf == 0).all()
+    at += 32 // buf.element_size()
+    out = c.attend(c.q, c.k, c.v, c.starts, out=buf[at:at + good.numel()].view(good.shape), out_dtype=dtype)[0]
+    assert torch.equal(out, good)
+
+
 def test_offsets_beyond_32_bits():
     """Queries, keys and outputs whose byte and element offsets pass 2^32."""
     from kv_cache_computation_gb300 import PromptAttention
