@@ -71,6 +71,11 @@ template <int NT, int PP, int TEAMS, int STAGES, int MINB, bool QREG>
 __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const __grid_constant__ QuantAttnArgs a)
 {
     constexpr int PADROWS = NT * 8, UNIT_TOK = PP * kPage, UNIT_BYTES = PP * kBCopyBytes;
+    // What a piece costs besides its units, in units: Q, the first scores, the rows on their way out.  By the clock 1 to
+    // 2 units at 8 rows, 2.4 at 16, 3.2 at 24, 4 to 5 at 32.  Four ragged requests of 21 rows for each of 4 KV heads:
+    // 91 us without extra units, 78.6 with NT, 60.6 with NT + 2, 60.3 with 2 NT; 32 ragged requests of 32 rows on one KV
+    // head 89, 79, 78.6, 78.9; one of 4096 tokens, 8 heads, a unit to a warp, 14.7, 14.8, 15.2, 15.4.
+    constexpr int EXTRA = NT + 2;
     constexpr int TEAM_BYTES = block_team_bytes(NT, PP, STAGES, QREG);
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
     extern __shared__ __align__(128) unsigned char dyn[];
@@ -81,7 +86,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
     pdl_wait();
     pdl_launch_dependents();
 
-    make_line<TEAMS, UNIT_TOK>(a, sm.line);
+    make_line<TEAMS, UNIT_TOK, EXTRA>(a, sm.line);
     const uint32_t bar0 = smem_u32(&sm.bar[team * STAGES]);
     const uint32_t ring = smem_u32(dyn) + (uint32_t)team * TEAM_BYTES;
     if (tid == 0) {
@@ -102,24 +107,45 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
         if (tid == 0 && !by_group) a.meta[cta] = make_int4(-1, 0, 0, 0);
         return;
     }
+    // The warp's range and the block's.  A bound that would leave a piece with extra units alone moves to its group's
+    // beginning.  A warp's range may be empty then; the block's, of TEAMS units and more, is not.
+    static_assert(EXTRA + 1 < TEAMS, "a block has a piece");
     const Cut cut(U, grid * TEAMS);
-    const long long lo = cut.first(cta * TEAMS + team), hi = cut.first(cta * TEAMS + team + 1);
-    const long long cta_lo = cut.first(cta * TEAMS), cta_hi = cut.first((cta + 1) * TEAMS);
+    long long bound = U;
+    {
+        const int at = lane & 1 ? team + 1 : team, i = cta * TEAMS + (lane & 2 ? (lane & 1 ? TEAMS : 0) : at);
+        const long long p = cut.first(i);
+        if (p < U) {
+            int b, g, u, n;
+            locate(a, sm.line, p, b, g, u, n);
+            bound = u <= EXTRA ? p - u : p;
+        }
+    }
+    const long long lo = __shfl_sync(0xffffffffu, bound, 0), hi = __shfl_sync(0xffffffffu, bound, 1),
+                    cta_lo = __shfl_sync(0xffffffffu, bound, 2), cta_hi = __shfl_sync(0xffffffffu, bound, 3);
     if (tid == 0) {
         sm.lo = cta_lo;     // for the merge behind the long loop
         sm.hi = cta_hi;
     }
     const Parking park{dyn, TEAM_BYTES, TEAMS, PADROWS};
+    // the group that starts in this block and runs on behind it, for the second kernel
+    auto leave_meta = [&] {
+        if (team == TEAMS - 1 && lane == 0) write_meta(a, sm.line, cut, U, grid, TEAMS, cta_lo, cta_hi);
+    };
+    if (lo >= hi) leave_meta();
 
     if (lo < hi) {
-        int left = (int)(hi - lo);      // units to go
+        int left = (int)(hi - lo);      // units to go, extra ones among them
         int b, g, u0, n_units;
         locate(a, sm.line, lo, b, g, u0, n_units);
+        // a group's own units: from its beginning EXTRA fewer
+        int n = min(left, n_units - u0) - (u0 == 0 ? EXTRA : 0);
+        if (u0) u0 -= EXTRA;
 
-        // The copies run ahead of the reading over the same units: ld_group units of (ld_b, ld_g) to go, tokens from
-        // the next unit on in the request, and the lane's page id of that unit, read one unit ahead.
+        // The copies run ahead of the reading over the same units: ld_group units of (ld_b, ld_g) to go and ld_left behind
+        // them, tokens from the next unit on in the request, and the lane's page id of that unit, read one unit ahead.
         const size_t page_stride = (size_t)Hkv * kBPageBytes;
-        int ld_left = left, ld_b = b, ld_g = g, ld_group = n_units - u0, ld_tok = sm.line.len[b] - u0 * UNIT_TOK;
+        int ld_b = b, ld_g = g, ld_group = n, ld_left = left - n - (u0 ? 0 : EXTRA), ld_tok = sm.line.len[b] - u0 * UNIT_TOK;
         const int32_t *ld_ids = a.table + (int64_t)b * a.table_stride + u0 * PP + lane;
         int next_id = 0;
         auto fetch = [&]() {
@@ -127,7 +153,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
             if (lane < PP && lane * kPage < ld_tok) next_id = *ld_ids;      // checked where it is used, when it has arrived
         };
         auto issue = [&](int s) {
-            if (ld_left == 0) return;
+            if (ld_group == 0) return;
             const uint32_t bar = bar0 + 8 * s;
             if ((unsigned)next_id >= (unsigned)a.st.num_pages) {
                 atomicOr(a.st.err, kQErrPage);
@@ -144,13 +170,15 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
             if (lane < pages)
                 bulk_load(ring + (uint32_t)s * UNIT_BYTES + lane * kBCopyBytes,
                           a.st.pages + (size_t)(unsigned)next_id * page_stride + (size_t)ld_g * kBPageBytes, kBCopyBytes, bar);
-            if (--ld_left == 0) return;
             if (--ld_group == 0) {
+                if (ld_left == 0) return;
                 if (++ld_g == Hkv) {
                     ld_g = 0;
                     ld_b++;
                 }
-                ld_group = (int)(sm.line.pre[ld_b + 1] - sm.line.pre[ld_b]);
+                const int all = min(ld_left, (int)(sm.line.pre[ld_b + 1] - sm.line.pre[ld_b]));
+                ld_left -= all;
+                ld_group = all - EXTRA;
                 ld_tok = sm.line.len[ld_b];
                 ld_ids = a.table + (int64_t)ld_b * a.table_stride + lane;
             } else {
@@ -163,16 +191,13 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
 #pragma unroll
         for (int s = 0; s < STAGES; s++) issue(s);
 
-        // while the first pages arrive: the group that starts in this block and runs on behind it, for the second kernel
-        // (the last warp of a block always has a unit)
-        if (team == TEAMS - 1 && lane == 0) write_meta(a, sm.line, cut, U, grid, TEAMS, cta_lo, cta_hi);
+        leave_meta();                   // while the first pages arrive
 
         int stage = 0;
         uint32_t phase = 0;
         const int tk = 4 * (g8 >> 1) + (g8 & 1);    // token of matrix row g; row g + 8 is token tk + 2
         while (left > 0) {
             // one piece: units [u0, u0 + n) of group (b, g)
-            const int n = min(left, n_units - u0);
             const int len = sm.line.len[b];
             const int full = max(len - (a.n_query - 1), 0);     // tokens every row sees
             uint32_t qf[QREG ? NT : 1][16];
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                     phase ^= 1;
                 }
             }
-            left -= n;
+            left -= n + (u0 ? 0 : EXTRA);
 
             if (met && a.n_query > 1) {
                 // the queries that see a token whose NaN was taken out get it here
@@ -420,7 +445,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) sum[nt][h] += __shfl_xor_sync(0xffffffffu, sum[nt][h], off);
                 }
-            const bool ends = u0 + n == n_units, whole = u0 == 0 && ends;
+            const bool ends = u0 + n + EXTRA == n_units, whole = u0 == 0 && ends;
             const int which = ends ? 0 : 1;     // 1: the group runs on into the next warp's range
             if (lane == 0) {
                 if (!whole) sm.piece_group[2 * team + which] = b * Hkv + g;
@@ -463,6 +488,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                 g = 0;
                 if (++b < a.batch) n_units = (int)(sm.line.pre[b + 1] - sm.line.pre[b]);
             }
+            n = min(left, n_units) - EXTRA;
         }
     }
     merge_pieces<TEAMS, TEAMS>(a, sm, park);

@@ -24,7 +24,9 @@ struct Line {
 };
 
 // Fills the line from the lengths; all threads of the block (kWarps warps).
-template <int kWarps, int kTok>
+// kExtra: units that each group counts besides its own, in front of them, for
+// what a piece costs whatever its length.
+template <int kWarps, int kTok, int kExtra = 0>
 __device__ __forceinline__ void make_line(const QuantAttnArgs &a, Line &line)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -41,7 +43,7 @@ __device__ __forceinline__ void make_line(const QuantAttnArgs &a, Line &line)
             }
             line.len[b] = len;
         }
-        const long long own = b < a.batch ? (len > kTok ? (len - 1) / kTok + 1 : 1) : 0;
+        const long long own = b < a.batch ? (len > kTok ? (len - 1) / kTok + 1 : 1) + kExtra : 0;
         long long x = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

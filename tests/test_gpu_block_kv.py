@@ -210,6 +210,18 @@ def test_attention_lengths(lens):
     c.check(*c.run(), requests=range(0, len(lens), max(1, len(lens) // 10)))
 
 
+@pytest.mark.parametrize("H,Hkv,nq", [(4, 1, 1), (48, 4, 1), (20, 1, 1), (60, 2, 1)])
+def test_attention_cut_at_any_place(H, Hkv, nq):
+    """Short requests, some without tokens: with more and more of them the cut of the line falls on every place of a group,
+    its beginning and what counts for a piece's own cost included."""
+    lens = np.random.default_rng(H).integers(0, 150, 420).tolist()
+    c = Case(lens, H, Hkv, nq, seed=H)
+    for B in list(range(1, 420, 23)) + [420]:
+        out, lse = c.run(q=c.dev["q"][:B], page_table=c.dev["page_table"][:B], lengths=c.dev["lengths"][:B])
+        c.check(out, lse, requests=range(B) if B == 420 else range(0, B, 5))
+    c.cache.sync()
+
+
 @pytest.mark.parametrize("H,Hkv,nq", [(32, 8, 1), (16, 1, 1), (32, 1, 1), (28, 4, 3)])
 def test_attention_long(H, Hkv, nq):
     c = Case([30001], H, Hkv, nq, seed=3)
