@@ -744,15 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             }
             if (!ok) break;
 
-            // the row's output, or its part of one
+            // The row's output, or its part of one.  What needs no product comes while the last one runs.
             const bool some = last > j0;
-            if (some) {
-                if (!wait_or_fail(B_(bars.o_full[x]), no & 1, fail)) break;
-                no++;
-                fence_after();
-            }
             const int slot = p->slot;
-            const bool part = slot >= 0, dirty = some && *(volatile int *)&queue.dirty[follow.place()];
+            const bool part = slot >= 0;
             const float scale = !some || sum == 0.f ? 0.f : part ? 1.f : 1.f / sum;
             const int row_tok = row / a.G;
             const int64_t out_row = (int64_t)(p->row0 + x * a.tile_tokens + row_tok) * a.heads + p->head * a.G + row - row_tok * a.G;
@@ -760,8 +755,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const bool fp32 = part || kWide;
             char *to = fp32 ? reinterpret_cast<char *>(part ? a.part_o + part_row * kD : reinterpret_cast<float *>(a.out) + out_row * kD)
                             : reinterpret_cast<char *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row * kD);
-            const int *bad = queue.bad[follow.place()];
+            if (valid) {
+                if (part) a.part_ml[part_row] = make_float2(ref, sum);
+                else if (a.lse) a.lse[out_row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
+            }
             const bool every = __all_sync(0xffffffffu, scale != 0.f);       // else some rows' O was never written, or is to be 0
+            if (some) {
+                if (!wait_or_fail(B_(bars.o_full[x]), no & 1, fail)) break;
+                no++;
+                fence_after();
+            }
+            const bool dirty = some && *(volatile int *)&queue.dirty[follow.place()];
+            const int *bad = queue.bad[follow.place()];
             // (rolled up: once per piece, its instructions come from far away)
 #pragma unroll 1
             for (int c = 0; c < (fp32 ? 8 : 4); c++) {
@@ -801,10 +806,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     store32(to + 64 * c, w);
                     store32(to + 64 * c + 32, w + 8);
                 }
-            }
-            if (valid) {
-                if (part) a.part_ml[part_row] = make_float2(ref, sum);
-                else if (a.lse) a.lse[out_row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
             }
             fence_before();
             __syncwarp();
