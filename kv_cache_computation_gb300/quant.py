@@ -47,7 +47,8 @@ class _PagedStore:
         with torch.cuda.device(self.device):
             self._store = torch.empty(store, dtype=torch.uint8, device=self.device)
             if share is not None:
-                if type(share) is not type(self) or share.device != self.device or share._scratch.numel() < scratch:
+                if (getattr(share, "_prefix", self._prefix) != self._prefix or share.device != self.device or
+                        share._scratch.numel() < scratch):
                     raise ValueError(f"share must be a {type(self).__name__} on the same device with as large a scratch")
                 self._scratch = share._scratch
             else:
