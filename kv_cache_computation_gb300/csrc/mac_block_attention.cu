@@ -15,13 +15,24 @@
 //
 // Rows, products, fragments' free orders, the split into equal ranges of a line
 // of units and the merge of pieces are those of the 4-bit store's attention
-// (mac_quant_attention.cu, mac_quant_line.cuh, mac_quant_merge.cuh): a warp takes
-// whole pages from a ring of its own, scores are S^T = K Q^T, the output O^T +=
+// (mac_quant_attention.cu, mac_quant_line.cuh, mac_quant_merge.cuh), but that a
+// piece's own cost counts in the line: a warp takes whole pages from a ring of its own, scores are S^T = K Q^T, the output O^T +=
 // V^T P^T, both mma.m16n8k16 in f16 with fp32 accumulators.
 // Roundings: Q is bf16 and becomes f16 with a power of two per row (exact but
 // for elements below 2^-28 of the row's largest); codes are exact in f16;
 // the weights w, at most 2^15, are rounded to f16 (2^-11 of each) and summed
 // unrounded in fp32; everything else stays in fp32.
+//
+// Measured (graph replays, 258 bytes per token and KV head): 8 x 131072, 32 / 8
+// heads 321 us (6.7 TB/s, the copy rate); 1 x 4096 14.5 us; 4 ragged requests to
+// 122880, 21 rows for each of 4 heads 62 us (3.8 TB/s); 32 ragged ones to 65536,
+// 32 rows on one head 79.5 us (2.7 TB/s).  8 x 65536 with 8 heads at 4, 8, 12, 16,
+// 24, 32 rows: 168, 174, 173, 179, 202, 254 us.
+// What bounds it.  Up to 16 rows the stream, around which a call pays about 13 us:
+// launch, lengths and line, the first page, the merges and the second kernel.  With
+// more rows the registers leave two warps to a scheduler, whose dependent
+// instructions' latencies nothing covers (issue slots 36 % used, tensor pipe 40 %
+// at 32 rows).
 #include "mac_block.cuh"
 #include "mac_quant_merge.cuh"
 
@@ -72,9 +83,10 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
 {
     constexpr int PADROWS = NT * 8, UNIT_TOK = PP * kPage, UNIT_BYTES = PP * kBCopyBytes;
     // What a piece costs besides its units, in units: Q, the first scores, the rows on their way out.  By the clock 1 to
-    // 2 units at 8 rows, 2.4 at 16, 3.2 at 24, 4 to 5 at 32.  Four ragged requests of 21 rows for each of 4 KV heads:
-    // 91 us without extra units, 78.6 with NT, 60.6 with NT + 2, 60.3 with 2 NT; 32 ragged requests of 32 rows on one KV
-    // head 89, 79, 78.6, 78.9; one of 4096 tokens, 8 heads, a unit to a warp, 14.7, 14.8, 15.2, 15.4.
+    // 2 units at 8 rows, 2.4 at 16, 3.2 at 24, 4 to 5 at 32.  us with 0, NT, NT + 2 (and 2 NT) units: 4 ragged requests of
+    // 21 rows for each of 4 KV heads 92, 77.8, 60.2 (60.3), the same of 28 rows 64.6 / 59.6 / 51.7; 32 ragged requests of
+    // 32 rows on one head 92.7 / 81.5 / 78.2 (78.9), of 8 rows 48.9 / 46.6 / 46.1; long uniform ones and one of 4096 tokens
+    // are the same with all.
     constexpr int EXTRA = NT + 2;
     constexpr int TEAM_BYTES = block_team_bytes(NT, PP, STAGES, QREG);
     static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
@@ -269,8 +281,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                 int ek[PP], ev[PP];
 #pragma unroll
                 for (int pp = 0; pp < PP; pp++) {
-                    const uint32_t page = unit + pp * kBCopyBytes;
-                    const uint32_t e0 = lds4(page + kBTail), e1 = lds4(page + kBTail + 4);
+                    const uint32_t e0 = lds4(unit + pp * kBCopyBytes + kBTail), e1 = lds4(unit + pp * kBCopyBytes + kBTail + 4);
                     // a page behind the request's last was not copied: any bytes
                     ek[pp] = (int)min(e0, (uint32_t)kBExpTop) - kBExpBias;
                     ev[pp] = (int)min(e1, (uint32_t)kBExpTop) - kBExpBias;
@@ -278,25 +289,29 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int k = 0; k < 4; k++) s[pp][nt][k] = 0.f;
+                }
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; i2++) {
-                        const uint4 ka = lds16(page + i2 * 512 + lane * 16), kb = lds16(page + (2 + i2) * 512 + lane * 16);
-                        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-                        // Q of the lane's elements 16 i2 .. 16 i2 + 15, two 16-byte words of fragments
-                        uint32_t f[NT][8];
+                for (int i2 = 0; i2 < 2; i2++) {
+                    // Q of the lane's elements 16 i2 .. 16 i2 + 15, two 16-byte words of fragments
+                    uint32_t f[NT][8];
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++) {
-                            if (QREG) {
+                    for (int nt = 0; nt < NT; nt++) {
+                        if (QREG) {
 #pragma unroll
-                                for (int k = 0; k < 8; k++) f[nt][k] = qf[nt][8 * i2 + k];
-                            } else {
+                            for (int k = 0; k < 8; k++) f[nt][k] = qf[nt][8 * i2 + k];
+                        } else {
 #pragma unroll
-                                for (int k = 0; k < 2; k++) {
-                                    const uint4 v = lds16(ring + STAGES * UNIT_BYTES + ((nt * 4 + 2 * i2 + k) * 32 + lane) * 16);
-                                    f[nt][4 * k] = v.x, f[nt][4 * k + 1] = v.y, f[nt][4 * k + 2] = v.z, f[nt][4 * k + 3] = v.w;
-                                }
+                            for (int k = 0; k < 2; k++) {
+                                const uint4 v = lds16(ring + STAGES * UNIT_BYTES + ((nt * 4 + 2 * i2 + k) * 32 + lane) * 16);
+                                f[nt][4 * k] = v.x, f[nt][4 * k + 1] = v.y, f[nt][4 * k + 2] = v.z, f[nt][4 * k + 3] = v.w;
                             }
                         }
+                    }
+#pragma unroll
+                    for (int pp = 0; pp < PP; pp++) {
+                        const uint32_t page = unit + pp * kBCopyBytes;
+                        const uint4 ka = lds16(page + i2 * 512 + lane * 16), kb = lds16(page + (2 + i2) * 512 + lane * 16);
+                        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
                             uint32_t a0, a1, a2, a3;
@@ -510,8 +525,12 @@ Variant variant()
 // As many warps as the registers of an output tile of 8 NT rows, and the rings, leave room for.
 Variant variant_for(int rows)
 {
-    if (rows <= 8) return variant<1, 2, 12, 2, 1, true>();
-    if (rows <= 16) return variant<2, 2, 12, 2, 1, true>();
+    // N tiles as the rows need: a tile more costs (8 x 65536, 8 heads) 4 rows 178 -> 185 us, 16 rows 194 -> 202, 24 rows
+    // 202 -> 249.  8 warps, two to a scheduler, where 12 would fit as well: 4 rows 178 -> 169, 16 rows 194 -> 179, 1 x
+    // 4096 16.5 -> 14.5; 6 warps 184 and 222, 16 of one-page units 182 and 316.  Two pages to a unit: one page 189 and 208
+    // (32 rows: 254 -> 296), four 184 and 198; a third stage 184 and 179.  Q in registers where they suffice.
+    if (rows <= 8) return variant<1, 2, 8, 2, 1, true>();
+    if (rows <= 16) return variant<2, 2, 8, 2, 1, true>();
     if (rows <= 24) return variant<3, 2, 8, 2, 1, false>();
     return variant<4, 2, 8, 2, 1, false>();
 }

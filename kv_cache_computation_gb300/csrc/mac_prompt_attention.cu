@@ -17,8 +17,11 @@
 // Per block and tile: S = Q K^T (8 tcgen05.mma of 128 x 128 x 16, operands in
 // shared memory, S in tensor memory), softmax by one thread per row, P in bf16
 // back into tensor memory over S, O += P V (8 more, P read from tensor memory).
-// The tensor pipe needs 512 cycles for each of the two products, and while it
-// works for one tile the other tile's four warps do their softmax.
+// The tensor pipe needs 512 cycles for each of the two products (64 for each of
+// the 8, whichever memory A comes from, and whatever the softmax does beside it:
+// measured), and while it works for one tile the other tile's four warps do their
+// softmax.  S, P and O of two tiles fill the 512 columns of tensor memory, and two
+// tiles of Q and four blocks of keys and values 192 KB of shared memory.
 // Roundings: scores, references, sums and O in fp32; P to bf16 (2^-8 of each
 // weight, as the bf16 output's own rounding; the sums take P unrounded).  Where
 // the output is fp32, P is a bf16 pair hi + lo (2^-16) and O += P_hi V + P_lo V.
@@ -27,12 +30,15 @@
 // last (longest) on, head by head.  With R + 1 or more items per CTA, a CTA takes
 // R whole items, one from each row of `grid` items (back and forth, so that lengths
 // even out), and what is left, one to two rows, is one line of blocks that is cut
-// so that all CTAs end together; an item that is cut is merged by a second kernel.
+// so that all CTAs end together; an item that is cut is merged by a second kernel
+// (there is none where no sequence has more than a block of keys).
 // Everything follows from the lengths on the device, in each CTA's prologue: a
 // captured call serves other lengths, and a call repeats bit for bit.
 //
-// Warps 0-3 softmax of tile A, 4-7 of tile B; warp 8 issues the products; warp 9
-// loads keys and values by TMA into a ring of four blocks; warp 10 loads Q and
+// Warps 0-3 softmax and output of tile A, 4-7 of tile B; warp 8 issues the
+// products; warp 11 finds the CTA's pieces (items, or parts of them), which takes
+// longer than a block of keys, and announces them up to four ahead; warp 9 loads
+// keys and values by TMA into a ring of four blocks; warp 10 loads Q and
 // looks through the value blocks on the causal edge (or a sequence's end): a NaN
 // or an infinity there would reach rows that do not see it, as 0 * NaN, so it is
 // taken out of the block and put back into the rows that do see it at the end.
@@ -41,6 +47,30 @@
 // returns.  Completion k of a barrier is awaited with parity k & 1; every role
 // waits each completion in order, and none can be two ahead of a waiter: a stage,
 // a tile's Q, S, P and O are filled again only after their reader has passed on.
+//
+// Measured (graph replays; 32 / 8 heads but where noted; 1965 TFLOP/s is the
+// library's largest product's rate): 32768 tokens 5.25 ms (1675 TFLOP/s of the
+// products that the causal edge leaves), 2048 and 509 tokens behind 30720 and
+// 8191 693 us (1638), 24 ragged prompts of 1 .. 4096 tokens 449 us (1212), 5 of 1
+// .. 6001 with 28 / 4 heads 262 us (1141), 512 fp32 rows behind 32256 253 to 280
+// us (995; with the second P V 1490), 16 tokens 10.7 us.
+// What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
+// from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
+// ex2 at 32 a cycle and SM, loads and stores of tensor memory, maximum and packing;
+// the rest barriers), its products 1024 and 190 until they are seen, and the other
+// tile fills 2048 of that.  In long calls the card then holds its power limit at
+// 1.7 to 1.85 GHz, and fewer cycles give little.  A piece costs about 6000 cycles
+// besides its blocks (first scores 1750, the first softmax, the output 3600), which
+// with the edge blocks' hidden halves is what ragged prompts lose; the prologue
+// (lengths, split, first loads) 8000 to 16000 a call.
+// Tried and slower (32768 tokens, us, against the form of the time): softmax
+// warps of half a row each 5.79 / 5.45 ms; a second warp to issue 7.05 / 6.0; P V
+// issued for the first keys before the last weights are there 5.70 / 5.33; waits
+// that spin 5.5 / 5.33; weights against the old reference, which the row's sum
+// then confirms, instead of a maximum first: no faster at 32768 tokens, 28 heads
+// 308 / 262 us; every eighth ex2 as a polynomial 5.43 / 5.28 (packed products run at
+// half rate); outputs through shared memory, in whole lines, slower than 32 bytes a
+// thread from the registers.
 #include "mac_device.cuh"
 #include "mac_prompt.cuh"
 
@@ -57,7 +87,7 @@ constexpr int kBlockBytes = 2 * kTok * 128;         // two column halves of 128 
 constexpr int kStages = 4;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kCheckWarp = 10;       // warp 11 announces the pieces
 constexpr int kPieces = 4;                          // pieces announced ahead
-constexpr int kThreads = 12 * 32;                   // three warpgroups; warp 11 has no role
+constexpr int kThreads = 12 * 32;                   // three warpgroups
 // registers: 168 per thread at launch (three warpgroups: 504), then 208 for the
 // softmax's two and 88 for the others'
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;

@@ -1,5 +1,5 @@
-// Parts of the attention over the 4-bit store: the line of work units and its
-// cut into equal ranges, and the unpacking of codes.
+// Parts of the attentions over the quantised stores: the line of work units and
+// its cut into equal ranges, and the unpacking of 4-bit codes.
 //
 // A unit is a fixed number of tokens of one (request, KV head) group; a request
 // without tokens has one unit, so that its output gets written.  The units of
