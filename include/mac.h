@@ -607,7 +607,7 @@ typedef struct {
 } mac_prompt_config;
 
 /* Bytes of the backing buffer (host arithmetic): partial results of the items
- * that several SMs work on, and the error word. */
+ * that several SMs work on, sums of long runs of keys, and the error word. */
 mac_status mac_prompt_query_sizes(const mac_prompt_config *cfg, size_t *scratch_bytes);
 
 /* A handle over a caller-allocated device buffer (256-byte aligned, at least
@@ -633,7 +633,8 @@ mac_status mac_prompt_destroy(mac_prompt_handle h);
  * Rows of no sequence are left as they are.  A key or value has no effect, NaN
  * included, on a query that does not see it; one that sees a value that is not
  * finite gives NaN in that element (or the infinity that the sum comes to).
- * The softmax weights are rounded to bf16 (fp32 outputs: to 16 bits).  Results
+ * The softmax weights are rounded to bf16 (fp32 outputs: to 17 bits, and the
+ * outputs' relative error is about 3e-6 up to 32768 keys and more).  Results
  * do not depend on other sequences' values, but the split of the work, and with
  * it the order of sums, depends on all starts of the call.  Async on stream. */
 mac_status mac_prompt_attention(mac_prompt_handle h, int batch, int n_q, int n_kv, int lag, const void *dev_q, int64_t q_stride,

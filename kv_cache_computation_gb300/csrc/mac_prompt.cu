@@ -32,7 +32,7 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // The error word comes first, at one place for all handles that share a scratch.
 struct Sizes {
-    size_t err, meta, part_ml, part_o, scratch;
+    size_t err, meta, part_ml, part_o, carry, scratch;
 };
 
 Sizes scratch_sizes()
@@ -42,7 +42,8 @@ Sizes scratch_sizes()
     z.meta = 256;
     z.part_ml = z.meta + align_up(kPMaxCtas * sizeof(PromptMeta));
     z.part_o = z.part_ml + align_up((size_t)kPMaxCtas * 2 * kPRows * sizeof(float2));
-    z.scratch = z.part_o + (size_t)kPMaxCtas * 2 * kPRows * kD * sizeof(float);
+    z.carry = z.part_o + (size_t)kPMaxCtas * 2 * kPRows * kD * sizeof(float);
+    z.scratch = z.carry + (size_t)kPMaxCtas * kPRows * kD * sizeof(float);
     return z;
 }
 
@@ -128,6 +129,7 @@ mac_status mac_prompt_create(const mac_prompt_config *cfg, void *dev_scratch, si
     a.meta = (PromptMeta *)(sc + z.meta);
     a.part_ml = (float2 *)(sc + z.part_ml);
     a.part_o = (float *)(sc + z.part_o);
+    a.carry = (float4 *)(sc + z.carry);
 
     cudaDeviceProp prop;
     bool good = cudaGetDevice(&h->device) == cudaSuccess && cudaGetDeviceProperties(&prop, h->device) == cudaSuccess;

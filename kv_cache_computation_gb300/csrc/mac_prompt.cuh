@@ -30,6 +30,7 @@ struct PromptArgs {
     float scale_log2;                       // score scale x log2(e)
     float *part_o;                          // [CTA][2][kPRows][128] unnormalised partial outputs
     float2 *part_ml;                        // [CTA][2][kPRows] reference (log2) and sum
+    float4 *carry;                          // [CTA][2 tiles][32][128 rows] sums of runs of products
     PromptMeta *meta;                       // [CTA]
     uint32_t *err;
 };

@@ -24,7 +24,8 @@
 // tiles of Q and four blocks of keys and values 192 KB of shared memory.
 // Roundings: scores, references, sums and O in fp32; P to bf16 (2^-8 of each
 // weight, as the bf16 output's own rounding; the sums take P unrounded).  Where
-// the output is fp32, P is a bf16 pair hi + lo (2^-16) and O += P_hi V + P_lo V.
+// the output is fp32, P is a bf16 pair hi + lo (2^-17 of each weight) and O += P_hi
+// V + P_lo V, in runs of eight blocks (kWideRun).
 //
 // Work split.  Items are numbered sequence by sequence, tile by tile from the
 // last (longest) on, head by head.  With R + 1 or more items per CTA, a CTA takes
@@ -52,8 +53,8 @@
 // library's largest product's rate): 32768 tokens 5.25 ms (1675 TFLOP/s of the
 // products that the causal edge leaves), 2048 and 509 tokens behind 30720 and
 // 8191 693 us (1638), 24 ragged prompts of 1 .. 4096 tokens 449 us (1212), 5 of 1
-// .. 6001 with 28 / 4 heads 262 us (1141), 512 fp32 rows behind 32256 253 to 280
-// us (995; with the second P V 1490), 16 tokens 10.7 us.
+// .. 6001 with 28 / 4 heads 262 us (1141), 512 fp32 rows behind 32256 298 us (913;
+// with the second P V 1370), 16 tokens 10.7 us.
 // What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
 // from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
 // ex2 at 32 a cycle and SM, loads and stores of tensor memory, maximum and packing;
@@ -94,6 +95,15 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTmemCols = 512;                      // S of A, B at 0, 128; O at 256, 384
 constexpr int kDynBytes = 1024 + (2 + kStages) * kBlockBytes;
 constexpr uint32_t kSpin = 1u << 22;
+// Blocks of a run, a power of two.  The tensor cores cut a sum off towards 0 where
+// a product is added to it: 1.4e-8 of it on average, always the same way, so that it
+// grows with the number of products (16 per block in the wide form, 8 in the other).
+// So a sum of a run's products goes to memory, in fp32, and the next run starts anew.
+// 512 fp32 rows behind 32256 keys, error and us with runs of 4, 8, 16 blocks and with
+// one: 2.8e-6 326, 3.4e-6 298, 5.2e-6 283, 2.9e-5 256 (fp32 products 3.2e-6).  Beside
+// outputs of 2^-9 512 blocks' 2^-14 are enough, which calls of at most 65536 keys do
+// not reach: they take the form without runs (24 ragged prompts 455 -> 448 us).
+constexpr int kWideRun = 8, kRun = 512;
 constexpr float kMargin = 8.f;                      // log2: how far a score may pass its row's reference
 constexpr float kLowest = -3e38f;                   // the reference before the first key: finite, so that masked scores weigh 0
 
@@ -553,6 +563,55 @@ __device__ __forceinline__ void rescale(uint32_t tO, float f)
     }
 }
 
+// A row's sum of the runs before, in memory: element 4 i .. 4 i + 3 at carry[128 i],
+// so that a warp's rows are one line.  leave_run adds O of the row to it (or starts
+// it; f brings it to O's reference), take_run adds it, times f, to O.
+__device__ __noinline__ void leave_run(uint32_t tO, float4 *carry, bool starts, float f)
+{
+    if (!starts && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+        for (int i = 0; i < kD / 4; i++) {
+            const float4 v = __ldcg(carry + 128 * i);
+            __stcg(carry + 128 * i, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+        }
+    }
+#pragma unroll 1
+    for (int c = 0; c < 4; c++) {
+        float o[32];
+        tmem_ld32(tO + 32 * c, o);
+        tmem_wait_ld();
+        float4 *to = carry + 1024 * c;
+        if (starts) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) __stcg(to + 128 * i, make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n"
+                             :: "l"(to + 128 * i), "f"(o[4 * i]), "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
+                             : "memory");
+        }
+    }
+}
+
+__device__ __noinline__ void take_run(uint32_t tO, const float4 *carry, float f)
+{
+#pragma unroll 1
+    for (int c = 0; c < 8; c++) {
+        float o[16];
+        tmem_ld16(tO + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float4 v = __ldcg(carry + 512 * c + 128 * i);
+            o[4 * i] = fmaf(v.x, f, o[4 * i]), o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+        }
+        tmem_st16(tO + 16 * c, reinterpret_cast<const uint32_t *>(o));
+    }
+    tmem_wait_st();
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // two fp32 operations in one instruction
@@ -649,6 +708,13 @@ __device__ __forceinline__ void softmax_block(uint32_t tS, uint32_t tO, float sc
     sum += (part[0] + part[1]) + (part[2] + part[3]);
 }
 
+// Does a run of blocks, whose products add up in tensor memory, begin with block j of a piece?
+template <bool kWide, bool kRuns>
+__device__ __forceinline__ bool run_begins(int j, int j0)
+{
+    return kRuns ? ((j - j0) & ((kWide ? kWideRun : kRun) - 1)) == 0 : j == j0;
+}
+
 struct Bars {
     unsigned long long full[kStages], empty[kStages];   // ring of key and value blocks
     unsigned long long q_full[2], q_empty[2];           // Q of a tile
@@ -685,7 +751,8 @@ struct Follow {
     }
 };
 
-template <bool kWide>
+// kWide: fp32 outputs.  kRuns: pieces may be longer than a run.
+template <bool kWide, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptArgs a,
                                                                       const __grid_constant__ PromptMaps maps)
 {
@@ -757,7 +824,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const int j0 = p->j0, last = p->last(x), edge = p->edge;
             const bool valid = row < p->rows(x);
             const int lim = valid ? p->seen(x * a.tile_tokens + row / a.G) : 0;       // keys the row sees
-            float ref = kLowest, sum = 0.f;
+            float ref = kLowest, sum = 0.f, carry_ref = kLowest;
+            bool carried = false;
+            float4 *carry = a.carry + ((int64_t)blockIdx.x * 2 + x) * (kD / 4) * 128 + row;
             for (int j = j0; j < last; j++) {
                 if (!wait_or_fail(B_(bars.s_full[x]), ns & 1, fail)) {
                     ok = false;
@@ -765,8 +834,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 ns++;
                 fence_after();
+                const bool starts = run_begins<kWide, kRuns>(j, j0);
+                if (kRuns && starts && j > j0) {
+                    // the products before are complete: these scores were issued behind them
+                    leave_run(tO, carry, !carried, ex2_approx(carry_ref - ref));
+                    carried = true;
+                    carry_ref = ref;
+                }
                 const int live = lim - j * kTok;        // of the block's keys, those that the row sees
-                softmax_block<kWide>(tS, tO, sc, live, j >= edge, j > j0, ref, sum);
+                softmax_block<kWide>(tS, tO, sc, live, j >= edge, !starts, ref, sum);
                 tmem_wait_st();
                 fence_before();
                 __syncwarp();
@@ -795,6 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 no++;
                 fence_after();
             }
+            if (kRuns && carried) take_run(tO, carry, ex2_approx(carry_ref - ref));
             const bool dirty = some && *(volatile int *)&queue.dirty[follow.place()];
             const int *bad = queue.bad[follow.place()];
             // (rolled up: once per piece, its instructions come from far away)
@@ -952,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 release(K::value);
             };
-            // block j: outputs, and the scores of j + 1; kSteady: both tiles go on, and no row is at its edge
+            // block j: outputs, and the scores of j + 1; kSteady: both tiles go on, no run begins, and no row is at its edge
             auto block = [&](auto Half, auto Steady, int j) {
                 constexpr int half = decltype(Half)::value;
                 constexpr bool kSteady = decltype(Steady)::value != 0;
@@ -979,14 +1056,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     if (!ready_a) wait(bars.p_full[0], np[0]);
                     ready_a = 0;
                     np[0]++;
-                    output(Zero{}, V{}, !kSteady && j == j0, !kSteady && j + 1 == last_a, test_k);
+                    output(Zero{}, V{}, !kSteady && run_begins<kWide, kRuns>(j, j0), !kSteady && j + 1 == last_a, test_k);
                 }
                 if (!ready_k) wait(bars.full[K::value], turn_next);
                 if (next_a) score(Zero{}, K{}, !kSteady && j + 2 == last_a, test_b);
                 if (now_b) {
                     if (!ready_b) wait(bars.p_full[1], np[1]);
                     np[1]++;
-                    output(One{}, V{}, !kSteady && j == j0, !kSteady && j + 1 == last_b, [] {});
+                    output(One{}, V{}, !kSteady && run_begins<kWide, kRuns>(j, j0), !kSteady && j + 1 == last_b, [] {});
                 }
                 release(V::value);
                 if (next_b) score(One{}, K{}, !kSteady && j + 2 == last_b, test_next);
@@ -1004,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 const int steady = min(min(last_a, last_b) - 2, edge);      // blocks j0 + 1 .. steady - 1
                 for (int j = j0; j < j1; j++) {
-                    if (j > j0 && j < steady) {
+                    if (j < steady && !run_begins<kWide, kRuns>(j, j0)) {
                         if (m & 1) block(One{}, One{}, j);
                         else block(Zero{}, One{}, j);
                     } else {
@@ -1212,9 +1289,11 @@ using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
 cudaError_t prompt_attention_config(int sm_count)
 {
     if (sm_count > kPMaxCtas) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(prompt_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
+    for (const auto kernel : {prompt_attention_kernel<false, false>, prompt_attention_kernel<false, true>, prompt_attention_kernel<true, true>}) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynBytes);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // Maps over [token][head][128] tensors: boxes of 64 elements (a 128-byte swizzle
@@ -1258,7 +1337,8 @@ cudaError_t prompt_maps(const PromptArgs &a, const void *q, int64_t q_stride, co
 
 cudaError_t launch_prompt_attention(const PromptArgs &a, const PromptMaps &maps, int sm_count, cudaStream_t s)
 {
-    const auto kernel = a.wide ? prompt_attention_kernel<true> : prompt_attention_kernel<false>;
+    const auto kernel = a.wide ? prompt_attention_kernel<true, true>
+                        : a.n_kv > kRun * kTok ? prompt_attention_kernel<false, true> : prompt_attention_kernel<false, false>;
     const cudaError_t e = launch_maybe_pdl(kernel, dim3(sm_count), dim3(kThreads), kDynBytes, s, true, a, maps);
     if (e != cudaSuccess || a.n_kv <= kTok) return e;       // items of one block are not cut
     const auto merge = a.wide ? prompt_merge_kernel<true> : prompt_merge_kernel<false>;

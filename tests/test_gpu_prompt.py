@@ -341,6 +341,31 @@ def test_refusals():
     assert torch.equal(again[0], good[0])
 
 
+@pytest.mark.parametrize("dtype,m,ramp", [(torch.float32, 32768, 0), (torch.float32, 32768, 2), (BF16, 81920, 0), (BF16, 81920, 2)])
+def test_rows_over_many_keys_lose_nothing_to_the_order_of_sums(dtype, m, ramp):
+    """The tensor cores cut sums off towards 0, which would add up over the hundreds of blocks that an item here has; the sums
+    of runs of them are kept apart, and follow the reference where keys that grow (ramp) move it.  A run has 128 products
+    of two weights (fp32 rows: 8 blocks) or 4096 (bf16: 512), each at most a step of 2^-23 of the sum, half on average: the
+    outputs shrink by at most products 2^-24.  Beside that there are, at random, half a step of the weights (fp32 rows:
+    2^-17, bf16: 2^-9), the scores' rounding (2^-21 in the exponent) and, of bf16 outputs, their own 2^-9."""
+    from kv_cache_computation_gb300 import PromptAttention
+    n, H = 5120, 8
+    q, k, v = (_randn((t, H, 128), 300 + i).cuda() for i, t in enumerate((n, m, m)))
+    k *= (1 + ramp * torch.arange(m).cuda() / m)[:, None, None].to(BF16)
+    attend = PromptAttention(H, H, max_tokens=n)
+    o, _ = attend(q, k, v, _i32([0, n]), _i32([0, m]), lag=64, out_dtype=dtype)
+    rows = torch.arange(17, n, 640).cuda()
+    s = torch.einsum("nhd,mhd->hnm", q[rows].double(), k.double()) / 128 ** 0.5
+    seen = (m - n + 1 - 64 + rows)[:, None] > torch.arange(m).cuda()
+    want = torch.einsum("hnm,mhd->nhd", s.masked_fill(~seen, float("-inf")).softmax(-1), v.double())
+    off = o[rows].double() - want
+    shrinks, own = (128 * 2 ** -24, 2 ** -17) if dtype == torch.float32 else (4096 * 2 ** -24, 2 ** -9 + 2 ** -9)
+    # of random parts the mean over 8 x 8 x 128 elements is left
+    assert ((off * want).sum() / (want * want).sum()).abs() <= shrinks + own / 64
+    assert off.norm() / want.norm() <= shrinks + own + 2 ** -20
+    attend.sync()
+
+
 @pytest.mark.parametrize("dtype,off", [(BF16, 8), (torch.float32, 4), (torch.float32, 12)])
 def test_refuses_outputs_off_their_32_bytes(dtype, off):
     """The rows are stored 32 bytes at a time: an out of the caller's that starts elsewhere is refused on the host."""
