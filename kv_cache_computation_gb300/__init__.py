@@ -18,6 +18,14 @@ attention over it):
     out, lse = QuantKV(32, 8, num_pages=4096, max_batch=B).decode_step_qkv(
         QkvRotary(32, 8), qkv, step.positions, step.slots, page_table, step.lengths, starts=step.starts)
 
+Before the steps: PromptAttention (causal attention of prompts packed behind
+one another, and of chunks behind earlier tokens) and MacAttention.prefill,
+which stores a prompt, attends over it and seeds the ring; BlockKV is a store
+of 8 bits per value with QuantKV's calls:
+
+    prompt = PromptAttention(32, 8, max_tokens=8192)
+    out, lse = mac.prefill(prompt, 0, q_pre_rope, q_post_rope, k, v)
+
 The CUDA library must be built first (``kv_cache_computation_gb300.build``);
 there is no CPU fallback.
 """
