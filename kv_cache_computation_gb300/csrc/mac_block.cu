@@ -35,11 +35,18 @@ namespace {
 
 constexpr int kThreads = 256;
 // Tokens of a call up to which every token's block looks through all slots.  Both
-// sides, us, 8 heads, scan against marks: 256 requests' tokens 3.6 against 8.8,
-// 1000 requests' 7.7 / 17; 1024 tokens in whole pages 13 / 10.
+// sides, us, 8 heads, scan against marks: 256 requests' tokens 3.6 / 8.8, 1000
+// requests' 10.4 / 17; 1024 tokens in whole pages 6.2 / 10; 2048 10.5 / 11.3, but
+// of 2000 requests on one head 10.5 / 6.9.
 constexpr int kScanTokens = 1024;
-constexpr int kMostBlocks = 1024;       // of a call through the marks, while a block takes fewer than 16 tokens
-constexpr int kFewTokens = 4;           // of a page: stored one after another
+// Beyond: blocks that fit an SM at once, so that a call is one wave of them, and at
+// most so many tokens to a block (32768 tokens, us: 16 to a block 42.8, 64 41, of
+// one head 13.7 and 8.4; with registers for three blocks 50, for five 80).
+constexpr int kBlocksPerSm = 4, kMostTokens = 64;
+// Tokens of a page up to which they are stored one after another (1024 tokens in
+// whole pages so 13 us against 6.2 at once, 1000 requests' tokens 7.7 against 10.4
+// where the kernel has both; 8 of them 2.8 either way).
+constexpr int kFewTokens = 4;
 // (token, head) pairs below which a gather's warp takes 4 tokens instead of 16
 // (us: 8 tokens 2.6 against 4.1, 1024 2.7 / 3.7, 8192 10.4 / 10.1, 32768 41 / 37).
 constexpr int kSmallGather = 16384;
@@ -283,9 +290,15 @@ __device__ __forceinline__ void store_page(const BlockMoveArgs &a, const int *to
     }
 }
 
+__device__ __forceinline__ void store(const BlockMoveArgs &a, const int *tokens, uint32_t mask, uint8_t *page, bool is_v, int h)
+{
+    if (__popc(mask) <= kFewTokens) store_tokens(a, tokens, mask, page, is_v, h);
+    else store_page(a, tokens, mask, page, is_v, h);
+}
+
 // Up to kScanTokens tokens: a block per token and eight (head, keys or values),
 // a warp each, which looks through the slots for the others of its page.
-__global__ void __launch_bounds__(kThreads) block_append_scan_kernel(const __grid_constant__ BlockMoveArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_append_scan_kernel(const __grid_constant__ BlockMoveArgs a)
 {
     __shared__ int s_token[kPage];
     __shared__ uint32_t s_mask;
@@ -307,15 +320,15 @@ __global__ void __launch_bounds__(kThreads) block_append_scan_kernel(const __gri
     __syncthreads();
     // the block that has the page's lowest slot stores the page
     if (__ffs(s_mask) - 1 != slot % kPage || s_token[slot % kPage] != (int)blockIdx.x || item >= 2 * Hkv) return;
-    store_tokens(a, s_token, s_mask, a.st.pages + ((size_t)page * Hkv + (item >> 1)) * kBPageBytes, item & 1, item >> 1);
+    store(a, s_token, s_mask, a.st.pages + ((size_t)page * Hkv + (item >> 1)) * kBPageBytes, item & 1, item >> 1);
 }
 
 // More tokens: a block takes the pages whose lowest slot is among its `tokens`
 // consecutive tokens (kept in the marks), and its warps go through their heads'
 // keys and values.
-__global__ void __launch_bounds__(kThreads, 4) block_append_kernel(const __grid_constant__ BlockMoveArgs a, int tokens)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) block_append_kernel(const __grid_constant__ BlockMoveArgs a, int tokens)
 {
-    __shared__ int s_page[kPage], s_token[kPage][kPage], s_pages;
+    __shared__ int s_page[kMostTokens], s_token[kMostTokens][kPage], s_pages;
     const int tid = threadIdx.x, Hkv = a.st.kv_heads;
     if (tid == 0) s_pages = 0;
     __syncthreads();
@@ -344,8 +357,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_append_kernel(const __grid_
         const int i = w / (2 * Hkv), item = w - i * 2 * Hkv, h = item >> 1, lane = tid & 31;
         uint8_t *page = a.st.pages + ((size_t)s_page[i] * Hkv + h) * kBPageBytes;
         const uint32_t mask = __ballot_sync(0xffffffffu, lane < kPage && s_token[i][lane & (kPage - 1)] >= 0);
-        if (__popc(mask) <= kFewTokens) store_tokens(a, s_token[i], mask, page, item & 1, h);
-        else store_page(a, s_token[i], mask, page, item & 1, h);
+        store(a, s_token[i], mask, page, item & 1, h);
     }
 }
 
@@ -627,9 +639,8 @@ mac_status mac_block_append(mac_block_handle h, int n_tokens, const void *dev_k,
     } else {
         e = launch_maybe_pdl(block_mark_kernel, dim3((n_tokens + kThreads - 1) / kThreads), dim3(kThreads), 0,
                              (cudaStream_t)stream, true, a);
-        // few to a block while they may all be of different pages, and no more than one page's where they fill them
         int tokens = 1;
-        while (tokens < kPage && n_tokens / tokens > kMostBlocks) tokens *= 2;
+        while (tokens < kMostTokens && n_tokens / tokens > kBlocksPerSm * h->sm_count) tokens *= 2;
         if (e == cudaSuccess)
             e = launch_maybe_pdl(block_append_kernel, dim3((n_tokens + tokens - 1) / tokens), dim3(kThreads), 0,
                                  (cudaStream_t)stream, true, a, tokens);
