@@ -38,8 +38,9 @@ class PromptAttention:
     gives out 0, lse -inf.  Rows of q that belong to no sequence are not written.
 
     max_tokens query tokens and max_batch sequences per call.  Calls on one
-    object must be ordered with one another (they share its scratch); objects
-    whose calls are ordered may share scratch: pass another as `share`.
+    object must be ordered with one another (they share its scratch, 101 MB
+    whatever the sizes); objects whose calls are ordered may share scratch: pass
+    another as `share`.
     """
 
     def __init__(self, heads, kv_heads, max_tokens, max_batch=1, head_dim=128, sm_scale=0.0, device=None, share=None):
@@ -98,15 +99,17 @@ class PromptAttention:
         sp = _dev(starts, "starts", torch.int32, (B + 1,), dev)
         kst = None if k_starts is None else _dev(k_starts, "k_starts", torch.int32, (B + 1,), dev)
         shape = (n, self.heads, self.head_dim)
+        op = None if out is None else _dev(out, "out", out_dtype, shape, dev)
+        lp = None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1], dev)
         with _on(dev, stream):
             if out is None:
                 out = _out(shape, dev, out_dtype)
+                op = out.data_ptr()
             if lse is None and want_lse:
                 lse = _out(shape[:-1], dev, torch.float32)
-            status = N.lib().mac_prompt_attention(
-                self._h, B, n, m, lag, qp, qs, kp, ks, vp, vs, sp, kst, _dev(out, "out", out_dtype, shape, dev),
-                int(out_dtype == torch.float32),
-                None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1], dev), _stream_ptr(stream, dev))
+                lp = lse.data_ptr()
+            status = N.lib().mac_prompt_attention(self._h, B, n, m, lag, qp, qs, kp, ks, vp, vs, sp, kst, op,
+                                                  int(out_dtype == torch.float32), lp, _stream_ptr(stream, dev))
         if status:
             _check("mac_prompt_attention", status, self._h)
         return out, lse

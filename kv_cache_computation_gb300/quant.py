@@ -115,15 +115,16 @@ class _PagedStore:
         qp = _dev(q, "q", torch.bfloat16, shape, self.device)
         table, row, cols = _table(page_table, B, self.device)
         lp = _dev(lengths, "lengths", torch.int32, (B,), self.device)
+        op = None if out is None else _dev(out, "out", torch.bfloat16, shape, self.device)
+        zp = None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1], self.device)
         with _on(self.device, stream):
             if out is None:
                 out = _out(shape, self.device)
+                op = out.data_ptr()
             if lse is None and want_lse:
                 lse = _out(shape[:-1], self.device, torch.float32)
-            self._call("attention", self._h, B, nq, qp, table, row, cols, lp,
-                       _dev(out, "out", torch.bfloat16, shape, self.device),
-                       None if lse is None else _dev(lse, "lse", torch.float32, shape[:-1], self.device),
-                       _stream_ptr(stream, self.device))
+                zp = lse.data_ptr()
+            self._call("attention", self._h, B, nq, qp, table, row, cols, lp, op, zp, _stream_ptr(stream, self.device))
         return out, lse
 
     def decode_step_qkv(self, rotary, qkv, positions, slots, page_table, lengths, q_weight=None, k_weight=None,
