@@ -200,7 +200,7 @@ mac_status mac_prompt_attention(mac_prompt_handle h, int batch, int n_q, int n_k
     if (q_stride % 8 || k_stride % 8 || v_stride % 8) return refuse(h);
     // blocks of keys per SM, at most: the split of the work counts them in 32 bits
     const int64_t items = ((int64_t)n_q / (2 * h->args.tile_tokens) + batch) * c.kv_heads;
-    if ((items / h->sm_count + 1) * ((int64_t)n_kv / 128 + 1) > (1ll << 30)) return refuse(h, "more work than a call may hold");
+    if ((items / h->sm_count + 1) * ((int64_t)n_kv / 128 + 1 + kPExtra) > (1ll << 30)) return refuse(h, "more work than a call may hold");
     PromptArgs a = h->args;
     a.batch = batch;
     a.lag = lag;

@@ -1,5 +1,5 @@
 """A restatement of the prompt attention kernel's work split, for the tests."""
-TOK = 128
+TOK, EXTRA = 128, 4
 
 
 def seen(n, m, lag, i):
@@ -21,7 +21,7 @@ def items(seqs, G, Hkv, lag):
 
 
 def cost(it):
-    return max(it[3], it[4], 1)
+    return EXTRA + max(it[3], it[4], 1)
 
 
 def split(its, grid):
@@ -44,6 +44,11 @@ def split(its, grid):
     for x in load:
         quota.append(min(at, total))
         at = min(at + max(hi - x, 0), total)
+    # a bound among an item's extra blocks, or behind them, moves to its beginning
+    for c, q in enumerate(quota):
+        start = max((p for p in pre[:-1] if p <= q), default=0)
+        if q < total and q - start <= EXTRA:
+            quota[c] = start
     return rounds, load, pre, quota + [total]
 
 
@@ -65,7 +70,7 @@ def walk(its, grid, c, sp):
         begins, ends = start >= at, stop <= end
         j0, j1, slot = 0, max(it[3], it[4]), -1
         if not (begins and ends):
-            slot, j0, j1 = (1 if begins else 0), at - start, min(j1, end - start)
+            slot, j0, j1 = (1 if begins else 0), max(at - start - EXTRA, 0), min(j1, end - start - EXTRA)
         yield rounds * grid + k, j0, j1, slot
         at = min(stop, end)
         k += 1

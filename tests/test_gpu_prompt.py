@@ -360,8 +360,10 @@ def test_rows_over_many_keys_lose_nothing_to_the_order_of_sums(dtype, m, ramp):
     want = torch.einsum("hnm,mhd->nhd", s.masked_fill(~seen, float("-inf")).softmax(-1), v.double())
     off = o[rows].double() - want
     shrinks, own = (128 * 2 ** -24, 2 ** -17) if dtype == torch.float32 else (4096 * 2 ** -24, 2 ** -9 + 2 ** -9)
-    # of random parts the mean over 8 x 8 x 128 elements is left
-    assert ((off * want).sum() / (want * want).sum()).abs() <= shrinks + own / 64
+    # A weight's rounding is one for all 128 elements of its row, so where one key has most of the weight the random parts
+    # are 64 numbers, one per row and head, within +-own: their mean has a deviation of own / 3^0.5 / 64^0.5 = own / 13.9,
+    # and own / 4 is 3.5 of those.
+    assert ((off * want).sum() / (want * want).sum()).abs() <= shrinks + own / 4
     assert off.norm() / want.norm() <= shrinks + own + 2 ** -20
     attend.sync()
 

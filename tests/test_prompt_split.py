@@ -40,12 +40,12 @@ def test_every_block_once_and_level_loads(grid):
         for c in range(grid):
             w = 0
             for i, j0, j1, slot in S.walk(its, grid, c, sp):
-                assert 0 <= j0 <= j1
+                assert 0 <= j0 <= j1 and (slot < 0 or j0 < j1)
                 done.setdefault(i, []).append((j0, j1, c, slot))
                 if slot >= 0:
                     assert (c, slot) not in slots           # one partial per CTA and slot
                     slots[c, slot] = i
-                w += max(j1 - j0, 1)
+                w += max(j1 - j0, 1) + (S.EXTRA if j0 == 0 else 0)
             work.append(w)
         assert sorted(done) == list(range(len(its)))
         merged = S.spans(its, grid, sp)
@@ -62,4 +62,5 @@ def test_every_block_once_and_level_loads(grid):
                 # a CTA between them without a share says so itself
                 assert set(range(first, last + 1)) - {x[2] for x in parts} <= {c for c in range(grid) if quota[c] == quota[c + 1]}
         if max(load) * grid <= sum(load) + pre[-1]:
-            assert max(work) - sum(work) / grid <= 1 + (max(work) - min(work) > 1)
+            # a share may pass the level by a block, and by the extra blocks that moved to it
+            assert max(work) - sum(work) / grid <= 2 + S.EXTRA
