@@ -123,6 +123,7 @@ mac_status mac_prompt_create(const mac_prompt_config *cfg, void *dev_scratch, si
     a.kv_heads = cfg->kv_heads;
     a.G = cfg->heads / cfg->kv_heads;
     a.tile_tokens = 128 / a.G;
+    a.pair_inverse = (uint32_t)(((1ull << 32) + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens));
     const double scale = cfg->sm_scale > 0.f ? (double)cfg->sm_scale : 1.0 / std::sqrt((double)kD);
     a.scale_log2 = (float)(scale * 1.4426950408889634);
     a.err = (uint32_t *)(sc + z.err);

@@ -7,10 +7,11 @@ namespace macgpu {
 
 constexpr int kPMaxBatch = 1024;        // sequences per call (their item counts stand in shared memory)
 constexpr int kPMaxGroup = 128;         // query heads per KV head: a tile has at least one token
+constexpr int kPLevels = 2048;          // levels by which items are ordered: of a block each up to 262144 keys
 constexpr int kPMaxCtas = 256;          // upper bound of the grid (one CTA per SM)
 constexpr int kPRows = 256;             // query rows of an item: two tiles of 128
 // Items per CTA, at least, in the line of blocks that is cut (more of them: items beside one another go to one CTA, and 5
-// prompts of 1 .. 6001 tokens take 269 us with two, 284 with four instead of 262).
+// prompts of 1 .. 6001 tokens took 269 us with two, 284 with four instead of 262).
 constexpr int kPLineRows = 1;
 // Blocks that an item counts besides its own in the split of the work: a piece costs 7000 to 10000 cycles whatever its
 // length, a block 2400 to 2700.  us with 0, 2, 4 and 5: 6001 tokens of 28 / 4 heads 235, 217, 209, 207; of 32 / 8 heads 311,
@@ -28,6 +29,7 @@ struct PromptMeta {
 
 struct PromptArgs {
     int heads, kv_heads, G, tile_tokens;    // tile_tokens: 128 / G query tokens to a tile of 128 rows
+    uint32_t pair_inverse;                  // 2^32 / (2 tile_tokens), rounded up
     int batch, lag;
     int n_q, n_kv;                          // tokens of q and of k, v
     const int32_t *starts, *k_starts;

@@ -27,12 +27,14 @@
 // the output is fp32, P is a bf16 pair hi + lo (2^-17 of each weight) and O += P_hi
 // V + P_lo V, in runs of eight blocks (kWideRun).
 //
-// Work split.  Items are numbered sequence by sequence, tile by tile from the
-// last (longest) on, head by head.  With R + 1 or more items per CTA, a CTA takes
-// R whole items, one from each row of `grid` items (back and forth, so that lengths
-// even out), and what is left, one to two rows, is one line of blocks that is cut
-// so that all CTAs end together (an item counts kPExtra blocks besides its own); an item that is cut is merged by a second kernel
-// (there is none where no sequence has more than a block of keys).
+// Work split.  Items are numbered from those of the most key blocks down, over all
+// sequences.  With R + 1 or more items per CTA, a CTA takes R whole items, one from
+// each row of `grid` items (back and forth, so that lengths even out), and what is
+// left, one to two rows, is one line of blocks that is cut so that all CTAs end
+// together (an item counts kPExtra blocks besides its own); an item that is cut is
+// merged by a second kernel (there is none where no sequence has more than a block of
+// keys).  Numbered sequence by sequence, 24 ragged prompts took 452 us instead of 427,
+// 5 with 28 / 4 heads 257 instead of 240: the whole items' loads differed by up to 13 %.
 // Everything follows from the lengths on the device, in each CTA's prologue: a
 // captured call serves other lengths, and a call repeats bit for bit.
 //
@@ -52,8 +54,8 @@
 // Measured (graph replays; 32 / 8 heads but where noted; 1965 TFLOP/s is the
 // library's largest product's rate): 32768 tokens 5.25 ms (1675 TFLOP/s of the
 // products that the causal edge leaves), 6001 tokens 255 us (1340), 2048 and 509
-// tokens behind 30720 and 8191 688 us (1650), 24 ragged prompts of 1 .. 4096 tokens
-// 450 us (1210), 5 of 1 .. 6001 with 28 / 4 heads 258 us (1160), 512 fp32 rows behind
+// tokens behind 30720 and 8191 690 us (1645), 24 ragged prompts of 1 .. 4096 tokens
+// 427 us (1275), 5 of 1 .. 6001 with 28 / 4 heads 240 us (1245), 512 fp32 rows behind
 // 32256 298 us (913; with the second P V 1370), 16 tokens 10.7 to 12.4 us.
 // What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
 // from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
@@ -292,54 +294,92 @@ struct Piece {
 };
 
 struct Split {
-    int pre[kPMaxBatch + 1];    // items of the sequences before b
+    int2 seq[kPMaxBatch];       // of a sequence its queries n, and m - n - lag
+    int above[kPLevels + 1];    // items of level k and more; a level is 2^shift blocks of an item
+    int before[kPMaxBatch + 1]; // items of one level of the sequences before b: of the level that item_at met last
     int scan[2][kThreads / 32];
     int cost[(kPLineRows + 1) * kPMaxCtas];     // prefix of the blocks of the items of the line
     int load[kPMaxCtas];        // blocks that the CTAs do in whole items
     int quota[kPMaxCtas + 1];   // where the CTAs' shares of the line begin
+    int top, shift, levels;
     int rounds, line_items, line_blocks;
 };
 
-// The last b with pre[b] <= i: item i's sequence.
-__device__ __forceinline__ int sequence_of(const PromptArgs &a, const Split &sp, int i)
+// x / (2 tile_tokens), x up to 2^24 and a tile more.
+__device__ __forceinline__ int pairs_of(const PromptArgs &a, int x) { return (int)__umulhi((uint32_t)x, a.pair_inverse); }
+
+// The following take of a sequence its queries n (x) and m - n - lag (y).
+__device__ __forceinline__ int tiles_of(const PromptArgs &a, int2 s) { return pairs_of(a, s.x + 2 * a.tile_tokens - 1); }
+
+// Key blocks that the tokens up to `token` (inclusive) of a sequence see.
+__device__ __forceinline__ int blocks_seen(int2 s, int token) { return (max(s.y + token + 1, 0) + kTok - 1) / kTok; }
+
+// Blocks of keys of an item, of its longer tile; one that sees no key still has its output to write.
+__device__ __forceinline__ int item_blocks(const PromptArgs &a, int2 s, int tile)
 {
-    int lo = 0, hi = a.batch;
+    return max(blocks_seen(s, min((tile + 1) * 2 * a.tile_tokens, s.x) - 1), 1);
+}
+
+// Tiles of a sequence whose items have at least so many blocks: its last ones.
+__device__ __forceinline__ int tiles_from(const PromptArgs &a, int2 s, int blocks)
+{
+    const int tiles = tiles_of(a, s);
+    if (blocks <= 1) return tiles;
+    const int need = (blocks - 1) * kTok + 1 - s.y;     // tokens up to the first whose block that is
+    if (need > s.x) return 0;
+    return need <= 0 ? tiles : tiles - pairs_of(a, need - 1);
+}
+
+// The level of item `i`: the last one with more than i items of it and above.
+__device__ __forceinline__ int level_of(const Split &sp, int i)
+{
+    int lo = 0, hi = sp.levels;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (sp.pre[mid] <= i) lo = mid;
+        if (sp.above[mid] > i) lo = mid;
         else hi = mid;
     }
     return lo;
 }
 
-__device__ __forceinline__ int tiles_of(const PromptArgs &a, const Seq &s)
+// Item `i` of the call, by a whole warp: items go by levels from the highest down, in a level by sequences, tiles from the
+// last down, and heads.  met: the level of sp.before, or -1.
+__device__ __forceinline__ Piece item_at(const PromptArgs &a, Split &sp, int i, int &met)
 {
-    return (uint32_t)(s.n + 2 * a.tile_tokens - 1) / (uint32_t)(2 * a.tile_tokens);
-}
-
-// Key blocks that the tokens up to `token` (inclusive) of a sequence see.
-__device__ __forceinline__ int blocks_seen(const PromptArgs &a, const Seq &s, int token)
-{
-    return (min(max(s.m - s.n - a.lag + token + 1, 0), s.m) + kTok - 1) / kTok;
-}
-
-// Work of an item in blocks, kPExtra among them for what a piece costs besides its own; one that sees no key still has
-// its output to write.
-__device__ __forceinline__ int item_cost(const PromptArgs &a, const Seq &s, int tile)
-{
-    return kPExtra + max(blocks_seen(a, s, min((tile + 1) * 2 * a.tile_tokens, s.n) - 1), 1);
-}
-
-// Item `i` of the call.
-__device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, int i)
-{
-    Piece p;
-    p.seq = sequence_of(a, sp, i);
-    const Seq s = sequence(a, p.seq, false);
-    const uint32_t in = i - sp.pre[p.seq], down = in / (uint32_t)a.kv_heads;
+    const int lane = threadIdx.x & 31, level = level_of(sp, i), low = level << sp.shift, high = (level + 1) << sp.shift;
+    if (level != met) {
+        met = level;
+        int all = 0;
+        __syncwarp();
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            const int2 q = b0 + lane < a.batch ? sp.seq[b0 + lane] : make_int2(0, 0);
+            const int own = (tiles_from(a, q, low) - tiles_from(a, q, high)) * a.kv_heads;
+            int x = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b0 + lane < a.batch) sp.before[b0 + lane] = all + x - own;
+            all += __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+    }
+    const int place = i - sp.above[level + 1];
+    int b = 0, end = a.batch;           // the last b with before[b] <= place
+    while (end - b > 1) {
+        const int mid = (b + end) >> 1;
+        if (sp.before[mid] <= place) b = mid;
+        else end = mid;
+    }
+    const Seq s = sequence(a, b, false);
+    const int2 q = sp.seq[b];
+    const uint32_t in = place - sp.before[b], down = in / (uint32_t)a.kv_heads;
     const int T = a.tile_tokens;
+    Piece p;
+    p.seq = b;
     p.head = in - down * a.kv_heads;
-    p.tile = tiles_of(a, s) - 1 - down;
+    p.tile = tiles_of(a, q) - 1 - tiles_from(a, q, high) - down;
     const int tok0 = 2 * p.tile * T, ta = min(T, s.n - tok0), tb = max(min(T, s.n - tok0 - T), 0);  // the item exists: ta >= 1
     p.row0 = s.q0 + tok0;
     p.key0 = s.k0;
@@ -347,8 +387,8 @@ __device__ __forceinline__ Piece item_at(const PromptArgs &a, const Split &sp, i
     p.first_seen = s.m - s.n - a.lag + tok0 + 1;
     p.rows_a = ta * a.G;
     p.rows_b = tb * a.G;
-    p.nblk_a = blocks_seen(a, s, tok0 + ta - 1);
-    p.nblk_b = tb > 0 ? blocks_seen(a, s, tok0 + T + tb - 1) : 0;
+    p.nblk_a = blocks_seen(q, tok0 + ta - 1);
+    p.nblk_b = tb > 0 ? blocks_seen(q, tok0 + T + tb - 1) : 0;
     p.edge = p.seen(0) / kTok;
     p.j0 = 0;
     p.j1 = max(p.nblk_a, p.nblk_b);
@@ -392,62 +432,75 @@ __device__ __forceinline__ int item_of(const Split &sp, int at)
     return lo;
 }
 
-// The whole split, by all threads of the CTA.  known: room for the sequences.
-__device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *known)
+// Blocks of item `i`, for one thread.
+__device__ __forceinline__ int blocks_at(const PromptArgs &a, const Split &sp, int i)
+{
+    const int level = level_of(sp, i);
+    if (sp.shift == 0) return level;
+    int in = i - sp.above[level + 1];
+    for (int b = 0;; b++) {
+        const int above = tiles_from(a, sp.seq[b], (level + 1) << sp.shift);
+        const int own = (tiles_from(a, sp.seq[b], level << sp.shift) - above) * a.kv_heads;
+        if (in < own) return item_blocks(a, sp.seq[b], tiles_of(a, sp.seq[b]) - 1 - above - in / a.kv_heads);
+        in -= own;
+    }
+}
+
+// The whole split, by all threads of the CTA.
+__device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
 {
     const int tid = threadIdx.x, grid = gridDim.x;
-    int items = 0, turn = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        int own = 0, all;
-        if (b < a.batch) {
-            const Seq s = sequence(a, b, blockIdx.x == 0);
-            known[b] = s;
-            own = tiles_of(a, s) * a.kv_heads;
-        }
-        const int at = block_scan(sp, own, &all, turn);
-        if (b < a.batch) sp.pre[b] = items + at;
-        items += all;
-    }
-    if (tid == 0) sp.pre[a.batch] = items;
-    if (tid < kPMaxCtas) sp.load[tid] = 0;
+    int turn = 0;
+    if (tid == 0) sp.top = 0;
     __syncthreads();
-    const int rounds = max(items / grid - kPLineRows, 0), first = rounds * grid, line = items - first;
-    // Blocks of the whole items: a thread goes through consecutive items, one search for all of them.
-    const int per = (first + kThreads - 1) / kThreads, stop = min(first, (tid + 1) * per);
-    if (tid * per < stop) {
-        int i = tid * per, b = sequence_of(a, sp, i), r = i / grid, at = i - r * grid;
-        Seq s = known[b];
-        int in = i - sp.pre[b], down = in / a.kv_heads, head = in - down * a.kv_heads, tile = tiles_of(a, s) - 1 - down;
-        int cost = item_cost(a, s, tile);
-#pragma unroll 1
-        for (; i < stop; i++) {
-            atomicAdd(&sp.load[r & 1 ? grid - 1 - at : at], cost);
-            if (++at == grid) {
-                at = 0;
-                r++;
-            }
-            if (++head < a.kv_heads || i + 1 == stop) continue;
-            head = 0;
-            if (--tile < 0) {
-                do s = known[++b];
-                while (s.n == 0);       // there is another item, so another sequence with queries
-                tile = tiles_of(a, s) - 1;
-            }
-            cost = item_cost(a, s, tile);
+    for (int b = tid; b < a.batch; b += kThreads) {
+        const Seq s = sequence(a, b, blockIdx.x == 0);
+        const int2 q = make_int2(s.n, s.m - s.n - a.lag);
+        sp.seq[b] = q;
+        if (s.n > 0) atomicMax(&sp.top, item_blocks(a, q, tiles_of(a, q) - 1));
+    }
+    __syncthreads();
+    const int top = sp.top;
+    int shift = 0;
+    while (top >> shift >= kPLevels) shift++;
+    const int levels = (top >> shift) + 1;
+    if (levels > 4 * a.batch) {         // a thread to a level, or, with many sequences, a warp (1024 of 16 tokens: 302 -> 262 us)
+        for (int k = tid; k <= levels; k += kThreads) {
+            int tiles = 0;
+            for (int b = 0; b < a.batch; b++) tiles += tiles_from(a, sp.seq[b], k << shift);
+            sp.above[k] = tiles * a.kv_heads;
         }
+    } else {
+        for (int k = tid >> 5; k <= levels; k += kThreads / 32) {
+            int tiles = 0;
+            for (int b = tid & 31; b < a.batch; b += 32) tiles += tiles_from(a, sp.seq[b], k << shift);
+            tiles = __reduce_add_sync(0xffffffffu, tiles);
+            if ((tid & 31) == 0) sp.above[k] = tiles * a.kv_heads;
+        }
+    }
+    if (tid == 0) {
+        sp.shift = shift;
+        sp.levels = levels;
+    }
+    __syncthreads();
+    const int items = sp.above[0], rounds = max(items / grid - kPLineRows, 0), first = rounds * grid, line = items - first;
+    // blocks of the whole items (where levels are coarse: about)
+    if (tid < kPMaxCtas) {
+        int load = 0;
+        if (tid < grid)
+            for (int r = 0, k = levels - 1; r < rounds; r++) {
+                const int i = r * grid + (r & 1 ? grid - 1 - tid : tid);
+                while (sp.above[k] <= i) k--;
+                load += (k << shift) + kPExtra;
+            }
+        sp.load[tid] = load;
     }
     // blocks of the line
     int total = 0;
     for (int i0 = 0; i0 < line; i0 += kThreads) {
         const int i = i0 + tid;
-        int all, own = 0;
-        if (i < line) {
-            const int b = sequence_of(a, sp, first + i);
-            const Seq s = known[b];
-            own = item_cost(a, s, tiles_of(a, s) - 1 - (int)((uint32_t)(first + i - sp.pre[b]) / (uint32_t)a.kv_heads));
-        }
-        const int at = block_scan(sp, own, &all, turn);
+        int all;
+        const int own = i < line ? blocks_at(a, sp, first + i) + kPExtra : 0, at = block_scan(sp, own, &all, turn);
         if (i < line) sp.cost[i] = total + at;
         total += all;
     }
@@ -517,7 +570,8 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp, Seq *
 // A CTA's pieces, one after another: first its whole items, then its share of
 // the line.
 struct Walk {
-    int round, item, at, end;
+    int round, item, at, end, met = -1;
+    PromptMeta meta{-1, 0, 0, 0, 0, {0, 0, 0}};     // the item that begins in this CTA's share and runs on behind it
     __device__ __forceinline__ Walk(const Split &sp)
     {
         round = 0;
@@ -525,20 +579,25 @@ struct Walk {
         end = sp.quota[blockIdx.x + 1];
         item = item_of(sp, at);
     }
-    __device__ __forceinline__ Piece next(const PromptArgs &a, const Split &sp)
+    __device__ __forceinline__ Piece next(const PromptArgs &a, Split &sp)
     {
         const int grid = gridDim.x;
         Piece p;
         p.seq = -1;
         if (round < sp.rounds) {
-            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x));
+            p = item_at(a, sp, round * grid + (round & 1 ? grid - 1 - blockIdx.x : blockIdx.x), met);
             round++;
         } else if (at < end) {
-            p = item_at(a, sp, sp.rounds * grid + item);
+            p = item_at(a, sp, sp.rounds * grid + item, met);
             const int start = sp.cost[item], stop = start + kPExtra + max(p.j1, 1);
             const bool begins = start >= at, ends = stop <= end;
             if (!begins || !ends) {
                 p.slot = begins ? 1 : 0;
+                if (begins) {
+                    int c = blockIdx.x;
+                    while (sp.quota[c + 1] < stop) c++;
+                    meta = PromptMeta{p.seq, p.head, p.tile, (int)blockIdx.x, c, {0, 0, 0}};
+                }
                 p.j0 = max(at - start - kPExtra, 0);
                 p.j1 = min(p.j1, end - start - kPExtra);
             }
@@ -825,9 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     const uint32_t tmem = 0;            // all 512 columns: the allocation starts at column 0
     if (tid == 0 && s_tmem != 0) s_fail = 1;
     pdl_wait();
-    make_split(a, sp, reinterpret_cast<Seq *>(base));
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");      // copies will land where the sequences stood
-    __syncthreads();
+    make_split(a, sp);
 
     Follow follow{queue, bars, fail};
     if (warp < 8) {
@@ -1211,25 +1268,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
                 if (p.seq < 0) break;
             }
+            if (lane == 0) a.meta[blockIdx.x] = walk.meta;      // for the second kernel
         }
     }
 
-    // the item that begins in this CTA's share and runs on behind it, for the second kernel
-    if (tid == kLoadWarp * 32) {
-        const int lo = sp.quota[blockIdx.x], hi = sp.quota[blockIdx.x + 1], grid = gridDim.x;
-        PromptMeta m{-1, 0, 0, 0, 0, {0, 0, 0}};
-        if (lo < hi) {
-            const int i = item_of(sp, hi - 1);
-            const int stop = i + 1 < sp.line_items ? sp.cost[i + 1] : sp.line_blocks;
-            if (sp.cost[i] >= lo && stop > hi) {
-                const Piece q = item_at(a, sp, sp.rounds * grid + i);
-                int c = blockIdx.x;
-                while (sp.quota[c + 1] < stop) c++;
-                m = PromptMeta{q.seq, q.head, q.tile, (int)blockIdx.x, c, {0, 0, 0}};
-            }
-        }
-        a.meta[blockIdx.x] = m;
-    }
     __syncthreads();
     if (*fail && tid == 0) atomicOr(a.err, kPErrTimeout);
     fence_before();

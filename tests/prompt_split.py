@@ -7,7 +7,7 @@ def seen(n, m, lag, i):
 
 
 def items(seqs, G, Hkv, lag):
-    """Items in order: (sequence, head, tile, blocks of tile A, of tile B, first block on the edge)."""
+    """Items in order, from those of the most blocks down: (sequence, head, tile, blocks of tile A, of tile B, first block on the edge)."""
     T, out = 128 // G, []
     for b, (n, m) in enumerate(seqs):
         for tile in reversed(range(-(-n // (2 * T)))):
@@ -17,7 +17,7 @@ def items(seqs, G, Hkv, lag):
                 nblk.append(-(-seen(n, m, lag, (2 * tile + x) * T + t - 1) // TOK) if t > 0 else 0)
             edge = seen(n, m, lag, 2 * tile * T) // TOK
             out += [(b, h, tile, nblk[0], nblk[1], edge) for h in range(Hkv)]
-    return out
+    return sorted(out, key=lambda it: -cost(it))
 
 
 def cost(it):

@@ -341,6 +341,13 @@ def test_refusals():
     assert torch.equal(again[0], good[0])
 
 
+def test_more_keys_than_levels():
+    """Sequences of more blocks than the split has levels to order its items by, beside short ones."""
+    c = Case([(40, 300001), (100, 100), (3, 262200), (1, 5), (70, 270000), (0, 9)], 4, 2, seed=77)
+    c.check(*c.run())
+    c.attend.sync()
+
+
 @pytest.mark.parametrize("dtype,m,ramp", [(torch.float32, 32768, 0), (torch.float32, 32768, 2), (BF16, 81920, 0), (BF16, 81920, 2)])
 def test_rows_over_many_keys_lose_nothing_to_the_order_of_sums(dtype, m, ramp):
     """The tensor cores cut sums off towards 0, which would add up over the hundreds of blocks that an item here has; the sums
