@@ -626,7 +626,8 @@ mac_status mac_prompt_destroy(mac_prompt_handle h);
  *   dev_starts    int32 [batch + 1], 0 <= starts[b] <= starts[b + 1] <= n_q
  *   dev_k_starts  int32 [batch + 1] likewise up to n_kv, or NULL: starts.  A
  *                 sequence whose starts are not so is left out, which
- *                 mac_prompt_sync reports
+ *                 mac_prompt_sync reports (all are, where starts go back so
+ *                 often that sequences share many of their rows)
  *   dev_out       [n_q][heads][128], bf16, or fp32 where out_fp32 is 1; 32-byte
  *                 aligned
  *   dev_lse       fp32 [n_q][heads], or NULL

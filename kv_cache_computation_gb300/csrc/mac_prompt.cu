@@ -200,13 +200,15 @@ mac_status mac_prompt_attention(mac_prompt_handle h, int batch, int n_q, int n_k
         return refuse(h);
     if (q_stride % 8 || k_stride % 8 || v_stride % 8) return refuse(h);
     // blocks of keys per SM, at most: the split of the work counts them in 32 bits
-    const int64_t items = ((int64_t)n_q / (2 * h->args.tile_tokens) + batch) * c.kv_heads;
+    const int most_tiles = n_q / (2 * h->args.tile_tokens) + batch;
+    const int64_t items = (int64_t)most_tiles * c.kv_heads;
     if ((items / h->sm_count + 1) * ((int64_t)n_kv / 128 + 1 + kPExtra) > (1ll << 30)) return refuse(h, "more work than a call may hold");
     PromptArgs a = h->args;
     a.batch = batch;
     a.lag = lag;
     a.n_q = n_q;
     a.n_kv = n_kv;
+    a.most_tiles = most_tiles;
     a.starts = dev_starts;
     a.k_starts = dev_k_starts ? dev_k_starts : dev_starts;
     a.out = dev_out;

@@ -32,6 +32,7 @@ struct PromptArgs {
     uint32_t pair_inverse;                  // 2^32 / (2 tile_tokens), rounded up
     int batch, lag;
     int n_q, n_kv;                          // tokens of q and of k, v
+    int most_tiles;                         // pairs of tiles that `batch` sequences of n_q tokens together can have
     const int32_t *starts, *k_starts;
     void *out;                              // bf16, or fp32 where wide
     int wide;

@@ -301,6 +301,7 @@ struct Split {
     int cost[(kPLineRows + 1) * kPMaxCtas];     // prefix of the blocks of the items of the line
     int load[kPMaxCtas];        // blocks that the CTAs do in whole items
     int quota[kPMaxCtas + 1];   // where the CTAs' shares of the line begin
+    unsigned long long tiles;   // of all sequences
     int top, shift, levels;
     int rounds, line_items, line_blocks;
 };
@@ -451,16 +452,26 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
 {
     const int tid = threadIdx.x, grid = gridDim.x;
     int turn = 0;
-    if (tid == 0) sp.top = 0;
+    if (tid == 0) {
+        sp.top = 0;
+        sp.tiles = 0;
+    }
     __syncthreads();
     for (int b = tid; b < a.batch; b += kThreads) {
         const Seq s = sequence(a, b, blockIdx.x == 0);
         const int2 q = make_int2(s.n, s.m - s.n - a.lag);
         sp.seq[b] = q;
-        if (s.n > 0) atomicMax(&sp.top, item_blocks(a, q, tiles_of(a, q) - 1));
+        if (s.n > 0) {
+            atomicMax(&sp.top, item_blocks(a, q, tiles_of(a, q) - 1));
+            atomicAdd(&sp.tiles, (unsigned long long)tiles_of(a, q));
+        }
     }
     __syncthreads();
-    const int top = sp.top;
+    // More tiles than sequences behind one another can have: starts that go back, with other sequences on the same rows.
+    // Nothing is done then; counts that fit 32 bits would not be sure.
+    const bool none = sp.tiles > (unsigned long long)a.most_tiles;
+    if (none && tid == 0 && blockIdx.x == 0) atomicOr(a.err, kPErrStarts);
+    const int top = none ? 0 : sp.top;
     int shift = 0;
     while (top >> shift >= kPLevels) shift++;
     const int levels = (top >> shift) + 1;
@@ -468,14 +479,14 @@ __device__ __forceinline__ void make_split(const PromptArgs &a, Split &sp)
         for (int k = tid; k <= levels; k += kThreads) {
             int tiles = 0;
             for (int b = 0; b < a.batch; b++) tiles += tiles_from(a, sp.seq[b], k << shift);
-            sp.above[k] = tiles * a.kv_heads;
+            sp.above[k] = none ? 0 : tiles * a.kv_heads;
         }
     } else {
         for (int k = tid >> 5; k <= levels; k += kThreads / 32) {
             int tiles = 0;
             for (int b = tid & 31; b < a.batch; b += 32) tiles += tiles_from(a, sp.seq[b], k << shift);
             tiles = __reduce_add_sync(0xffffffffu, tiles);
-            if ((tid & 31) == 0) sp.above[k] = tiles * a.kv_heads;
+            if ((tid & 31) == 0) sp.above[k] = none ? 0 : tiles * a.kv_heads;
         }
     }
     if (tid == 0) {

@@ -269,6 +269,25 @@ def test_bad_starts_are_reported_and_left_out(starts, k_starts, bad):
             assert (out[60:] == 9.0).all()
 
 
+def test_starts_that_go_back_again_and_again():
+    """Sequences that share nearly all their rows, between others that are left out: more tiles than the call's tokens can
+    have.  Nothing is written, it is reported, and the next call is as ever."""
+    from kv_cache_computation_gb300 import MacError, PromptAttention
+    n, B = 1000, 201
+    q, k, v = _randn((n, 8, 128), 5), _randn((n, 2, 128), 6), _randn((n, 2, 128), 7)
+    attend = PromptAttention(8, 2, max_tokens=n, max_batch=B)
+    out, lse = torch.full_like(q, 9.0), torch.full((n, 8), 9.0, device="cuda")
+    attend(q, k, v, _i32([0, n] * 101), out=out, lse=lse)
+    with pytest.raises(MacError, match="starts"):
+        attend.sync()
+    assert (out == 9.0).all() and (lse == 9.0).all()
+    one = attend(q, k, v, _i32([0, n]))
+    attend.sync()
+    o, l, mag, top = _reference(q, k, v, 0, 128 ** -0.5)
+    to, tl = _tolerance(o, mag, top, l, n, False)
+    assert ((one[0].double() - o).abs() <= to).all() and ((one[1].double() - l).abs() <= tl).all()
+
+
 def test_reproducible_captured_other_stream_and_shared_scratch():
     """Two runs agree bit for bit; a captured call serves other lengths, tokens and sequences when replayed; objects that
     share a scratch do not disturb one another."""
