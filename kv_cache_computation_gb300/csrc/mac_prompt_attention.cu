@@ -52,11 +52,12 @@
 // a tile's Q, S, P and O are filled again only after their reader has passed on.
 //
 // Measured (graph replays; 32 / 8 heads but where noted; 1965 TFLOP/s is the
-// library's largest product's rate): 32768 tokens 5.25 ms (1675 TFLOP/s of the
-// products that the causal edge leaves), 6001 tokens 255 us (1340), 2048 and 509
-// tokens behind 30720 and 8191 690 us (1645), 24 ragged prompts of 1 .. 4096 tokens
-// 427 us (1275), 5 of 1 .. 6001 with 28 / 4 heads 240 us (1245), 512 fp32 rows behind
-// 32256 298 us (913; with the second P V 1370), 16 tokens 10.7 to 12.4 us.
+// library's largest product's rate): 32768 tokens 4.95 ms, 5.42 one after another
+// (1775 and 1620 TFLOP/s of the products that the causal edge leaves), 6001 tokens
+// 250 us (1370), 2048 and 509 tokens behind 30720 and 8191 685 us (1660), 24 ragged
+// prompts of 1 .. 4096 tokens 414 us (1315), 5 of 1 .. 6001 with 28 / 4 heads 233 us
+// (1285), 512 fp32 rows behind 32256 290 to 310 us (910; with the second P V 1365),
+// 16 tokens 10.7 to 12.4 us.
 // What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
 // from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
 // ex2 at 32 a cycle and SM, loads and stores of tensor memory, maximum and packing;
@@ -1053,8 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             auto test = [&](unsigned long long &bar, uint32_t k) { return phase_done(B_(bar), k & 1); };
             auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
             // scores of tile x against the key block at `keys`; `ahead` is called before the last products
-            auto score = [&](auto X, uint32_t keys, bool final, auto &&ahead) {
-                constexpr int x = decltype(X)::value;
+            auto score = [&](uint32_t x, uint32_t keys, bool final, auto &&ahead) {
                 auto product = [&](int k) {
                     const uint32_t off = ((k >> 2) * (kBlockBytes / 2) + (k & 3) * 32) >> 4;
                     if (k == 0) mma_ss<false>(128 * x, q_low + x * kStep + off, keys + off, kIdescS);
@@ -1074,8 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                 }
             };
             // weights of tile x times the value block at `values`
-            auto output = [&](auto X, uint32_t values, bool first, bool final, auto &&ahead) {
-                constexpr int x = decltype(X)::value;
+            auto output = [&](uint32_t x, uint32_t values, bool first, bool final, auto &&ahead) {
                 auto product = [&](int part, int k, uint32_t add) {
                     mma_ts(256 + 128 * x, 128 * x + 64 * part + 8 * k, values + k * (2048 >> 4), kIdescO, add);
                 };
@@ -1099,77 +1098,76 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             auto release = [&](int st) {
                 if (elect_one()) commit(B_(bars.empty[st]));
             };
-            using Zero = std::integral_constant<int, 0>;
-            using One = std::integral_constant<int, 1>;
             while (const Piece *p = follow.take()) {
                 const int j0 = same(p->j0), j1 = same(p->j1), edge = same(p->edge), last_a = same(p->last(0)), last_b = same(p->last(1));
                 __syncwarp();
                 follow.done(lane == 0);
                 if (j1 == j0) continue;
-                uint32_t ready_v = 0, ready_a = 0;
                 // Outputs of block j, and the scores of j + 1 (m: its keys are use 2 m of the ring, block j's values use
-                // 2 m - 1).  Steady blocks: both tiles go on, no run begins and no row is at its edge.  One body for both halves of
-                // the ring (two, with stages that are constants: 24 ragged prompts 428 us instead of 422, 512 fp32 rows 344 instead
-                // of 315, 32768 tokens the same).
+                // 2 m - 1), tile after tile.  Steady blocks: both tiles go on, no run begins and no row is at its edge.  The others,
+                // with the piece's first scores (j = j0 - 1) among them, have a body of their own.  One of each, for both tiles and
+                // both halves of the ring: code that comes only now and then has to be fetched from far away.  With bodies for
+                // every tile and half, of constants, 24 ragged prompts took 431 us instead of 414, chunks 697 instead of 685, 32768
+                // tokens 5.07 ms instead of 4.95; all blocks through the general body 449, 780 and 5.82.
+                uint32_t ready_v = 0, ready_p[2] = {0, 0};
                 auto steady = [&] {
                     const uint32_t k = 2 * (m & 1), v = 3 - k, keys = key_low + k * kStep, values = value_low + v * kStep;
-                    uint32_t ready_k = 0, ready_b = 0;
+                    uint32_t ready_k = 0;
                     if (!ready_v) wait(bars.full[v], (m - 1) >> 1);
-                    if (!ready_a) wait(bars.p_full[0], np[0]);
-                    np[0]++;
-                    output(Zero{}, values, false, false, [&] { ready_k = test(bars.full[k], m >> 1); });
-                    if (!ready_k) wait(bars.full[k], m >> 1);
-                    score(Zero{}, keys, false, [&] { ready_b = test(bars.p_full[1], np[1]); });
-                    if (!ready_b) wait(bars.p_full[1], np[1]);
-                    np[1]++;
-                    output(One{}, values, false, false, [] {});
-                    release(v);
-                    score(One{}, keys, false, [&] {
-                        ready_v = test(bars.full[k + 1], m >> 1);
-                        ready_a = test(bars.p_full[0], np[0]);
-                    });
+#pragma unroll 1
+                    for (uint32_t x = 0; x < 2; x++) {
+                        if (!(x ? ready_p[1] : ready_p[0])) wait(bars.p_full[x], x ? np[1] : np[0]);
+                        if (x) np[1]++;
+                        else np[0]++;
+                        output(x, values, false, false, [&] {
+                            if (!x) ready_k = test(bars.full[k], m >> 1);
+                        });
+                        if (x) release(v);
+                        else if (!ready_k) wait(bars.full[k], m >> 1);
+                        score(x, keys, false, [&] {
+                            if (x) ready_v = test(bars.full[k + 1], m >> 1);
+                            const uint32_t other = test(bars.p_full[1 - x], x ? np[0] : np[1]);
+                            if (x) ready_p[0] = other;
+                            else ready_p[1] = other;
+                        });
+                    }
                     release(k);
                 };
-                // The others, with the piece's first scores (j = j0 - 1) among them, share one body: code that comes only now
-                // and then has to be fetched from far away (6001 tokens, 32 / 8 heads: 267 us with bodies of their own, 255
-                // with one; all blocks through it 32768 tokens 5.37 -> 5.70 ms).
                 auto block = [&](int j) {
-                    const bool now = j >= j0, more = j + 1 < j1, now_a = now && j < last_a, now_b = now && j < last_b,
-                               next_a = j + 1 < last_a, next_b = j + 1 < last_b;
-                    const uint32_t half = m & 1, v = 3 - 2 * half, k = 2 * half, turn_v = (m - 1) >> 1, turn = m >> 1;
+                    const bool now = j >= j0, more = j + 1 < j1;
+                    const uint32_t half = m & 1, v = 3 - 2 * half, k = 2 * half;
                     const uint32_t keys = key_low + k * kStep, values = value_low + v * kStep;
-                    uint32_t ready_k = !more, ready_b = 0;
+                    uint32_t ready_k = !more;
                     if (now) {
-                        if (!ready_v) wait(bars.full[v], turn_v);
-                        if (j >= edge) wait(bars.v_ok[1 - half], turn_v);
+                        if (!ready_v) wait(bars.full[v], (m - 1) >> 1);
+                        if (j >= edge) wait(bars.v_ok[1 - half], (m - 1) >> 1);
                     }
-                    if (now_a) {
-                        if (!ready_a) wait(bars.p_full[0], np[0]);
-                        np[0]++;
-                        output(Zero{}, values, run_begins<kWide, kRuns>(j, j0), j + 1 == last_a, [&] {
-                            if (more) ready_k = test(bars.full[k], turn);
-                        });
-                    }
-                    if (!ready_k) wait(bars.full[k], turn);
-                    if (next_a) {
-                        if (!now) wait(bars.q_full[0], nq[0]++);
-                        score(Zero{}, keys, j + 2 == last_a, [&] {
-                            if (now_b) ready_b = test(bars.p_full[1], np[1]);
-                        });
-                    }
-                    if (now_b) {
-                        if (!ready_b) wait(bars.p_full[1], np[1]);
-                        np[1]++;
-                        output(One{}, values, run_begins<kWide, kRuns>(j, j0), j + 1 == last_b, [] {});
-                    }
-                    if (now) release(v);
-                    ready_v = ready_a = 0;
-                    if (next_b) {
-                        if (!now) wait(bars.q_full[1], nq[1]++);
-                        score(One{}, keys, j + 2 == last_b, [&] {
-                            if (more) ready_v = test(bars.full[k + 1], turn);
-                            if (now && next_a) ready_a = test(bars.p_full[0], np[0]);
-                        });
+#pragma unroll 1
+                    for (uint32_t x = 0; x < 2; x++) {
+                        const int last = x ? last_b : last_a;
+                        if (now && j < last) {
+                            if (!(x ? ready_p[1] : ready_p[0])) wait(bars.p_full[x], x ? np[1] : np[0]);
+                            if (x) np[1]++;
+                            else np[0]++;
+                            output(x, values, run_begins<kWide, kRuns>(j, j0), j + 1 == last, [&] {
+                                if (!x && more) ready_k = test(bars.full[k], m >> 1);
+                            });
+                        }
+                        if (x) {
+                            if (now) release(v);
+                            ready_v = ready_p[0] = 0;
+                        } else {
+                            if (!ready_k) wait(bars.full[k], m >> 1);
+                            ready_p[1] = 0;
+                        }
+                        if (j + 1 < last) {
+                            if (!now) wait(bars.q_full[x], x ? nq[1]++ : nq[0]++);
+                            score(x, keys, j + 2 == last, [&] {
+                                if (x) ready_v = test(bars.full[k + 1], m >> 1);
+                                else if (now && j < last_b) ready_p[1] = test(bars.p_full[1], np[1]);
+                                if (x && now && j + 1 < last_a) ready_p[0] = test(bars.p_full[0], np[0]);
+                            });
+                        }
                     }
                     if (more) release(k);
                 };
