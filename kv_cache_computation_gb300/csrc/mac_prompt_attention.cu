@@ -55,8 +55,8 @@
 // library's largest product's rate): 32768 tokens 4.95 ms, 5.42 one after another
 // (1775 and 1620 TFLOP/s of the products that the causal edge leaves), 6001 tokens
 // 250 us (1370), 2048 and 509 tokens behind 30720 and 8191 685 us (1660), 24 ragged
-// prompts of 1 .. 4096 tokens 414 us (1315), 5 of 1 .. 6001 with 28 / 4 heads 233 us
-// (1285), 512 fp32 rows behind 32256 290 to 310 us (910; with the second P V 1365),
+// prompts of 1 .. 4096 tokens 414 us (1315), 5 of 1 .. 6001 with 28 / 4 heads 222 us
+// (1350), 512 fp32 rows behind 32256 290 to 310 us (910; with the second P V 1365),
 // 16 tokens 10.7 to 12.4 us.
 // What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
 // from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
@@ -67,8 +67,8 @@
 // besides its blocks (first scores, first softmax, the output, code that was not
 // near), which with the edge blocks' hidden halves is what ragged prompts lose; the
 // prologue (lengths, split, first loads) 8000 to 16000 a call.
-// Tried and slower (32768 tokens, us, against the form of the time): softmax
-// warps of half a row each 5.79 / 5.45 ms; a second warp to issue 7.05 / 6.0; P V
+// Tried and slower (32768 tokens, ms, against the form of the time): softmax
+// warps of half a row each 5.79 / 5.45; a second warp to issue 7.05 / 6.0; P V
 // issued for the first keys before the last weights are there 5.70 / 5.33; waits
 // that spin 5.5 / 5.33; weights against the old reference, which the row's sum
 // then confirms, instead of a maximum first: no faster at 32768 tokens, 28 heads
@@ -81,7 +81,6 @@
 #include "mac_prompt.cuh"
 
 #include <climits>
-#include <type_traits>
 #include <cudaTypedefs.h>
 
 namespace macgpu {
@@ -883,6 +882,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         s_fail = 0;
     }
+    // Rows of the tiles that no token fills, where 128 is no multiple of the group: zeros, which no copy overwrites.  Scores
+    // from whatever stood there could take the paths for references that move or are huge (5 prompts with 28 / 4 heads 233 -> 222 us).
+    const int used = a.tile_tokens * a.G, spare = (128 - used) * 8;
+    for (int i = tid; i < 4 * spare; i += kThreads)
+        *reinterpret_cast<uint4 *>(base + i / spare * (kBlockBytes / 2) + used * 128 + i % spare * 16) = make_uint4(0, 0, 0, 0);
+    if (spare) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     for (int i = tid; i < kPieces * kD; i += kThreads) queue.bad[i / kD][i % kD] = INT_MAX;
     if (tid < kPieces) queue.dirty[tid] = 0;
     if (warp == 0) {
