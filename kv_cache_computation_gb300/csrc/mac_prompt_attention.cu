@@ -71,8 +71,8 @@
 // warps of half a row each 5.79 / 5.45; a second warp to issue 7.05 / 6.0; P V
 // issued for the first keys before the last weights are there 5.70 / 5.33; waits
 // that spin 5.5 / 5.33; weights against the old reference, which the row's sum
-// then confirms, instead of a maximum first: no faster at 32768 tokens, 28 heads
-// 308 / 262 us; every eighth ex2 as a polynomial 5.43 / 5.28 (packed products run at
+// then confirms, instead of a maximum first: no faster, chunks 677 / 685 us; every
+// eighth ex2 as a polynomial 5.43 / 5.28 (packed products run at
 // half rate); outputs through shared memory, in whole lines, slower than 32 bytes a
 // thread from the registers.  A third part of the weights for fp32 outputs, in the
 // first one's place after its products: error 7e-7 instead of 2e-6 at 2048 keys, 512
