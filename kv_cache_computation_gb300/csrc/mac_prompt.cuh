@@ -10,12 +10,12 @@ constexpr int kPMaxGroup = 128;         // query heads per KV head: a tile has a
 constexpr int kPLevels = 2048;          // levels by which items are ordered: of a block each up to 262144 keys
 constexpr int kPMaxCtas = 256;          // upper bound of the grid (one CTA per SM)
 constexpr int kPRows = 256;             // query rows of an item: two tiles of 128
-// Items per CTA, at least, in the line of blocks that is cut (more of them: items beside one another go to one CTA, and 5
-// prompts of 1 .. 6001 tokens took 269 us with two, 284 with four instead of 262).
+// Items per CTA, at least, in the line of blocks that is cut.  us with one and two: chunks of 2048 and 509 tokens 674, 707;
+// 24 ragged prompts 415, 418; 5 with 28 / 4 heads 222, 227.
 constexpr int kPLineRows = 1;
 // Blocks that an item counts besides its own in the split of the work: a piece costs 7000 to 10000 cycles whatever its
-// length, a block 2400 to 2700.  us with 0, 2, 4 and 5: 6001 tokens of 28 / 4 heads 235, 217, 209, 207; of 32 / 8 heads 311,
-// 263, 255, 260; ten prompts of 958 tokens 121, 109, 105, 105; 24 ragged ones 453, 451, 453, 458.
+// length, a block 2400 to 2700.  us without and with them, when they came: 6001 tokens of 28 / 4 heads 235, 209, of 32 / 8
+// heads 311, 255; ten prompts of 958 tokens 121, 105.  With 2, 4 and 6: 194, 192 and 194 us, 245, 246, 246, and 91, 90, 93.
 constexpr int kPExtra = 4;
 
 // bits of the device error word
