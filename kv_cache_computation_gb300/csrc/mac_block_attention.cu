@@ -11,7 +11,9 @@
 //   lse = ln 2 (low + log2 l)
 // so that a page's value scale costs one subtraction per row and page: it goes
 // into the exponent, the reference is that of the products, and the codes need
-// no scaling at all.
+// no scaling at all.  A w below fp32's range adds nothing to out, but w 2^-ev may
+// still count in l: there it is taken as one power, 2^(s_t - low), and so are the
+// factors that bring sums to a later reference (sum_at).
 //
 // Rows, products, fragments' free orders, the split into equal ranges of a line
 // of units and the merge of pieces are those of the 4-bit store's attention
@@ -47,6 +49,11 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t &lo, uint32_t &hi)
         : "=r"(lo), "=r"(hi)
         : "r"(w));
 }
+
+// Value scales below this one can make a token whose weight w is under fp32's range (2^-126 of the row's reference) count in
+// l, by w 2^-ev: l is at least 2^9 2^-60, and as many tokens as a length can hold, each 2^-126 2^-ev, stay below 2^-24 of
+// that for ev >= -21.
+constexpr int kSmallExp = -21;
 
 __host__ __device__ constexpr int block_team_bytes(int nt, int pp, int stages, bool qreg)
 {
@@ -373,9 +380,9 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                             // a row moves by its own scores alone; those of 2^23 and more are whole numbers too coarse to
                             // take the shift from
                             y = y - low[nt][h] > kMargin + kPShift ? (fabsf(y) < 0x1p23f ? y - kPShift : y) : low[nt][h];
-                            const float f = ex2_approx(low[nt][h] - y);
+                            const float d = low[nt][h] - y, f = ex2_approx(d);
                             low[nt][h] = y;
-                            sum[nt][h] *= f;
+                            sum[nt][h] = sum_at<true>(sum[nt][h], f, d);
 #pragma unroll
                             for (int j = 0; j < 8; j++) {
                                 o[nt][j][h] *= f;
@@ -383,6 +390,18 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                             }
                         }
                 }
+                // A weight below 2^-126 becomes 0 further down; with a small value scale its part of the sum is still to count
+#pragma unroll
+                for (int pp = 0; pp < PP; pp++)
+                    if (ev[pp] < kSmallExp) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                const float w = s[pp][nt][k] - (low[nt][k & 1] - (float)ev[pp]);
+                                if (w < -126.f) sum[nt][k & 1] += ex2_approx(w - (float)ev[pp]);
+                            }
+                    }
                 uint32_t pb[PP][NT][2];     // P^T fragments: tokens 4 c .. 4 c + 3, row g
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
@@ -506,7 +525,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
             n = min(left, n_units) - EXTRA;
         }
     }
-    merge_pieces<TEAMS, TEAMS>(a, sm, park);
+    merge_pieces<TEAMS, TEAMS, true>(a, sm, park);
 }
 
 struct Variant {
@@ -557,7 +576,7 @@ cudaError_t launch_block_attention(const QuantAttnArgs &a, int sm_count, cudaStr
     const int grid = grid_of(v, sm_count);
     const cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.teams * 32), v.smem, s, true, a);
     if (e != cudaSuccess) return e;
-    return launch_quant_combine(a, grid, v.padrows, sm_count, s);
+    return launch_quant_combine<true>(a, grid, v.padrows, sm_count, s);
 }
 
 }  // namespace macgpu

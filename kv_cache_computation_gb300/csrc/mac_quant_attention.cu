@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) quant_attention_kernel(const
             }
         }
     }
-    merge_pieces<TEAMS, TEAMS>(a, sm, park);
+    merge_pieces<TEAMS, TEAMS, false>(a, sm, park);
 }
 
 struct Variant {
@@ -558,7 +558,7 @@ cudaError_t launch_quant_attention(const QuantAttnArgs &a, int sm_count, cudaStr
     const int grid = grid_of(v, sm_count);
     cudaError_t e = launch_maybe_pdl(v.kernel, dim3(grid), dim3(v.teams * 32), v.smem, s, true, a);
     if (e != cudaSuccess) return e;
-    return launch_quant_combine(a, grid, v.padrows, sm_count, s);
+    return launch_quant_combine<false>(a, grid, v.padrows, sm_count, s);
 }
 
 }  // namespace macgpu

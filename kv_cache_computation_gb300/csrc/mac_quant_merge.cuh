@@ -35,6 +35,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A sum of weights, l, at a reference -d log2 units higher: l 2^d, with w = 2^d.  kFar, for the 8-bit store: its references
+// are those of products, in whose units a token's weight may be 2^69, so that l 2^d counts where 2^d alone is 0 already.
+template <bool kFar>
+__device__ __forceinline__ float sum_at(float l, float w, float d)
+{
+    if (kFar && d < -120.f) return l * 0x1p-120f * ex2_approx(d + 120.f);
+    return l * w;
+}
+
 // What the merge needs of a block: the line, the block's units of it, and the
 // group of each parked piece, in order (-1: none).
 struct MergeState {
@@ -109,7 +118,7 @@ struct Parking {
 };
 
 // Behind the long loop: all warps of the block (WARPS, in TEAMS teams).
-template <int TEAMS, int WARPS>
+template <int TEAMS, int WARPS, bool FAR>
 __device__ __forceinline__ void merge_pieces(const QuantAttnArgs &a, const MergeState &sm, const Parking &park)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Hkv = a.st.kv_heads;
@@ -142,8 +151,8 @@ __device__ __forceinline__ void merge_pieces(const QuantAttnArgs &a, const Merge
             const bool none = ml.y == 0.f;      // saw no token
             const float m = warp_max(none ? -CUDART_INF_F : ml.x);
             // a NaN sum survives: its weight is a number or NaN, and the product NaN
-            const float w = none ? 0.f : exp2f(ml.x - m);
-            const float l = warp_sum(none ? 0.f : ml.y * w);
+            const float d = ml.x - m, w = none ? 0.f : exp2f(d);
+            const float l = warp_sum(none ? 0.f : sum_at<FAR>(ml.y, w, d));
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             uint32_t rest_of = __ballot_sync(0xffffffffu, !none);
             while (rest_of) {
@@ -178,6 +187,7 @@ __device__ __forceinline__ void merge_pieces(const QuantAttnArgs &a, const Merge
 // that the merge took without), then with them.
 constexpr int kCombineWarps = 8, kCombineBatch = 8;
 
+template <bool FAR>
 __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const __grid_constant__ QuantAttnArgs a,
                                                                           int padrows, int rpb)
 {
@@ -220,13 +230,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
                 if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);      // a sum of 0 saw no token
             const float wo = l == 0.f ? 0.f : ex2_approx(m - top);
             o = make_float4(o.x * wo, o.y * wo, o.z * wo, o.w * wo);
-            l *= wo;
+            l = sum_at<FAR>(l, wo, m - top);
 #pragma unroll
             for (int i = 0; i < kCombineBatch; i++) {
                 // a NaN sum survives: its weight is a number or NaN, and the product NaN
                 const bool some = ml[i].y != 0.f;
-                const float w = some ? ex2_approx(ml[i].x - top) : 0.f;
-                l += some ? ml[i].y * w : 0.f;
+                const float d = ml[i].x - top, w = some ? ex2_approx(d) : 0.f;
+                l += some ? sum_at<FAR>(ml[i].y, w, d) : 0.f;
                 o.x += some ? x[i].x * w : 0.f;
                 o.y += some ? x[i].y * w : 0.f;
                 o.z += some ? x[i].z * w : 0.f;
@@ -250,8 +260,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) quant_combine_kernel(const
                 const float2 ml = sml[warp + w];
                 const float4 x = so[warp + w][lane];
                 if (ml.y == 0.f) continue;
-                const float f = ex2_approx(ml.x - top);
-                l += ml.y * f;
+                const float d = ml.x - top, f = ex2_approx(d);
+                l += sum_at<FAR>(ml.y, f, d);
                 o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
             }
             const int b = group / a.st.kv_heads;
@@ -273,13 +283,14 @@ inline int quant_grid(int sm_count, int blocks_per_sm, int teams, int padrows)
     return grid < kMaxCtas ? grid : kMaxCtas;
 }
 
+template <bool FAR>
 static inline cudaError_t launch_quant_combine(const QuantAttnArgs &a, int grid, int padrows, int sm_count, cudaStream_t s)
 {
     // as many warps to a row as keep the blocks, most of which find nothing to merge, near one wave
     const int items = meta_by_group(a, grid) ? a.batch * a.st.kv_heads : grid;
     int rpb = 1;
     while (rpb < kCombineWarps && rpb < a.rows && (int64_t)items * ((a.rows + rpb - 1) / rpb) > 4 * sm_count) rpb *= 2;
-    return launch_maybe_pdl(quant_combine_kernel, dim3(items, (a.rows + rpb - 1) / rpb), dim3(kCombineWarps * 32), 0, s, true,
+    return launch_maybe_pdl(quant_combine_kernel<FAR>, dim3(items, (a.rows + rpb - 1) / rpb), dim3(kCombineWarps * 32), 0, s, true,
                             a, padrows, rpb);
 }
 
