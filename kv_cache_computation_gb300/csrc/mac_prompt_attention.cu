@@ -619,6 +619,9 @@ struct Walk {
     }
 };
 
+// An infinity becomes NaN, as the values on an edge become (x * 0 is NaN for it, else a zero of x's sign).
+__device__ __forceinline__ float finite_or_nan(float x) { return __fmaf_rn(x, 0.f, x); }
+
 // 32 bytes of a row.
 __device__ __forceinline__ void store32(void *to, const uint32_t *w)
 {
@@ -979,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     tmem_ld16(tO + 16 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i++) o[i] *= scale;
+                    for (int i = 0; i < 16; i++) o[i] = finite_or_nan(o[i] * scale);
                     if (!every || dirty) {
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
@@ -994,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i++) o[i] *= scale;
+                    for (int i = 0; i < 32; i++) o[i] = finite_or_nan(o[i] * scale);
                     if (!every || dirty) {
 #pragma unroll
                         for (int i = 0; i < 32; i++) {
