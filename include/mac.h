@@ -633,7 +633,8 @@ mac_status mac_prompt_destroy(mac_prompt_handle h);
  *   dev_lse       fp32 [n_q][heads], or NULL
  * Rows of no sequence are left as they are.  A key or value has no effect, NaN
  * included, on a query that does not see it; one that sees a value that is not
- * finite gives NaN in that element.
+ * finite gives NaN in that element, and one whose scores are all minus infinity
+ * (an infinity in it, or in the keys that it sees) NaN.
  * The softmax weights are rounded to bf16 (fp32 outputs: to 17 bits, and the
  * outputs' relative error is about 3e-6 up to 32768 keys and more).  Results
  * do not depend on other sequences' values, but the split of the work, and with

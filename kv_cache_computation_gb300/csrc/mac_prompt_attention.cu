@@ -953,7 +953,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             const bool some = last > j0;
             const int slot = p->slot;
             const bool part = slot >= 0;
-            const float scale = !some || sum == 0.f ? 0.f : part ? 1.f : 1.f / sum;
+            // a row that sees keys and has no weight, its scores being minus infinity, is 0 / 0
+            const float none = lim > 0 && !part ? CUDART_NAN_F : 0.f;
+            const float scale = !some || sum == 0.f ? none : part ? 1.f : 1.f / sum;
             const int row_tok = row / a.G;
             const int64_t out_row = (int64_t)(p->row0 + x * a.tile_tokens + row_tok) * a.heads + p->head * a.G + row - row_tok * a.G;
             const int64_t part_row = ((int64_t)blockIdx.x * 2 + slot) * kPRows + 128 * x + row;
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
                             : reinterpret_cast<char *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + out_row * kD);
             if (valid) {
                 if (part) a.part_ml[part_row] = make_float2(ref, sum);
-                else if (a.lse) a.lse[out_row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
+                else if (a.lse) a.lse[out_row] = sum == 0.f ? none - CUDART_INF_F : (ref + log2f(sum)) * kLn2;
             }
             const bool every = __all_sync(0xffffffffu, scale != 0.f);       // else some rows' O was never written, or is to be 0
             if (some) {
@@ -1348,14 +1350,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prompt_merge_kernel(const __
     for (int x = 0; x < 2; x++) {
         if (tok[x] >= s.n) continue;
         const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
-        const float4 v = l[x] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+        const float none = s.m > 0 && s.m - s.n - a.lag + tok[x] + 1 > 0 ? CUDART_NAN_F : 0.f;      // as in a whole item
+        const float4 v = l[x] == 0.f ? make_float4(none, none, none, none)
                                      : make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv);
         const int64_t at = (int64_t)(s.q0 + tok[x]) * a.heads + meta.head * a.G + row_head;
         if (kWide) reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at * kD)[lane] = v;
         else
             reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + at * kD)[lane] =
                 make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-        if (lane == 0 && a.lse) a.lse[at] = l[x] == 0.f ? -CUDART_INF_F : (m[x] + log2f(l[x])) * kLn2;
+        if (lane == 0 && a.lse) a.lse[at] = l[x] == 0.f ? none - CUDART_INF_F : (m[x] + log2f(l[x])) * kLn2;
     }
 }
 

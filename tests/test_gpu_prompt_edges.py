@@ -1,9 +1,9 @@
 """Prompt attention where it can go wrong beside what test_gpu_prompt.py covers:
-infinities wherever they stand."""
+infinities wherever they stand, and rows whose every score is minus infinity."""
 import pytest
 import torch
 
-from test_gpu_prompt import BF16, F32, _i32, _randn
+from test_gpu_prompt import BF16, F32, Case, _i32, _randn
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -37,3 +37,40 @@ def test_an_infinite_value_gives_nan_wherever_it_stands(H, Hkv, m, wide):
         got = chunks(c)
         assert torch.equal(torch.isnan(got), bad) and not torch.isinf(got).any()
         assert torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H,Hkv,seqs,lag", [(8, 2, [(1, 1), (40, 40), (7, 300)], 0), (28, 4, [(130, 400), (9, 9)], 3),
+                                            (4, 1, [(5, 9000), (3, 3)], 0), (32, 8, [(600, 2000), (40, 40)], 64)])
+def test_scores_of_minus_infinity_alone_are_no_empty_row(H, Hkv, seqs, lag, wide):
+    """A query with an infinity whose scores are all minus infinity: 0 / 0, which is NaN and not the output 0, lse -inf of a
+    row that sees nothing.  So is one that sees an infinite key alone.  Rows that see nothing stay as they are."""
+    c = Case(seqs, H, Hkv, lag=lag, seed=7, wide=wide)
+    G = H // Hkv
+    c.k[:, :, 5] = c.k[:, :, 5].abs() + 0.5
+    clean, clse = c.run()
+    rows = torch.zeros(int(c.qs[-1]), H, dtype=torch.bool, device="cuda")
+    empty = torch.zeros_like(rows)
+    for b, (n, m) in enumerate(seqs):
+        for i in {0, n // 2, n - 1}:
+            c.q[int(c.qs[b]) + i, (b + i) % H, 5] = float("-inf")
+            rows[int(c.qs[b]) + i, (b + i) % H] = True
+        for i in range(n):
+            if m - n + i + 1 - lag <= 0:
+                empty[int(c.qs[b]) + i] = True
+    out, lse = c.run()
+    c.attend.sync()
+    n = int(c.qs[-1])
+    out, lse, clean, clse = out[:n], lse[:n], clean[:n], clse[:n]
+    assert torch.isnan(out[rows & ~empty]).all() and torch.isnan(lse[rows & ~empty]).all()
+    assert (out[empty] == 0).all() and torch.isneginf(lse[empty]).all()
+    good = ~rows & ~empty
+    assert torch.equal(out[good], clean[good]) and torch.equal(lse[good], clse[good])
+    # a key: the query that sees it alone
+    if lag == 0 and seqs[0] == (1, 1):
+        c = Case(seqs, H, Hkv, seed=8, wide=wide)
+        c.q[0, :, 9] = c.q[0, :, 9].abs() + 0.5
+        c.k[0, Hkv - 1, 9] = float("-inf")
+        out, lse = c.run()
+        assert torch.isnan(out[0, -G:]).all() and torch.isnan(lse[0, -G:]).all()
+        assert torch.isfinite(out[0, :-G]).all()
