@@ -168,6 +168,10 @@ mac_status mac_set_page_table(mac_handle h, int req, const int32_t *dev_pages, i
 mac_status mac_append_kv(mac_handle h, int req, const void *dev_k, const void *dev_v, int64_t n_tokens,
                          void *stream);
 
+/* The tokens that request req may hold: max_ctx, or what its page table has
+ * room for where that is less.  Host only. */
+mac_status mac_get_capacity(mac_handle h, int req, int64_t *tokens);
+
 /* One MAC decode step for requests 0..batch-1 (Figure 2 (a)->(b)->(c)):
  * appends k_new/v_new (device bf16 [batch][kv_heads][head_dim], post-RoPE)
  * at position m = length + 1, runs Match on q_pre (pre-RoPE, device bf16

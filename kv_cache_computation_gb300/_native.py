@@ -9,7 +9,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmac.so")
 
-MAC_OK = 0
+MAC_OK, MAC_ERR_CAPACITY = 0, -4
 STATUS = {0: "MAC_OK", -1: "MAC_ERR_INVALID_ARG", -2: "MAC_ERR_OOM", -3: "MAC_ERR_CUDA", -4: "MAC_ERR_CAPACITY",
           -5: "MAC_ERR_TIMEOUT", -6: "MAC_ERR_STATE"}
 
@@ -77,6 +77,7 @@ SIGNATURES = {
     "mac_destroy": (_i, [_vp]),
     "mac_set_page_table": (_i, [_vp, _i, _vp, _i, _vp]),
     "mac_append_kv": (_i, [_vp, _i, _vp, _vp, _i64, _vp]),
+    "mac_get_capacity": (_i, [_vp, _i, _pi64]),
     "mac_decode_step": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mac_decode_step_host": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "mac_full_step": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),

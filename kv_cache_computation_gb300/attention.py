@@ -185,7 +185,7 @@ class MacAttention:
         `prompt` (a PromptAttention of the same heads and scale), and the ring is seeded with its last queries and their
         summaries AS_{1:pos-r}, so that the first decode steps can already reuse them.  q_pre, q_post bf16 [tokens, heads,
         128] (before and after the rotation), k, v bf16 [tokens, kv_heads, 128]; at least one token.  Returns (out, lse).
-        Waits for the stream, as seed_ring does."""
+        What is refused is refused before the request is touched.  Waits for the stream, as seed_ring does."""
         n, L = q_post.shape[0], self.ring_len
         if prompt.heads != self.heads or prompt.kv_heads != self.kv_heads or prompt.device != self.device:
             raise ValueError("prompt was made for other heads or another device")
@@ -195,14 +195,20 @@ class MacAttention:
             raise ValueError(f"a prompt of {n} tokens; the PromptAttention was made for 1 to {prompt.max_tokens}")
         qs, ks = (n, self.heads, self.head_dim), (n, self.kv_heads, self.head_dim)
         for t, name, shape in ((q_pre, "q_pre", qs), (q_post, "q_post", qs), (k, "k", ks), (v, "v", ks)):
-            _dev(t, name, torch.bfloat16, shape, self.device)
-        last = min(L, n)
+            if _dev(t, name, torch.bfloat16, shape, self.device) % 16:
+                raise ValueError(f"{name} must start on 16 bytes")
+        room, last = ctypes.c_int64(), min(L, n)
         with _guard(self.device, stream):
+            _check("mac_get_capacity", N.lib().mac_get_capacity(self._h, req, ctypes.byref(room)), self._h)
+            if n > room.value:
+                raise N.MacError("mac_append_kv", N.MAC_ERR_CAPACITY,
+                                 f"a prompt of {n} tokens; request {req} may hold {room.value}")
             starts = torch.tensor([[0, n], [0, last]], dtype=torch.int32, device=self.device)
-            self.reset_request(req)
-            self.append_kv(req, k, v)
+            # the attention first: what it refuses leaves the request as it was
             out, lse = prompt(q_post, k, v, starts[0])
             o, z = prompt(q_post[n - last:], k, v, starts[1], starts[0], lag=self.band_r, out_dtype=torch.float32)
+            self.reset_request(req)
+            self.append_kv(req, k, v)
             self.seed_ring(req, q_pre[n - last:], o, z, np.arange(n - last + 1, n + 1))
         return out, lse
 

@@ -591,6 +591,15 @@ mac_status mac_append_kv(mac_handle h, int req, const void *dev_k, const void *d
     return MAC_OK;
 }
 
+mac_status mac_get_capacity(mac_handle h, int req, int64_t *tokens)
+{
+    const mac_status st = check_handle(h);
+    if (st != MAC_OK) return st;
+    if (req < 0 || req >= h->cfg.max_batch || !tokens) return MAC_ERR_INVALID_ARG;
+    *tokens = capacity(h, req);
+    return MAC_OK;
+}
+
 mac_status mac_decode_step(mac_handle h, int batch, const void *dev_q_pre, const void *dev_q_post,
                            const void *dev_k_new, const void *dev_v_new, void *dev_out, float *dev_lse_out,
                            void *stream)
