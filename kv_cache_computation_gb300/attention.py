@@ -189,7 +189,8 @@ class MacAttention:
         n, L = q_post.shape[0], self.ring_len
         if prompt.heads != self.heads or prompt.kv_heads != self.kv_heads or prompt.device != self.device:
             raise ValueError("prompt was made for other heads or another device")
-        if (prompt.cfg.sm_scale or self.head_dim ** -0.5) != (self.cfg.sm_scale or self.head_dim ** -0.5):
+        usual = ctypes.c_float(self.head_dim ** -0.5).value         # as a scale that is given is held
+        if (prompt.cfg.sm_scale or usual) != (self.cfg.sm_scale or usual):
             raise ValueError("prompt was made with another scale")
         if not 1 <= n <= prompt.max_tokens:
             raise ValueError(f"a prompt of {n} tokens; the PromptAttention was made for 1 to {prompt.max_tokens}")

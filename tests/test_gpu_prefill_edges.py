@@ -1,4 +1,5 @@
-"""MacAttention.prefill: what it refuses leaves the request as it was."""
+"""MacAttention.prefill: what it refuses leaves the request as it was, and scales that
+are the same."""
 import numpy as np
 import pytest
 import torch
@@ -64,3 +65,17 @@ def test_what_prefill_refuses_leaves_the_request_as_it_was(page):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     mac.prefill(prompt, 0, *_inputs(64, 61))                         # as long as the request may be
     assert mac.read_ring(0)["kv_len"] == 64
+
+
+def test_prefill_takes_the_same_scale_given_or_by_default():
+    from kv_cache_computation_gb300 import PromptAttention
+    same = 128 ** -0.5
+    x = _inputs(40)
+    want = _mac(H, Hkv).prefill(PromptAttention(H, Hkv, max_tokens=40), 0, *x)
+    for of_mac, of_prompt in ((0.0, same), (same, 0.0), (same, same), (float(np.float32(same)), 0.0)):
+        mac = _mac(H, Hkv, sm_scale=of_mac)
+        got = mac.prefill(PromptAttention(H, Hkv, max_tokens=40, sm_scale=of_prompt), 0, *x)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for of_mac, of_prompt in ((0.0, 0.1), (0.1, 0.0), (same, 0.0884)):
+        with pytest.raises(ValueError, match="scale"):
+            _mac(H, Hkv, sm_scale=of_mac).prefill(PromptAttention(H, Hkv, max_tokens=40, sm_scale=of_prompt), 0, *x)
