@@ -1,5 +1,5 @@
-"""MacAttention.prefill: what it refuses leaves the request as it was, and scales that
-are the same."""
+"""MacAttention.prefill: what it refuses leaves the request as it was; scales that
+are the same; another stream."""
 import numpy as np
 import pytest
 import torch
@@ -79,3 +79,27 @@ def test_prefill_takes_the_same_scale_given_or_by_default():
     for of_mac, of_prompt in ((0.0, 0.1), (0.1, 0.0), (same, 0.0884)):
         with pytest.raises(ValueError, match="scale"):
             _mac(H, Hkv, sm_scale=of_mac).prefill(PromptAttention(H, Hkv, max_tokens=40, sm_scale=of_prompt), 0, *x)
+
+
+def test_prefill_on_another_stream():
+    """Inputs made on that stream, by work that is still under way when the call is made."""
+    from kv_cache_computation_gb300 import PromptAttention
+    n = 700
+    prompt, mac, other = PromptAttention(H, Hkv, max_tokens=n), _mac(H, Hkv), _mac(H, Hkv)
+    x = _inputs(n)
+    want = mac.prefill(prompt, 1, *x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        y = [torch.zeros_like(t) for t in x]
+        big = torch.ones(1 << 28, device="cuda")
+        for _ in range(10):
+            big.mul_(1.0)
+        for a, b in zip(y, x):
+            a.copy_(b)
+    got = other.prefill(prompt, 1, *y, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    a, b = mac.read_ring(1), other.read_ring(1)
+    for key in a:
+        assert np.array_equal(a[key], b[key]), key

@@ -1,5 +1,6 @@
 """Prompt attention where it can go wrong beside what test_gpu_prompt.py covers:
-infinities wherever they stand, and rows whose every score is minus infinity."""
+infinities wherever they stand, rows whose every score is minus infinity, large
+groups with many items, many short prompts."""
 import pytest
 import torch
 
@@ -74,3 +75,25 @@ def test_scores_of_minus_infinity_alone_are_no_empty_row(H, Hkv, seqs, lag, wide
         out, lse = c.run()
         assert torch.isnan(out[0, -G:]).all() and torch.isnan(lse[0, -G:]).all()
         assert torch.isfinite(out[0, :-G]).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H,Hkv,seqs", [(32, 1, [(1500, 1500), (3, 700)]), (33, 1, [(900, 1200)]), (64, 1, [(700, 700)] * 2),
+                                        (100, 1, [(800, 800), (1, 1)]), (128, 1, [(500, 3000)]), (256, 2, [(400, 900), (33, 33)])])
+def test_many_items_of_large_groups(H, Hkv, seqs, wide):
+    """Tiles of 4 tokens down to one: whole items, the line that is cut and its merge together."""
+    c = Case(seqs, H, Hkv, seed=H, wide=wide)
+    c.check(*c.run())
+    c.attend.sync()
+
+
+@pytest.mark.parametrize("H,Hkv,lens", [(32, 8, [16] * 1024), (8, 2, [16] * 300), (8, 2, [64] * 256), (28, 4, [70] * 100),
+                                        (16, 1, list(range(1, 140)))])
+def test_many_short_prompts(H, Hkv, lens):
+    c = Case([(n, n) for n in lens], H, Hkv, seed=len(lens))
+    out, lse = c.run()
+    step = max(1, len(lens) // 40)
+    c.check(out, lse, only=sorted(set(range(0, len(lens), step)) | {len(lens) - 1}))
+    n = int(c.qs[-1])
+    assert torch.isfinite(out[:n]).all() and torch.isfinite(lse[:n]).all()
+    c.attend.sync()
