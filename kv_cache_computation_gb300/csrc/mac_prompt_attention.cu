@@ -975,44 +975,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             if (kRuns && carried) take_run(tO, carry, ex2_approx(carry_ref - ref));
             const bool dirty = some && *(volatile int *)&queue.dirty[follow.place()];
             const int *bad = queue.bad[follow.place()];
-            // (rolled up: once per piece, its instructions come from far away)
+            // (rolled up: once per piece, its instructions come from far away; with a body of 32 columns for bf16 24 ragged
+            // prompts 412 us instead of 407, 1024 of 16 tokens 291 instead of 278)
 #pragma unroll 1
-            for (int c = 0; c < (fp32 ? 8 : 4); c++) {
+            for (int c = 0; c < 8; c++) {
+                float o[16];
+                tmem_ld16(tO + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i++) o[i] = finite_or_nan(o[i] * scale);
+                if (!every || dirty) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        if (scale == 0.f) o[i] = 0.f;
+                        if (dirty && bad[16 * c + i] < lim) o[i] = CUDART_NAN_F;
+                    }
+                }
+                if (!valid) continue;
                 uint32_t w[16];
                 if (fp32) {
-                    float o[16];
-                    tmem_ld16(tO + 16 * c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i++) o[i] = finite_or_nan(o[i] * scale);
-                    if (!every || dirty) {
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            if (scale == 0.f) o[i] = 0.f;
-                            if (dirty && bad[16 * c + i] < lim) o[i] = CUDART_NAN_F;
-                        }
-                    }
 #pragma unroll
                     for (int i = 0; i < 16; i++) w[i] = __float_as_uint(o[i]);
-                } else {
-                    float o[32];
-                    tmem_ld32(tO + 32 * c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; i++) o[i] = finite_or_nan(o[i] * scale);
-                    if (!every || dirty) {
-#pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            if (scale == 0.f) o[i] = 0.f;
-                            if (dirty && bad[32 * c + i] < lim) o[i] = CUDART_NAN_F;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) w[i] = bf16_pair(o[2 * i], o[2 * i + 1]);
-                }
-                if (valid) {
                     store32(to + 64 * c, w);
                     store32(to + 64 * c + 32, w + 8);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) w[i] = bf16_pair(o[2 * i], o[2 * i + 1]);
+                    store32(to + 32 * c, w);
                 }
             }
             fence_before();
