@@ -369,6 +369,10 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                             x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]) + (float)ev[pp]);
                         moves |= x[nt][h] - low[nt][h] > kMargin + kPShift;
                     }
+                int least = ev[0];
+#pragma unroll
+                for (int pp = 1; pp < PP; pp++) least = min(least, ev[pp]);
+                moves |= least < kSmallExp;     // what they need stands behind the same branch (24 rows: 206 us beside it, 201 in it)
                 if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
@@ -389,19 +393,19 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                                 o[nt][j][2 + h] *= f;
                             }
                         }
-                }
-                // A weight below 2^-126 becomes 0 further down; with a small value scale its part of the sum is still to count
+                    // a weight below 2^-126 becomes 0 further down; with a small value scale its part of the sum still counts
+                    if (least < kSmallExp) {
 #pragma unroll
-                for (int pp = 0; pp < PP; pp++)
-                    if (ev[pp] < kSmallExp) {
+                        for (int pp = 0; pp < PP; pp++)
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
+                            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const float w = s[pp][nt][k] - (low[nt][k & 1] - (float)ev[pp]);
-                                if (w < -126.f) sum[nt][k & 1] += ex2_approx(w - (float)ev[pp]);
-                            }
+                                for (int k = 0; k < 4; k++) {
+                                    const float w = s[pp][nt][k] - (low[nt][k & 1] - (float)ev[pp]);
+                                    if (w < -126.f) sum[nt][k & 1] += ex2_approx(w - (float)ev[pp]);
+                                }
                     }
+                }
                 uint32_t pb[PP][NT][2];     // P^T fragments: tokens 4 c .. 4 c + 3, row g
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
