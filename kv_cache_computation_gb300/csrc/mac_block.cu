@@ -14,8 +14,10 @@
 // call; beyond, a first kernel notes them in the pages' marks.  Either way the
 // block that has the page's lowest slot stores the whole page, head by head, a
 // warp to keys or values: lane l has elements 4 l .. 4 l + 3 of all 16 tokens, so
-// a token is one coalesced 256-byte load, the page's largest element one warp
-// maximum, and nothing is read twice.
+// a token is one coalesced 256-byte load and the page's largest element one warp
+// maximum.  Nothing is read twice, but for the tokens of pages that get few of them
+// or some that are not finite: those are loaded for the maximum and again for the
+// codes.
 #include "../../include/mac.h"
 #include "mac_block.cuh"
 #include "mac_device.cuh"

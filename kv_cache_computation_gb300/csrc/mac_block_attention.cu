@@ -26,11 +26,11 @@
 // unrounded in fp32; everything else stays in fp32.
 //
 // Measured (graph replays, 258 bytes per token and KV head): 8 x 131072, 32 / 8
-// heads 321 us (6.7 TB/s, the copy rate); 1 x 4096 14.5 us; 4 ragged requests to
+// heads 321 us (6.7 TB/s, the copy rate); 1 x 4096 12.7 us; 4 ragged requests to
 // 122880, 21 rows for each of 4 heads 62 us (3.8 TB/s); 32 ragged ones to 65536,
-// 32 rows on one head 79.5 us (2.7 TB/s).  8 x 65536 with 8 heads at 4, 8, 12, 16,
-// 24, 32 rows: 168, 174, 173, 179, 202, 254 us.
-// What bounds it.  Up to 16 rows the stream, around which a call pays about 13 us:
+// 32 rows on one head 80 us (2.7 TB/s).  8 x 65536 with 8 heads at 4, 8, 12, 16,
+// 24, 32 rows: 169, 173, 174, 178, 201, 252 us.
+// What bounds it.  Up to 16 rows the stream, around which a call pays about 11 us:
 // launch, lengths and line, the first page, the merges and the second kernel.  With
 // more rows the registers leave two warps to a scheduler, whose dependent
 // instructions' latencies nothing covers (issue slots 36 % used, tensor pipe 40 %
@@ -550,7 +550,7 @@ Variant variant_for(int rows)
 {
     // N tiles as the rows need: a tile more costs (8 x 65536, 8 heads) 4 rows 178 -> 185 us, 16 rows 194 -> 202, 24 rows
     // 202 -> 249.  8 warps, two to a scheduler, where 12 would fit as well: 4 rows 178 -> 169, 16 rows 194 -> 179, 1 x
-    // 4096 16.5 -> 14.5; 6 warps 184 and 222, 16 of one-page units 182 and 316.  Two pages to a unit: one page 189 and 208
+    // 4096 16.5 -> 14.5 (figures of the time); 6 warps 184 and 222, 16 of one-page units 182 and 316.  Two pages to a unit: one page 189 and 208
     // (32 rows: 254 -> 296), four 184 and 198; a third stage 184 and 179.  Q in registers where they suffice.
     if (rows <= 8) return variant<1, 2, 8, 2, 1, true>();
     if (rows <= 16) return variant<2, 2, 8, 2, 1, true>();

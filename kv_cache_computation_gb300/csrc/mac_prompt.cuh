@@ -7,15 +7,15 @@ namespace macgpu {
 
 constexpr int kPMaxBatch = 1024;        // sequences per call (their item counts stand in shared memory)
 constexpr int kPMaxGroup = 128;         // query heads per KV head: a tile has at least one token
-constexpr int kPLevels = 2048;          // levels by which items are ordered: of a block each up to 262144 keys
+constexpr int kPLevels = 2048;          // levels by which items are ordered: of a block each up to 262016 keys
 constexpr int kPMaxCtas = 256;          // upper bound of the grid (one CTA per SM)
 constexpr int kPRows = 256;             // query rows of an item: two tiles of 128
 // Items per CTA, at least, in the line of blocks that is cut.  us with one and two: chunks of 2048 and 509 tokens 674, 707;
 // 24 ragged prompts 415, 418; 5 with 28 / 4 heads 222, 227.
 constexpr int kPLineRows = 1;
 // Blocks that an item counts besides its own in the split of the work: a piece costs 7000 to 10000 cycles whatever its
-// length, a block 2400 to 2700.  us without and with them, when they came: 6001 tokens of 28 / 4 heads 235, 209, of 32 / 8
-// heads 311, 255; ten prompts of 958 tokens 121, 105.  With 2, 4 and 6: 194, 192 and 194 us, 245, 246, 246, and 91, 90, 93.
+// length, a block 2400 to 2700.  us with 0, 2, 4 and 6: 6001 tokens of 32 / 8 heads 252, 216, 212, 216, of 28 / 4 heads
+// 220, 194, 193, 193; ten prompts of 958 tokens 90, 88.5, 88, 91; 1024 prompts of 16 tokens 293, 287, 288, 288.
 constexpr int kPExtra = 4;
 
 // bits of the device error word

@@ -52,12 +52,14 @@
 // a tile's Q, S, P and O are filled again only after their reader has passed on.
 //
 // Measured (graph replays; 32 / 8 heads but where noted; 1965 TFLOP/s is the
-// library's largest product's rate): 32768 tokens 4.95 ms, 5.42 one after another
-// (1775 and 1620 TFLOP/s of the products that the causal edge leaves), 6001 tokens
-// 250 us (1370), 2048 and 509 tokens behind 30720 and 8191 685 us (1660), 24 ragged
-// prompts of 1 .. 4096 tokens 414 us (1315), 5 of 1 .. 6001 with 28 / 4 heads 222 us
-// (1350), 512 fp32 rows behind 32256 290 to 310 us (910; with the second P V 1365),
-// 16 tokens 10.7 to 12.4 us.
+// library's largest product's rate): 32768 tokens 4.95 ms with rests between calls,
+// 5.3 to 5.5 on end (1775 and 1600 to 1650 TFLOP/s of the products that the causal
+// edge leaves), 6001 tokens 212 us (1390), 2048 and 509 tokens behind 30720 and 8191
+// 675 us (1680), 24 ragged prompts of 1 .. 4096 tokens 409 us (1330), 5 of 1 .. 6001
+// with 28 / 4 heads 219 us (1365), 512 fp32 rows behind 32256 288 to 324 us (840 to
+// 945; with the second P V 1260 to 1415), 16 tokens 8.6 us on end, 12.4 a replay by
+// itself; 100 prompts of 1000 tokens 860 us (955), 256 of 64 tokens 94, 1024 of 16
+// 276 (their bytes take 50).
 // What bounds it.  A steady block takes 2450 to 2600 cycles of the pipe's 2048:
 // from scores to weights a tile takes 1240 (880 of them the softmax itself: 512 of
 // ex2 at 32 a cycle and SM, loads and stores of tensor memory, maximum and packing;
@@ -65,8 +67,10 @@
 // tile fills 2048 of that.  In long calls the card then holds its power limit at
 // 1.7 to 1.85 GHz, and fewer cycles give little.  A piece costs 7000 to 10000 cycles
 // besides its blocks (first scores, first softmax, the output, code that was not
-// near), which with the edge blocks' hidden halves is what ragged prompts lose; the
-// prologue (lengths, split, first loads) 8000 to 16000 a call.
+// near), which with the edge blocks' hidden halves is what ragged prompts lose; a
+// prompt of at most 128 / G tokens is a piece per KV head with an empty tile B, and
+// many of those run one after another.  The prologue (lengths, split, first loads)
+// takes 8000 to 16000 a call.
 // Tried and slower (32768 tokens, ms, against the form of the time): softmax
 // warps of half a row each 5.79 / 5.45; a second warp to issue 7.05 / 6.0; P V
 // issued for the first keys before the last weights are there 5.70 / 5.33; waits
@@ -76,7 +80,10 @@
 // half rate); outputs through shared memory, in whole lines, slower than 32 bytes a
 // thread from the registers.  A third part of the weights for fp32 outputs, in the
 // first one's place after its products: error 7e-7 instead of 2e-6 at 2048 keys, 512
-// rows behind 32256 476 us instead of 298.
+// rows behind 32256 476 us instead of 298.  Only where a sequence has few keys: error
+// 4e-7 to 1.2e-6 instead of 1.6e-6 to 2.2e-6 up to 2048 keys (fp32 products 2e-7 to
+// 8e-7), 64 keys 7.6 -> 8.3 us, 256 18.6 -> 23, 2048 41 -> 61, and the choice alone
+// took the rows behind 32256 keys from 287 to 353 us.
 #include "mac_device.cuh"
 #include "mac_prompt.cuh"
 
