@@ -13,7 +13,8 @@
 // into the exponent, the reference is that of the products, and the codes need
 // no scaling at all.  A w below fp32's range adds nothing to out, but w 2^-ev may
 // still count in l: there it is taken as one power, 2^(s_t - low), and so are the
-// factors that bring sums to a later reference (sum_at).
+// factors that bring sums to a later reference (sum_at).  Scores of 2^23 and more,
+// which exponents cannot be added to, are held less a whole number per row.
 //
 // Rows, products, fragments' free orders, the split into equal ranges of a line
 // of units and the merge of pieces are those of the 4-bit store's attention
@@ -26,11 +27,11 @@
 // unrounded in fp32; everything else stays in fp32.
 //
 // Measured (graph replays, 258 bytes per token and KV head): 8 x 131072, 32 / 8
-// heads 321 us (6.7 TB/s, the copy rate); 1 x 4096 12.7 us; 4 ragged requests to
-// 122880, 21 rows for each of 4 heads 62 us (3.8 TB/s); 32 ragged ones to 65536,
-// 32 rows on one head 80 us (2.7 TB/s).  8 x 65536 with 8 heads at 4, 8, 12, 16,
-// 24, 32 rows: 169, 173, 174, 178, 201, 252 us.
-// What bounds it.  Up to 16 rows the stream, around which a call pays about 11 us:
+// heads 321 us (6.7 TB/s, the copy rate); 1 x 4096 14 us; 4 ragged requests to
+// 122880, 21 rows for each of 4 heads 64 us (3.7 TB/s); 32 ragged ones to 65536,
+// 32 rows on one head 81 us (2.7 TB/s).  8 x 65536 with 8 heads at 4, 8, 12, 16,
+// 24, 32 rows: 169, 174, 175, 178, 202, 258 us.
+// What bounds it.  Up to 16 rows the stream, around which a call pays about 12 us:
 // launch, lengths and line, the first page, the merges and the second kernel.  With
 // more rows the registers leave two warps to a scheduler, whose dependent
 // instructions' latencies nothing covers (issue slots 36 % used, tensor pipe 40 %
@@ -53,7 +54,7 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t &lo, uint32_t &hi)
 // Value scales below this one can make a token whose weight w is under fp32's range (2^-126 of the row's reference) count in
 // l, by w 2^-ev: l is at least 2^9 2^-60, and as many tokens as a length can hold, each 2^-126 2^-ev, stay below 2^-24 of
 // that for ev >= -21.
-constexpr int kSmallExp = -21;
+constexpr int kSmallExp = -21, kAlways = 1000;
 
 __host__ __device__ constexpr int block_team_bytes(int nt, int pp, int stages, bool qreg)
 {
@@ -67,6 +68,8 @@ struct BlockSmem : MergeState {
     // several queries: the first token with a NaN that only some of them see, per warp and element
     int bad[TEAMS][kD];
     float row_sc[TEAMS][kQMaxRows];     // log2 units of a row's raw scores, per warp
+    // what is taken off a row's scores where they are too coarse, in all and by the last step, per warp
+    float row_base[TEAMS][kQMaxRows], row_off[TEAMS][kQMaxRows];
 };
 
 // A quad of tokens' value codes (4 elements x 4 tokens) of which the request has
@@ -96,7 +99,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
     // are the same with all.
     constexpr int EXTRA = NT + 2;
     constexpr int TEAM_BYTES = block_team_bytes(NT, PP, STAGES, QREG);
-    static_assert(2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
+    static_assert(kQMaxRows == 32 && 2 * TEAMS <= kMaxPieces && TEAMS * STAGES <= 64, "block shape");
     extern __shared__ __align__(128) unsigned char dyn[];
     __shared__ BlockSmem<TEAMS> sm;
     const int tid = threadIdx.x, lane = tid & 31, team = tid >> 5;
@@ -256,7 +259,8 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                     }
                 }
             }
-            const uint32_t sc0 = smem_u32(&sm.row_sc[team][2 * c4]);
+            const uint32_t sc0 = smem_u32(&sm.row_sc[team][2 * c4]), base0 = smem_u32(&sm.row_base[team][2 * c4]);
+            int small = kSmallExp;      // kAlways where some row's base is not 0
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
@@ -271,6 +275,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
             }
 
             __syncwarp();
+            sm.row_base[team][lane] = 0.f;
             if (a.n_query > 1) {
 #pragma unroll
                 for (int i = 0; i < kD / 32; i++) sm.bad[team][lane + 32 * i] = 0x7fffffff;
@@ -357,33 +362,81 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                                     if (tok0 + pp * kPage + tk + 2 * k >= lim) s[pp][nt][2 * k + h] = -CUDART_INF_F;
                         }
                 }
-                float x[NT][2];
-                bool moves = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        x[nt][h] = -CUDART_INF_F;
-#pragma unroll
-                        for (int pp = 0; pp < PP; pp++)
-                            x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]) + (float)ev[pp]);
-                        moves |= x[nt][h] - low[nt][h] > kMargin + kPShift;
-                    }
-                int least = ev[0];
-#pragma unroll
-                for (int pp = 1; pp < PP; pp++) least = min(least, ev[pp]);
-                moves |= least < kSmallExp;     // what they need stands behind the same branch (24 rows: 206 us beside it, 201 in it)
-                if (__any_sync(0xffffffffu, moves)) {
+                auto top_products = [&](float (&x)[NT][2]) {
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
-                            float y = x[nt][h];
+                            x[nt][h] = -CUDART_INF_F;
 #pragma unroll
-                            for (int off = 4; off < 32; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                            // a row moves by its own scores alone; those of 2^23 and more are whole numbers too coarse to
-                            // take the shift from
-                            y = y - low[nt][h] > kMargin + kPShift ? (fabsf(y) < 0x1p23f ? y - kPShift : y) : low[nt][h];
+                            for (int pp = 0; pp < PP; pp++)
+                                x[nt][h] = fmaxf(x[nt][h], fmaxf(s[pp][nt][h], s[pp][nt][2 + h]) + (float)ev[pp]);
+                        }
+                };
+                float x[NT][2];
+                top_products(x);
+                bool moves = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) moves |= x[nt][h] - low[nt][h] > kMargin + kPShift;
+                int least = ev[0];
+#pragma unroll
+                for (int pp = 1; pp < PP; pp++) least = min(least, ev[pp]);
+                // What small scales and coarse scores need stands behind the branch of references that move (8 x 65536, us at 24
+                // and 32 rows: 208 and 262 beside it, 202 and 258 in it).
+                moves |= least < small;
+                if (__any_sync(0xffffffffu, moves)) {
+                    // Scores of 2^23 and more are too coarse to add exponents to and to take the shift from: such a row's are from
+                    // here on those above its largest product now, and the second pass takes that off this unit's.
+                    uint32_t off = base0;
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; pass++) {
+                        if (small == kAlways) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++) {
+                                float base[2];
+                                lds8(off + nt * 32, base);
+#pragma unroll
+                                for (int pp = 0; pp < PP; pp++)
+#pragma unroll
+                                    for (int k = 0; k < 4; k++) s[pp][nt][k] -= base[k & 1];
+                            }
+                            top_products(x);
+                        }
+                        bool far = false;
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    x[nt][h] = fmaxf(x[nt][h], __shfl_xor_sync(0xffffffffu, x[nt][h], o));
+                                far |= x[nt][h] - low[nt][h] > kMargin + kPShift && fabsf(x[nt][h]) >= 0x1p23f;
+                            }
+                        if (!__any_sync(0xffffffffu, far)) break;
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const bool it = x[nt][h] - low[nt][h] > kMargin + kPShift && fabsf(x[nt][h]) >= 0x1p23f;
+                                const float base = it ? x[nt][h] : 0.f;
+                                low[nt][h] -= base;
+                                if (g8 == 0) {
+                                    sm.row_off[team][nt * 8 + 2 * c4 + h] = base;
+                                    sm.row_base[team][nt * 8 + 2 * c4 + h] += base;
+                                }
+                            }
+                        small = kAlways;
+                        off = smem_u32(&sm.row_off[team][2 * c4]);
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            // a row moves by its own scores alone
+                            const float y = x[nt][h] - low[nt][h] > kMargin + kPShift ? x[nt][h] - kPShift : low[nt][h];
                             const float d = low[nt][h] - y, f = ex2_approx(d);
                             low[nt][h] = y;
                             sum[nt][h] = sum_at<true>(sum[nt][h], f, d);
@@ -482,6 +535,7 @@ __global__ void __launch_bounds__(TEAMS * 32, MINB) block_attention_kernel(const
                 for (int h = 0; h < 2; h++) {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) sum[nt][h] += __shfl_xor_sync(0xffffffffu, sum[nt][h], off);
+                    if (small == kAlways) low[nt][h] += sm.row_base[team][nt * 8 + 2 * c4 + h];
                 }
             const bool ends = u0 + n + EXTRA == n_units, whole = u0 == 0 && ends;
             const int which = ends ? 0 : 1;     // 1: the group runs on into the next warp's range
